@@ -12,6 +12,9 @@ import ctypes as C
 
 STEP_DEFAULT, STEP_SEPARATE, STEP_BATCHED, STEP_DETERMINISTIC = 0, 1, 2, 4
 
+from ._lib import (ACT_GELU_TANH, ACT_SILU, NORM_LAYER, NORM_RMS, TYPE_BF16,  # noqa: F401
+                   TYPE_E4M3, TYPE_F16, TYPE_F32, AttentionArgs, DecoderLayer, GluArgs,
+                   KvAppendArgs, KvCache, ResidualNormArgs)
 from ._lib import (FMT_FP16, FMT_INT4, MAX_DIN, MAX_MATS, MODE_THRESHOLD, MODE_TOPK,  # noqa: F401
                    MODE_TOPK_GUIDED, TIER_APPROX, TIER_FULL, TIER_SKIP, BLOCK_ERROR_FN,
                    SPAX_ERR_WORKSPACE, Layout, MoveStats, Phase, SpaxError, Step, StorageStats,
@@ -28,6 +31,11 @@ __all__ = [
     "spax_greedy_allocation", "spax_allocation_at",
     "topk_params", "threshold_params", "guided_params", "make_phase", "Layout", "TierParams",
     "Phase", "Step", "SpaxError", "LIB_PATH",
+    "spax_kv_append", "spax_attention_workspace_bytes", "spax_paged_attention",
+    "spax_residual_norm", "spax_glu", "spax_layers_workspace_bytes", "spax_decode_layers",
+    "make_kv_cache", "make_kv_append", "make_attention", "make_residual_norm", "make_glu",
+    "make_layer", "layer_array", "KvCache", "KvAppendArgs", "AttentionArgs", "ResidualNormArgs",
+    "GluArgs", "DecoderLayer",
 ]
 
 
@@ -263,6 +271,291 @@ def spax_decode_step_projections_noalloc(phases, flags: int = 0, stream=None,
     st = _step(phases, None, 0, flags, events)
     check(lib.spax_decode_step_projections_noalloc(C.byref(st), _stream(stream)),
           "spax_decode_step_projections_noalloc")
+
+
+# ------------------------------------------------------------------ between the projections
+#
+# A make_* function describes one call in terms of tensors (shapes, strides, types and the device
+# are checked here, the rest by the library); the struct it returns keeps its tensors alive and
+# is handed to the call as often as their contents change.  The call runs on the tensors' own
+# device, on that device's current stream unless one is given.
+
+def _type_of(t) -> int:
+    name = str(t.dtype)
+    types = {"torch.float32": TYPE_F32, "torch.float16": TYPE_F16, "torch.bfloat16": TYPE_BF16,
+             "torch.float8_e4m3fn": TYPE_E4M3}
+    if name not in types:
+        raise TypeError(f"no operator takes {name}")
+    return types[name]
+
+
+def _rows(t, name, dims):
+    """Checks a tensor of `dims` axes whose last axis is contiguous."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} axes, not {dims}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis is not contiguous")
+    return t
+
+
+def _flat(t, name, n, dtype):
+    if t is None:
+        return None
+    if str(t.dtype) != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} is not a contiguous tensor of {n} values")
+    return t
+
+
+def _same_shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+
+
+def _keep(struct, *tensors, parts=()):
+    """Ties the tensors (and the structs in parts) to the struct; all are on one device."""
+    devices = {t.device for t in tensors if t is not None}
+    devices |= {p._device for p in parts}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+    struct._keep = (tensors, parts)
+    struct._device = next(iter(devices)) if devices else None
+    return struct
+
+
+def _call(fn, where, device, stream, *args):
+    """Runs fn(*args, stream) with the tensors' device current."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: the tensors are on {device}, not on a GPU")
+    import torch
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(stream))
+    if status:
+        check(status, where)
+
+
+def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None) -> KvCache:
+    """A paged cache: k and v [n_pages, n_kv_heads, page_size, head_dim] (a view of any order,
+    e.g. of [n_pages, page_size, n_kv_heads, head_dim] with its middle axes swapped), page_table
+    int32 [n_seqs, max_pages]; scales fp32 [n_kv_heads] for float8_e4m3fn."""
+    _rows(k, "k", 4)
+    _rows(v, "v", 4)
+    _same_shape(v, "v", k.shape)
+    if v.dtype != k.dtype:
+        raise TypeError(f"v is {v.dtype}, k is {k.dtype}")
+    _rows(page_table, "page_table", 2)
+    if str(page_table.dtype) != "torch.int32":
+        raise TypeError(f"page_table is {page_table.dtype}, not torch.int32")
+    c = KvCache()
+    c.type = _type_of(k)
+    c.n_pages, c.n_kv_heads, c.page_size, c.head_dim = (int(n) for n in k.shape)
+    c.k, c.v, c.page_table = k.data_ptr(), v.data_ptr(), page_table.data_ptr()
+    c.k_scale = _ptr(_flat(k_scale, "k_scale", k.shape[1], "torch.float32"))
+    c.v_scale = _ptr(_flat(v_scale, "v_scale", k.shape[1], "torch.float32"))
+    c.k_page_stride, c.k_head_stride, c.k_row_stride = k.stride()[:3]
+    c.v_page_stride, c.v_head_stride, c.v_row_stride = v.stride()[:3]
+    c.n_seqs, c.max_pages = (int(n) for n in page_table.shape)
+    c.table_stride = page_table.stride(0)
+    return _keep(c, k, v, page_table, k_scale, v_scale)
+
+
+def make_kv_append(cache: KvCache, q, k, v, positions, q_out, seq=None, inv_freq=None,
+                   interleaved: bool = False) -> KvAppendArgs:
+    """q [n_tokens, n_heads, head_dim], k and v [n_tokens, n_kv_heads, head_dim] of one type (views
+    of a fused row, for instance), q_out like q in the cache's type (float16 or bfloat16 for
+    an e4m3 cache); q and q_out may both be None.  positions int32 [n_tokens], seq likewise
+    (None: token t belongs to sequence t), inv_freq fp32 [rot_dim / 2] (None: no rotation)."""
+    _rows(k, "k", 3)
+    _rows(v, "v", 3)
+    n = int(k.shape[0])
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    _same_shape(k, "k", shape)
+    _same_shape(v, "v", shape)
+    a = KvAppendArgs()
+    a.cache = C.pointer(cache)
+    a.src_type = _type_of(k)
+    a.n_tokens = n
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        _rows(q, "q", 3)
+        _same_shape(q, "q", (n, q.shape[1], cache.head_dim))
+        _rows(q_out, "q_out", 3)
+        _same_shape(q_out, "q_out", q.shape)
+        a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), int(q.shape[1])
+        a.q_token_stride, a.q_head_stride = q.stride()[:2]
+        a.out_token_stride, a.out_head_stride = q_out.stride()[:2]
+        a.out_type = _type_of(q_out)
+    else:
+        a.out_type = TYPE_F16 if cache.type == TYPE_E4M3 else cache.type
+    for t, name in ((q, "q"), (v, "v")):
+        if t is not None and t.dtype != k.dtype:
+            raise TypeError(f"{name} is {t.dtype}, k is {k.dtype}")
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    a.k_token_stride, a.k_head_stride = k.stride()[:2]
+    a.v_token_stride, a.v_head_stride = v.stride()[:2]
+    a.positions = _ptr(_flat(positions, "positions", n, "torch.int32"))
+    a.seq = _ptr(_flat(seq, "seq", n, "torch.int32"))
+    if inv_freq is not None:
+        a.inv_freq = _ptr(_flat(inv_freq, "inv_freq", inv_freq.numel(), "torch.float32"))
+        a.rot_dim = 2 * inv_freq.numel()
+    a.interleaved = int(bool(interleaved))
+    return _keep(a, q, k, v, positions, q_out, seq, inv_freq, parts=(cache,))
+
+
+def spax_kv_append(args: KvAppendArgs, stream=None) -> None:
+    _call(lib.spax_kv_append, "spax_kv_append", args._device, stream, args)
+
+
+def make_attention(cache: KvCache, q, lens, out, max_len: int | None = None,
+                   scale: float | None = None, window: int = 0, lse=None) -> AttentionArgs:
+    """q and out [n_seqs, n_heads, head_dim], lens int32 [n_seqs] (keys of each sequence, the new
+    token's own among them), lse fp32 [n_seqs, n_heads] or None.  max_len: bound on lens
+    (default: what the page table holds); scale: default 1 / sqrt(head_dim)."""
+    _rows(q, "q", 3)
+    _rows(out, "out", 3)
+    _same_shape(q, "q", (cache.n_seqs, q.shape[1], cache.head_dim))
+    _same_shape(out, "out", q.shape)
+    if q.dtype != out.dtype:
+        raise TypeError(f"out is {out.dtype}, q is {q.dtype}")
+    a = AttentionArgs()
+    a.cache = C.pointer(cache)
+    a.q, a.out, a.type, a.n_heads = q.data_ptr(), out.data_ptr(), _type_of(q), int(q.shape[1])
+    a.q_seq_stride, a.q_head_stride = q.stride()[:2]
+    a.out_seq_stride, a.out_head_stride = out.stride()[:2]
+    a.lens = _ptr(_flat(lens, "lens", cache.n_seqs, "torch.int32"))
+    a.lse = _ptr(_flat(lse, "lse", cache.n_seqs * a.n_heads, "torch.float32"))
+    a.max_len = int(cache.max_pages * cache.page_size if max_len is None else max_len)
+    a.scale = float(cache.head_dim ** -0.5 if scale is None else scale)
+    a.window = int(window)
+    return _keep(a, q, lens, out, lse, parts=(cache,))
+
+
+def spax_attention_workspace_bytes(args: AttentionArgs) -> int:
+    return int(lib.spax_attention_workspace_bytes(C.byref(args)))
+
+
+def spax_paged_attention(args: AttentionArgs, ws=None, ws_bytes: int | None = None,
+                         stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    _call(lib.spax_paged_attention, "spax_paged_attention", args._device, stream, args, _ptr(ws),
+          ws_bytes)
+
+
+_NORMS = {"rms": NORM_RMS, "layer": NORM_LAYER}
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU_TANH}
+
+
+def make_residual_norm(residual, block, residual_out, x, kind: str = "rms", pre_weight=None,
+                       pre_bias=None, post_weight=None, post_bias=None, gate=None,
+                       scale: float = 1.0, eps: float = 1e-5) -> ResidualNormArgs:
+    """residual, block, residual_out, x [n_rows, d] (any may be None, see the library), gate [d],
+    [1, d] or [n_rows, d]; weights and biases fp32 [d].  kind: 'rms' or 'layer'."""
+    a = ResidualNormArgs()
+    a.kind = _NORMS.get(kind, kind)
+    shape = None
+    for t, name in ((residual, "residual"), (block, "block"), (residual_out, "residual_out"),
+                    (x, "x")):
+        if t is None:
+            continue
+        _rows(t, name, 2)
+        if shape is None:
+            shape = tuple(t.shape)
+        _same_shape(t, name, shape)
+        setattr(a, name, t.data_ptr())
+        setattr(a, name + "_stride", t.stride(0))
+    if shape is None:
+        raise ValueError("no rows given")
+    a.n_rows, a.d = (int(n) for n in shape)
+    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
+        raise TypeError(f"residual_out is {residual_out.dtype}, residual is {residual.dtype}")
+    stream_type = residual if residual is not None else residual_out
+    a.residual_type = TYPE_F32 if stream_type is None else _type_of(stream_type)
+    a.block_type = TYPE_F32 if block is None else _type_of(block)
+    a.x_type = TYPE_F32 if x is None else _type_of(x)
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.view(1, -1) if gate.is_contiguous() else gate[None]
+        _rows(gate, "gate", 2)
+        if tuple(gate.shape) not in ((1, shape[1]), shape):
+            raise ValueError(f"gate has shape {tuple(gate.shape)}")
+        a.gate, a.gate_type = gate.data_ptr(), _type_of(gate)
+        a.gate_stride = 0 if gate.shape[0] == 1 else gate.stride(0)
+    for t, name in ((pre_weight, "pre_weight"), (pre_bias, "pre_bias"),
+                    (post_weight, "post_weight"), (post_bias, "post_bias")):
+        setattr(a, name, _ptr(_flat(t, name, shape[1], "torch.float32")))
+    a.scale, a.eps = float(scale), float(eps)
+    return _keep(a, residual, block, residual_out, x, gate, pre_weight, pre_bias, post_weight,
+                 post_bias)
+
+
+def spax_residual_norm(args: ResidualNormArgs, stream=None) -> None:
+    _call(lib.spax_residual_norm, "spax_residual_norm", args._device, stream, args)
+
+
+def make_glu(gate, up, x, act: str = "silu") -> GluArgs:
+    """gate, up and x [n_rows, d] (gate and up of one type).  act: 'silu' or 'gelu' (tanh form)."""
+    a = GluArgs()
+    for t, name in ((gate, "gate"), (up, "up"), (x, "x")):
+        _rows(t, name, 2)
+        _same_shape(t, name, gate.shape)
+        setattr(a, name, t.data_ptr())
+        setattr(a, name + "_stride", t.stride(0))
+    if gate.dtype != up.dtype:
+        raise TypeError(f"up is {up.dtype}, gate is {gate.dtype}")
+    a.src_type, a.x_type, a.act = _type_of(gate), _type_of(x), _ACTS.get(act, act)
+    a.n_rows, a.d = (int(n) for n in gate.shape)
+    return _keep(a, gate, up, x)
+
+
+def spax_glu(args: GluArgs, stream=None) -> None:
+    _call(lib.spax_glu, "spax_glu", args._device, stream, args)
+
+
+def make_layer(qkv: Phase, append: KvAppendArgs, attention: AttentionArgs, o: Phase,
+               attn_norm: ResidualNormArgs, gate_up: Phase, glu: GluArgs, down: Phase,
+               mlp_norm: ResidualNormArgs) -> DecoderLayer:
+    """One decoder layer of spax_decode_layers, in the order in which its parts run."""
+    parts = dict(qkv=qkv, append=append, attention=attention, o=o, attn_norm=attn_norm,
+                 gate_up=gate_up, glu=glu, down=down, mlp_norm=mlp_norm)
+    L = DecoderLayer()
+    for name, p in parts.items():
+        setattr(L, name, C.pointer(p))
+    L._keep = parts
+    devices = {p._device for p in (append, attention, attn_norm, glu, mlp_norm)}
+    if len(devices) > 1:
+        raise ValueError(f"parts on different devices: {sorted(map(str, devices))}")
+    L._device = next(iter(devices))
+    return L
+
+
+def layer_array(layers):
+    arr = (DecoderLayer * len(layers))(*layers)
+    arr._keep = [L._keep for L in layers]
+    arr._device = layers[0]._device if layers else None
+    return arr
+
+
+def spax_layers_workspace_bytes(layers) -> int:
+    arr = layers if isinstance(layers, C.Array) else layer_array(layers)
+    return int(lib.spax_layers_workspace_bytes(arr, len(arr)))
+
+
+def spax_decode_layers(layers, ws, ws_bytes: int | None = None, flags: int = 0,
+                       stream=None) -> None:
+    """A whole batch-one decode step through decoder layers: their projections with the operators
+    between them.  layers: make_layer structs, or their layer_array."""
+    arr = layers if isinstance(layers, C.Array) else layer_array(layers)
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    _call(lib.spax_decode_layers, "spax_decode_layers", arr._device, stream, arr, len(arr),
+          int(flags), _ptr(ws), int(ws_bytes))
 
 
 # ------------------------------------------------------------------ diagnostics

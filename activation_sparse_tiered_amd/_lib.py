@@ -57,6 +57,64 @@ class Step(C.Structure):
                 ("ws", C.c_void_p), ("ws_bytes", C.c_size_t), ("events", C.POINTER(C.c_void_p))]
 
 
+# ------------------------------------------------------------------ between the projections
+TYPE_F32, TYPE_F16, TYPE_BF16, TYPE_E4M3 = 0, 1, 2, 3
+NORM_RMS, NORM_LAYER = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
+
+
+def _struct(pointers=(), strides=(), ints=(), floats=(), pad=False, first=()):
+    return (list(first) + [(n, C.c_void_p) for n in pointers] + [(n, C.c_int64) for n in strides]
+            + [(n, C.c_int32) for n in ints] + [(n, C.c_float) for n in floats]
+            + ([("reserved0", C.c_int32)] if pad else []))
+
+
+class KvCache(C.Structure):
+    _fields_ = _struct(("k", "v", "page_table", "k_scale", "v_scale"),
+                       ("k_page_stride", "k_head_stride", "k_row_stride", "v_page_stride",
+                        "v_head_stride", "v_row_stride", "table_stride"),
+                       ("type", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_seqs",
+                        "max_pages"), pad=True)
+
+
+class KvAppendArgs(C.Structure):
+    _fields_ = _struct(("q", "k", "v", "q_out", "positions", "seq", "inv_freq"),
+                       ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                        "v_token_stride", "v_head_stride", "out_token_stride",
+                        "out_head_stride"),
+                       ("src_type", "out_type", "n_tokens", "n_heads", "rot_dim", "interleaved"),
+                       first=[("cache", C.POINTER(KvCache))])
+
+
+class AttentionArgs(C.Structure):
+    _fields_ = _struct(("q", "out", "lse", "lens"),
+                       ("q_seq_stride", "q_head_stride", "out_seq_stride", "out_head_stride"),
+                       ("type", "n_heads", "max_len", "window"), ("scale",), pad=True,
+                       first=[("cache", C.POINTER(KvCache))])
+
+
+class ResidualNormArgs(C.Structure):
+    _fields_ = _struct(("residual", "block", "residual_out", "x", "gate", "post_weight",
+                        "post_bias", "pre_weight", "pre_bias"),
+                       ("residual_stride", "block_stride", "residual_out_stride", "x_stride",
+                        "gate_stride"),
+                       ("residual_type", "block_type", "gate_type", "x_type", "kind", "n_rows",
+                        "d"), ("scale", "eps"), pad=True)
+
+
+class GluArgs(C.Structure):
+    _fields_ = _struct(("gate", "up", "x"), ("gate_stride", "up_stride", "x_stride"),
+                       ("src_type", "x_type", "act", "n_rows", "d"), pad=True)
+
+
+class DecoderLayer(C.Structure):
+    _fields_ = [("qkv", C.POINTER(Phase)), ("append", C.POINTER(KvAppendArgs)),
+                ("attention", C.POINTER(AttentionArgs)), ("o", C.POINTER(Phase)),
+                ("attn_norm", C.POINTER(ResidualNormArgs)), ("gate_up", C.POINTER(Phase)),
+                ("glu", C.POINTER(GluArgs)), ("down", C.POINTER(Phase)),
+                ("mlp_norm", C.POINTER(ResidualNormArgs))]
+
+
 class StorageStats(C.Structure):
     _fields_ = [("selected_bytes", C.c_int64), ("moved_bytes", C.c_int64),
                 ("read_bytes", C.c_int64), ("n_blocks", C.c_int64), ("n_ranges", C.c_int32),
@@ -113,6 +171,14 @@ def _load():
         "spax_step_workspace_bytes": (C.c_size_t, [C.POINTER(Phase), C.c_int32]),
         "spax_decode_step_projections": (C.c_int, [C.POINTER(Step), P]),
         "spax_decode_step_projections_noalloc": (C.c_int, [C.POINTER(Step), P]),
+        "spax_kv_append": (C.c_int, [C.POINTER(KvAppendArgs), P]),
+        "spax_attention_workspace_bytes": (C.c_size_t, [C.POINTER(AttentionArgs)]),
+        "spax_paged_attention": (C.c_int, [C.POINTER(AttentionArgs), P, C.c_size_t, P]),
+        "spax_residual_norm": (C.c_int, [C.POINTER(ResidualNormArgs), P]),
+        "spax_glu": (C.c_int, [C.POINTER(GluArgs), P]),
+        "spax_layers_workspace_bytes": (C.c_size_t, [C.POINTER(DecoderLayer), C.c_int32]),
+        "spax_decode_layers": (C.c_int, [C.POINTER(DecoderLayer), C.c_int32, C.c_int32, P,
+                                         C.c_size_t, P]),
         "spax_column_ranges": (C.c_int, [P, C.c_int32, C.c_int32, P, P, C.POINTER(C.c_int32)]),
         "spax_pinned_workspace_bytes": (C.c_size_t, [C.POINTER(Layout)]),
         "spax_storage_ledger": (C.c_int, [C.POINTER(Layout), P, C.c_int32, P, C.c_int32,

@@ -30,7 +30,8 @@ FLAGS = [
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
 SOURCES = ["host.cpp", "api.cpp", "pack.hip", "tiers.hip", "gemv.hip", "decode.hip", "batch.hip",
-           "pinned.cpp", "probe.hip", "budgets.cpp"]
+           "pinned.cpp", "probe.hip", "budgets.cpp", "api_layer.cpp", "layers.cpp",
+           "kv_append.hip", "attention.hip", "norm.hip", "glu.hip"]
 
 
 def hipcc() -> str:

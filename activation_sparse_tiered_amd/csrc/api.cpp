@@ -137,6 +137,10 @@ int check_gemv_args(const spax_layout* L, const void* packed, const uint16_t* x,
   return SPAX_OK;
 }
 
+}  // namespace
+
+namespace spax {
+
 // Every check of spax_decode_step_projections, before anything is enqueued.  noalloc: the
 // workspace is not used (the batched form's tables go to the static scratch, whose size
 // bounds the number of phases).
@@ -195,7 +199,7 @@ int validate_step(const spax_step* step, bool noalloc) {
   return SPAX_OK;
 }
 
-}  // namespace
+}  // namespace spax
 
 extern "C" {
 

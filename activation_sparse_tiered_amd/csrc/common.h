@@ -120,8 +120,20 @@ int launch_decode_step_batched(const spax_step* st, int n_cu, hipStream_t s);
 // no allocation); at most kStaticScratchBytes of tables.
 constexpr size_t kStaticScratchBytes = 256 * 1024;
 int launch_decode_step_batched_static(const spax_step* st, int n_cu, hipStream_t s);
-// Enqueue a validated step; noalloc: the batched form takes its tables from the static scratch.
-int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc);
+// What a layer enqueues between its phases (layers.cpp).
+struct StepHooks {
+  virtual ~StepHooks() = default;
+  // Enqueue what follows phase i.
+  virtual int after(int i, hipStream_t s) = 0;
+  // Whether what follows phase i reads or writes a byte of [p, p + n).
+  virtual bool touches_after(int i, const void* p, size_t n) const = 0;
+};
+// Every check of spax_decode_step_projections (noalloc: with no workspace).
+int validate_step(const spax_step* step, bool noalloc);
+// Enqueue a validated step; noalloc: the batched form takes its tables from the static scratch;
+// hooks (not with the batched form): called after each phase.
+int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc,
+                       StepHooks* hooks = nullptr);
 
 inline size_t aligned_size(size_t b) { return (b + 255) / 256 * 256; }
 

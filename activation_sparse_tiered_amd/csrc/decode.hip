@@ -493,7 +493,7 @@ size_t deterministic_workspace_bytes(const spax_phase* phases, int32_t n_phases)
   return mx;
 }
 
-int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc) {
+int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc, StepHooks* hooks) {
   if (st->flags & SPAX_STEP_BATCHED)
     return noalloc ? launch_decode_step_batched_static(st, cu_count(), s)
                    : launch_decode_step_batched(st, cu_count(), s);
@@ -515,7 +515,8 @@ int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc) {
     if (i + 1 >= n || partials) return false;
     const spax_phase& nx = st->phases[i + 1];
     return fused_phase_ok(st->phases[i].layout) && plan_of(nx.layout).n_chunks > 1 &&
-           !phase_touches(st->phases[i], nx.y, 4 * (size_t)nx.layout->d_out_total);
+           !phase_touches(st->phases[i], nx.y, 4 * (size_t)nx.layout->d_out_total) &&
+           !(hooks && hooks->touches_after(i, nx.y, 4 * (size_t)nx.layout->d_out_total));
   };
   for (int i = 0; i < n; ++i) {
     const spax_phase& ph = st->phases[i];
@@ -543,6 +544,7 @@ int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc) {
                               ph.y, cleared || clear_in_mask, s, false, partials);
       if (rc) return rc;
       if (st->events) SPAX_HIP_CHECK(hipEventRecord(st->events[2 * i + 1], s));
+      if (hooks && (rc = hooks->after(i, s))) return rc;
       continue;
     }
     if (plan.n_chunks > 1 && !cleared && !partials) {
@@ -596,6 +598,10 @@ int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc) {
     if (st->events) SPAX_HIP_CHECK(hipEventRecord(st->events[2 * i + 1], s));
     if (a.partials) {
       int rc = launch_reduce_chunks(partials, plan.n_chunks, L->d_out_total, ph.y, s);
+      if (rc) return rc;
+    }
+    if (hooks) {
+      const int rc = hooks->after(i, s);
       if (rc) return rc;
     }
   }

@@ -443,6 +443,220 @@ int spax_decode_step_projections(const spax_step* step, hipStream_t stream);
  */
 int spax_decode_step_projections_noalloc(const spax_step* step, hipStream_t stream);
 
+/* ---------------------------------------------------------------- between the projections */
+
+/*
+ * Operators of a decoder layer that stand between two projection groups: the paged cache append
+ * with rotation, the attention of one new token per sequence, the residual add with its norms,
+ * and the gated activation.  They take rows of any number of tokens; spax_decode_layers runs
+ * them with the projections for the one token of a batch-one step.
+ *
+ * All of them: pointers inside the structs are device pointers, the structs themselves are host
+ * memory read during the call; strides are in elements, positive, and every row's own values
+ * are contiguous; sums, statistics and angles are kept in 32 bits or more and each result is
+ * rounded once, to nearest even; no atomics, so the same inputs give the same bits; kernel
+ * launches only, so a call can be captured into a graph; pointers and stream belong to the
+ * current device.  No output may share bytes with another output or with an input, except
+ * where stated.  Columns of the same rows (equal row strides) are told apart; any other strided
+ * buffer counts as the whole span from its first to its last element.
+ */
+enum { SPAX_F32 = 0, SPAX_F16 = 1, SPAX_BF16 = 2, SPAX_E4M3 = 3 };
+
+/*
+ * A paged cache of keys and values.  Page p holds page_size rows of every key head: the row of
+ * head h and position r in the page starts at k + p * k_page_stride + h * k_head_stride +
+ * r * k_row_stride (elements), head_dim values; v likewise.  Any order of pages, heads and rows
+ * in memory is a choice of strides.  Position i of sequence s is row i % page_size of page
+ * page_table[s * table_stride + i / page_size].  An entry outside [0, n_pages) names no page:
+ * nothing is read or written there.
+ *   E4M3: a stored value q of head h stands for q * k_scale[h] (v_scale[h]); NULL means 1.
+ * Limits: head_dim 64, 96, 128, 192 or 256; page_size a power of two, 4..65536; k and v 16-byte
+ * aligned and their strides a multiple of 16 bytes (rows may not overlap, nor k's with v's).
+ */
+typedef struct spax_kv_cache {
+  void* k;
+  void* v;
+  const int32_t* page_table;
+  const float* k_scale;        /* E4M3 only: n_kv_heads values, may be NULL */
+  const float* v_scale;
+  int64_t k_page_stride, k_head_stride, k_row_stride;
+  int64_t v_page_stride, v_head_stride, v_row_stride;
+  int64_t table_stride;        /* >= max_pages                              */
+  int32_t type;                /* SPAX_F16, SPAX_BF16 or SPAX_E4M3          */
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int32_t n_seqs, max_pages;   /* rows and used columns of page_table       */
+  int32_t reserved0;
+} spax_kv_cache;
+
+/*
+ * Append: for token t of sequence s = seq[t] (t itself if seq is NULL) at position p =
+ * positions[t], k and v go to row p of s in the cache and q to q_out.  The leading rot_dim
+ * values of every q and k head are rotated pair by pair on the way: with angle a = p *
+ * inv_freq[i] (product and reduction by whole turns in 64 bits),
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a),
+ * pair i being (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved; later values and v are
+ * copied.  E4M3: x / scale, clamped to +-448 (NaN stays NaN).
+ *   q, k, v : src_type; token t, head h starts at t * token_stride + h * head_stride (a fused
+ *             q|k|v row is three pointers into it).  q and q_out may both be NULL (n_heads 0).
+ *   q_out   : out_type (SPAX_F16 or SPAX_BF16).  May be q itself, if type and strides agree.
+ *   cache   : type out_type or SPAX_E4M3.
+ * p < 0 is padding: nothing is cached and the token's q_out is zeros.  A position past max_pages
+ * or on an entry that names no page, or a sequence outside [0, n_seqs), caches nothing (q_out is
+ * written).  Two tokens of one call on one row: the row then holds, value by value, either
+ * token's.  n_tokens 0 does nothing.
+ * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (head_dim, page_size, rot_dim odd or past head_dim, a
+ * size < 1, n_tokens > n_seqs without seq); SPAX_ERR_UNSUPPORTED (types); SPAX_ERR_ALIGN
+ * (a pointer not aligned to its element, the cache as above); SPAX_ERR_PARAM (strides that
+ * overlap, outputs that overlap); SPAX_ERR_HIP.
+ */
+typedef struct spax_kv_append_args {
+  const spax_kv_cache* cache;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const int32_t* positions;
+  const int32_t* seq;          /* may be NULL */
+  const float* inv_freq;       /* rot_dim / 2 values; NULL with rot_dim 0 */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+  int32_t src_type, out_type, n_tokens, n_heads, rot_dim, interleaved;
+} spax_kv_append_args;
+
+int spax_kv_append(const spax_kv_append_args* a, hipStream_t stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache.  Sequence s (row s of the page
+ * table) holds n = lens[s] keys, the new token's own among them; query head h reads key head
+ * h / (n_heads / n_kv_heads).  Over the keys j in [max(0, n - window), n) (window 0: all):
+ *   score_j = scale * k_scale * q . k_j,   out = v_scale * sum_j softmax(score)_j v_j,
+ *   lse = ln sum_j exp(score_j).
+ * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)].  Keys on entries
+ * that name no page are left out; bytes of rows outside the range never reach the result,
+ * whatever they hold.  A sequence with no keys, or whose scores are all -inf, gives zeros and
+ * lse -inf.  q, out : `type` (SPAX_F16 or SPAX_BF16), the cache's type or the cache E4M3; 16-byte
+ * aligned with strides a multiple of 8 elements.  Probabilities enter the product with v as the
+ * sum of two `type` values, so they carry twice its precision.
+ *   max_len : host bound on lens; sets how the keys are shared out, and the workspace.
+ *   ws      : spax_attention_workspace_bytes(a) bytes (0: none needed), 256-byte aligned, any
+ *             contents; calls that may run at the same time need a workspace each.
+ * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (as for the cache; n_heads not a multiple of
+ * n_kv_heads; max_len < 1 or past max_pages * page_size; window < 0); SPAX_ERR_UNSUPPORTED
+ * (types); SPAX_ERR_ALIGN; SPAX_ERR_PARAM (scale not finite, overlapping buffers);
+ * SPAX_ERR_WORKSPACE; SPAX_ERR_HIP.
+ */
+typedef struct spax_attention_args {
+  const spax_kv_cache* cache;
+  const void* q;
+  void* out;
+  float* lse;                  /* n_seqs * n_heads, may be NULL */
+  const int32_t* lens;
+  int64_t q_seq_stride, q_head_stride, out_seq_stride, out_head_stride;
+  int32_t type, n_heads, max_len, window;
+  float scale;
+  int32_t reserved0;
+} spax_attention_args;
+
+size_t spax_attention_workspace_bytes(const spax_attention_args* a);
+int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+
+/* spax_residual_norm_args.kind: x * w / sqrt(mean x^2 + eps), or (x - mean x) * w /
+ * sqrt(mean (x - mean x)^2 + eps); plus the bias if there is one. */
+enum { SPAX_NORM_RMS = 0, SPAX_NORM_LAYER = 1 };
+
+/*
+ * A block's output joins the residual stream, and the next block's input leaves it.  Per row:
+ *   t = block;  t = norm(t; post_weight, post_bias) if post_weight;  t = t * gate if gate;
+ *   h = residual + scale * t;   x = norm(h; pre_weight, pre_bias)   (from h before rounding).
+ * residual_out gets h, x the normed row; either may be NULL, not both.  residual or block may be
+ * NULL (0 is taken), not both; residual_out may be residual itself (type and stride alike), x
+ * may be block itself likewise.  gate: gate_type, one row (gate_stride 0) or one per row.
+ * Weights and biases are fp32 rows of d (weight NULL: ones for pre, no norm for post).
+ *   residual, residual_out : residual_type; block : block_type (SPAX_F32, SPAX_F16, SPAX_BF16);
+ *   x : x_type (the same three).  1 <= d <= 32768; n_rows 0 does nothing.
+ * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE; SPAX_ERR_UNSUPPORTED (types, kind); SPAX_ERR_ALIGN (a
+ * pointer not aligned to its element); SPAX_ERR_PARAM (scale or eps not finite, eps < 0, a
+ * stride below d, a bias without its weight, overlapping buffers); SPAX_ERR_HIP.
+ */
+typedef struct spax_residual_norm_args {
+  const void* residual;
+  const void* block;
+  void* residual_out;
+  void* x;
+  const void* gate;
+  const float* post_weight;
+  const float* post_bias;
+  const float* pre_weight;
+  const float* pre_bias;
+  int64_t residual_stride, block_stride, residual_out_stride, x_stride, gate_stride;
+  int32_t residual_type, block_type, gate_type, x_type, kind, n_rows, d;
+  float scale, eps;
+  int32_t reserved0;
+} spax_residual_norm_args;
+
+int spax_residual_norm(const spax_residual_norm_args* a, hipStream_t stream);
+
+/* spax_glu_args.act: g / (1 + exp(-g)), or the tanh form of gelu,
+ * g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+enum { SPAX_ACT_SILU = 0, SPAX_ACT_GELU_TANH = 1 };
+
+/*
+ * x = act(gate) * up, row by row (gate and up: src_type, usually the two halves of a gate|up
+ * projection's row; x: x_type; types SPAX_F32, SPAX_F16, SPAX_BF16).  Any d >= 1; n_rows 0 does
+ * nothing.  x may be gate or up itself (type and stride alike).
+ * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE; SPAX_ERR_UNSUPPORTED (types, act); SPAX_ERR_ALIGN;
+ * SPAX_ERR_PARAM (a stride below d, overlapping buffers); SPAX_ERR_HIP.
+ */
+typedef struct spax_glu_args {
+  const void* gate;
+  const void* up;
+  void* x;
+  int64_t gate_stride, up_stride, x_stride;
+  int32_t src_type, x_type, act, n_rows, d, reserved0;
+} spax_glu_args;
+
+int spax_glu(const spax_glu_args* a, hipStream_t stream);
+
+/*
+ * One decoder layer of a batch-one step, in order: qkv, append, attention, o, attn_norm,
+ * gate_up, glu, down, mlp_norm.  attn_norm's x is gate_up's input; mlp_norm's x is the next
+ * layer's qkv input (the first layer's is the caller's, e.g. spax_residual_norm without a
+ * block).  All pointers are host structs; layers may share buffers (stream order).
+ */
+typedef struct spax_decoder_layer {
+  const spax_phase* qkv;
+  const spax_kv_append_args* append;
+  const spax_attention_args* attention;
+  const spax_phase* o;
+  const spax_residual_norm_args* attn_norm;
+  const spax_phase* gate_up;
+  const spax_glu_args* glu;
+  const spax_phase* down;
+  const spax_residual_norm_args* mlp_norm;
+} spax_decoder_layer;
+
+/* Workspace of spax_decode_layers in every launch form: the larger of the step's and the
+ * attentions' (they use it one after another).  0 for invalid input. */
+size_t spax_layers_workspace_bytes(const spax_decoder_layer* layers, int32_t n_layers);
+
+/*
+ * A whole batch-one decode step through n_layers decoder layers: the projections of
+ * spax_decode_step_projections with the operators above between them, nothing else enqueued.
+ *   flags : SPAX_STEP_DEFAULT, SPAX_STEP_SEPARATE and SPAX_STEP_DETERMINISTIC as for the step
+ *           (SPAX_STEP_BATCHED needs independent phases: SPAX_ERR_UNSUPPORTED).
+ *   ws    : spax_layers_workspace_bytes bytes, 256-byte aligned, disjoint from every buffer of
+ *           the layers.
+ * Everything is checked before anything is enqueued: each part as by its own call, that one row
+ * (token, sequence) passes through, and that the parts are wired to each other: append reads
+ * inside qkv's y and the attention reads append's q_out and its cache; o reads the attention's
+ * out; attn_norm reads o's y and writes gate_up's x; glu reads inside gate_up's y and writes
+ * down's x; mlp_norm reads down's y and writes the next layer's x.
+ * Errors: of the parts; SPAX_ERR_PARAM for a part wired elsewhere (message names layer and part).
+ */
+int spax_decode_layers(const spax_decoder_layer* layers, int32_t n_layers, int32_t flags,
+                       void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---------------------------------------------------------------- diagnostics */
 
 /* A plain streaming read, to measure what a launch that only reads gets from the memory
