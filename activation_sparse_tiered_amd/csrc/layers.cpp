@@ -1,4 +1,5 @@
 // spax_decode_layers: a batch-one decode step through whole decoder layers.
+#include <cstdio>
 #include <vector>
 
 #include "layer_ops.h"
@@ -156,7 +157,14 @@ int decode_layers(const spax_decoder_layer* layers, int32_t n, int32_t flags, vo
   step.phases = phases.data();
   step.ws = ws;
   step.ws_bytes = ws_bytes;
-  if ((st = validate_step(&step, false))) return st;
+  if ((st = validate_step(&step, false))) {
+    char msg[400];
+    snprintf(msg, sizeof(msg), "%s", spax_last_error());
+    int phase = 0, at = 0;
+    if (sscanf(msg, "phase %d: %n", &phase, &at) < 1) return st;
+    static const char* const name[kPhases] = {"qkv", "o", "gate_up", "down"};
+    return fail(st, "layer %d, %s: %s", phase / kPhases, name[phase % kPhases], msg + at);
+  }
   if (flags & SPAX_STEP_DETERMINISTIC) {
     const size_t det = deterministic_workspace_bytes(phases.data(), step.n_phases);
     need = det > need ? det : need;
