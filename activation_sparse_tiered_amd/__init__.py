@@ -320,19 +320,44 @@ def _keep(struct, *tensors, parts=()):
     if len(devices) > 1:
         raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
     struct._keep = (tensors, parts)
-    struct._device = next(iter(devices)) if devices else None
+    return _on(struct, next(iter(devices)))
+
+
+def _on(struct, device):
+    struct._device = device
+    struct._index = device.index if device.type == "cuda" else None
     return struct
 
 
-def _call(fn, where, device, stream, *args):
-    """Runs fn(*args, stream) with the tensors' device current."""
-    if device.type != "cuda":
-        raise ValueError(f"{where}: the tensors are on {device}, not on a GPU")
+def _fast(name, slow):
+    """torch's own C function for `slow`, where this torch has it (a microsecond a call less)."""
     import torch
-    index = device.index
-    if index == torch.cuda.current_device():
-        status = fn(*args, _stream(stream))
+    return getattr(torch._C, name, slow)
+
+
+def _public_stream(index):
+    import torch
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _public_device():
+    import torch
+    return torch.cuda.current_device()
+
+
+_current_stream = _fast("_cuda_getCurrentRawStream", _public_stream)
+_current_device = _fast("_cuda_getDevice", _public_device)
+
+
+def _call(fn, where, desc, stream, *args):
+    """Runs fn(*args, stream) with the device of desc's tensors current."""
+    index = desc._index
+    if index is None:
+        raise ValueError(f"{where}: the tensors are on {desc._device}, not on a GPU")
+    if index == _current_device():
+        status = fn(*args, _current_stream(index) if stream is None else _stream(stream))
     else:
+        import torch
         with torch.cuda.device(index):
             status = fn(*args, _stream(stream))
     if status:
@@ -409,7 +434,7 @@ def make_kv_append(cache: KvCache, q, k, v, positions, q_out, seq=None, inv_freq
 
 
 def spax_kv_append(args: KvAppendArgs, stream=None) -> None:
-    _call(lib.spax_kv_append, "spax_kv_append", args._device, stream, args)
+    _call(lib.spax_kv_append, "spax_kv_append", args, stream, args)
 
 
 def make_attention(cache: KvCache, q, lens, out, max_len: int | None = None,
@@ -444,7 +469,7 @@ def spax_paged_attention(args: AttentionArgs, ws=None, ws_bytes: int | None = No
                          stream=None) -> None:
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
-    _call(lib.spax_paged_attention, "spax_paged_attention", args._device, stream, args, _ptr(ws),
+    _call(lib.spax_paged_attention, "spax_paged_attention", args, stream, args, _ptr(ws),
           ws_bytes)
 
 
@@ -496,7 +521,7 @@ def make_residual_norm(residual, block, residual_out, x, kind: str = "rms", pre_
 
 
 def spax_residual_norm(args: ResidualNormArgs, stream=None) -> None:
-    _call(lib.spax_residual_norm, "spax_residual_norm", args._device, stream, args)
+    _call(lib.spax_residual_norm, "spax_residual_norm", args, stream, args)
 
 
 def make_glu(gate, up, x, act: str = "silu") -> GluArgs:
@@ -515,7 +540,7 @@ def make_glu(gate, up, x, act: str = "silu") -> GluArgs:
 
 
 def spax_glu(args: GluArgs, stream=None) -> None:
-    _call(lib.spax_glu, "spax_glu", args._device, stream, args)
+    _call(lib.spax_glu, "spax_glu", args, stream, args)
 
 
 def make_layer(qkv: Phase, append: KvAppendArgs, attention: AttentionArgs, o: Phase,
@@ -531,15 +556,16 @@ def make_layer(qkv: Phase, append: KvAppendArgs, attention: AttentionArgs, o: Ph
     devices = {p._device for p in (append, attention, attn_norm, glu, mlp_norm)}
     if len(devices) > 1:
         raise ValueError(f"parts on different devices: {sorted(map(str, devices))}")
-    L._device = next(iter(devices))
-    return L
+    return _on(L, next(iter(devices)))
 
 
 def layer_array(layers):
     arr = (DecoderLayer * len(layers))(*layers)
     arr._keep = [L._keep for L in layers]
-    arr._device = layers[0]._device if layers else None
-    return arr
+    devices = {L._device for L in layers}
+    if len(devices) != 1:
+        raise ValueError(f"{len(layers)} layers on {len(devices)} devices")
+    return _on(arr, next(iter(devices)))
 
 
 def spax_layers_workspace_bytes(layers) -> int:
@@ -554,7 +580,7 @@ def spax_decode_layers(layers, ws, ws_bytes: int | None = None, flags: int = 0,
     arr = layers if isinstance(layers, C.Array) else layer_array(layers)
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
-    _call(lib.spax_decode_layers, "spax_decode_layers", arr._device, stream, arr, len(arr),
+    _call(lib.spax_decode_layers, "spax_decode_layers", arr, stream, arr, len(arr),
           int(flags), _ptr(ws), int(ws_bytes))
 
 

@@ -237,10 +237,9 @@ int check_attention(const spax_attention_args* a, Spans* spans) {
   if ((st = check_rows2("q", n, a->q_seq_stride, a->n_heads, a->q_head_stride, d, false)) ||
       (st = check_rows2("out", n, a->out_seq_stride, a->n_heads, a->out_head_stride, d, true)))
     return st;
-  const AttentionPlan plan = attention_plan(a);
-  if (n * a->n_heads > INT32_MAX ||
-      n * c.n_kv_heads * plan.head_tiles > INT32_MAX / plan.max_chunks)
-    return fail(SPAX_ERR_SHAPE, "more than 2^31 - 1 pieces of work");
+  if (a->n_heads > 65535 || attention_plan(a).units > INT32_MAX)
+    return fail(SPAX_ERR_SHAPE, "%d heads, or %d sequences of %d keys, are too many", a->n_heads,
+                c.n_seqs, a->max_len);
   Spans b;
   add_rows(&b, a->q, n, a->q_seq_stride, a->n_heads, a->q_head_stride, d, a->type, false, "q");
   add_rows(&b, a->out, n, a->out_seq_stride, a->n_heads, a->out_head_stride, d, a->type, true,

@@ -18,17 +18,22 @@
 //   * p is split into two 16-bit values, p = hi + lo, each multiplied: rounding p to 16 bits
 //     would cost as much error again as rounding the result.
 #include "layer_ops.h"
+#include "mask_core.h"
 
 namespace spax {
 namespace {
 
 using namespace elem;
 
-constexpr int kTile = 32;        // keys per wave and step
-constexpr int kAttnWaves = 4;
-constexpr int kAttnThreads = 64 * kAttnWaves;
+// Keys that a wave takes per step: 32, or 64 where 32 keys and values would be half the registers
+// a wave can spare for them.
+constexpr int tile_keys(bool narrow, int dim) { return (narrow ? dim / 2 : dim) <= 64 ? 64 : 32; }
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kJoinThreads = 256;
+constexpr int kWaves = 8;        // per workgroup: two per SIMD leave a wave 256 registers
+constexpr int kMaxShares = 256;
+constexpr int kSeqCost = 4;      // what a sequence costs besides its keys, in tiles
 
 struct AttnArgs {
   const void *q, *k, *v;
@@ -39,7 +44,7 @@ struct AttnArgs {
   int64_t qs, qh, os, oh;
   int64_t k_page, k_head, k_row, v_page, v_head, v_row, table_stride;
   int32_t n_heads, n_kv, group, head_tiles, n_seqs, n_pages, page_shift;
-  int32_t max_len, window, chunk_tiles, max_chunks;
+  int32_t max_len, window, shares, lds_waves;
   float scale;
 };
 
@@ -73,14 +78,16 @@ struct Mma<bf16> {
   typedef bf16x2 v2;
 };
 
+__device__ inline u32x4 load16(const void* p) { return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)); }
+
 // N dwords at p (aligned to their own size, at most 16 bytes; 3 dwords never occur).
 template <int N>
 __device__ inline void load_words(const void* p, uint32_t* w) {
   if constexpr (N == 4) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+    const u32x4 x = load16(p);
     w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
   } else if constexpr (N == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     w[0] = x.x; w[1] = x.y;
   } else {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
@@ -106,31 +113,46 @@ struct Wave {
   f32x4 o[VN];
   float m, l;  // of head lane % 16: the running max (scaled to log2), this lane's part of the sum
 
-  // The K rows of 16 keys as the first operand, widened if need be.
-  static __device__ inline void load_k(const uint8_t* row, int g, u32x4 k[KC]) {
+  // A lane's part of the K rows of 16 keys, as stored.  Which dims a lane holds for which step is
+  // free as long as Q's are the same: 16 bytes per load, so a step of 32 dims of a 16-bit row
+  // (dims 32 c + 8 g ..), or two steps of an 8-bit row (64 c + 16 g .. for steps 2c and 2c + 1;
+  // a last single step by 8 bytes).
+  static constexpr int kPairs = NARROW ? KC / 2 : 0;
+  static constexpr int KW = NARROW ? kPairs + (KC & 1) : KC;  // loads
+  static __device__ inline void load_k(const uint8_t* row, int g, u32x4 k[KW]) {
     if constexpr (!NARROW) {
 #pragma unroll
-      for (int c = 0; c < KC; ++c) k[c] = *reinterpret_cast<const u32x4*>(row + 64 * c + 16 * g);
+      for (int c = 0; c < KC; ++c) k[c] = load16(row + 64 * c + 16 * g);
     } else {
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(row + 32 * c + 8 * g);
-        k[c].x = w.x;
-        k[c].y = w.y;
+      for (int c = 0; c < kPairs; ++c) k[c] = load16(row + 64 * c + 16 * g);
+      if constexpr (KC & 1) {
+        uint32_t w[2];
+        load_words<2>(row + 64 * kPairs + 8 * g, w);
+        k[kPairs].x = w[0];
+        k[kPairs].y = w[1];
       }
     }
   }
-  static __device__ inline u32x4 widen_k(u32x4 k) {
+  // Step c's operand.
+  static __device__ inline u32x4 k_step(const u32x4 k[KW], int c) {
     if constexpr (NARROW) {
+      const u32x4 w = k[c / 2];
+      const uint32_t x = c % 2 ? w.z : w.x, y = c % 2 ? w.w : w.y;
       u32x4 r;
-      r.x = Mma<T>::template widen<false>(k.x);
-      r.y = Mma<T>::template widen<true>(k.x);
-      r.z = Mma<T>::template widen<false>(k.y);
-      r.w = Mma<T>::template widen<true>(k.y);
+      r.x = Mma<T>::template widen<false>(x);
+      r.y = Mma<T>::template widen<true>(x);
+      r.z = Mma<T>::template widen<false>(y);
+      r.w = Mma<T>::template widen<true>(y);
       return r;
     } else {
-      return k;
+      return k[c];
     }
+  }
+  // Byte offset in a Q row of step c's eight values.
+  static __device__ inline int q_at(int c, int g) {
+    if (NARROW && c < 2 * kPairs) return 2 * (64 * (c / 2) + 16 * g + 8 * (c % 2));
+    return 2 * (32 * c + 8 * g);
   }
   // A lane's piece of one V row: VN values, packed as stored.
   static constexpr int VW = (VN * EB + 3) / 4 < 1 ? 1 : (VN * EB + 3) / 4;
@@ -142,294 +164,493 @@ struct Wave {
     else if constexpr (n1 * EB == 2)
       w[n0 * EB / 4] = *reinterpret_cast<const uint16_t*>(row + 16 * n0 * EB + n1 * EB * r);
   }
+  // Where a piece's rows are.
+  struct Source {
+    const int32_t* table;
+    const uint8_t *k, *v;
+    int64_t k_page, k_row, v_page, v_row;
+    int page_shift, n_pages, lo, hi;
+    float to_log2;
+    // The table entry of key tile * kTile + lane % kTile (past the end: of the last key).
+    __device__ inline int look_up(int tile, int lane) const {
+      const int at = (tile * kTile + (lane & (kTile - 1))) >> page_shift;
+      const int end = (hi - 1) >> page_shift;
+      return table[at < end ? at : end];
+    }
+  };
+  // A tile's keys and values, 16 keys per K operand and 32 per V operand.
+  static constexpr int kTile = tile_keys(NARROW, D);
+  static constexpr int KH = kTile / 16, VH = kTile / 32;
+  struct Tile {
+    u32x4 k[KH][KW];
+    uint32_t v[VH][8][VW];
+    int page;  // of key lane % kTile, or -1 (see place)
+    int kb;
+    bool whole;
+  };
+
+  __device__ inline void begin() {
+#pragma unroll
+    for (int c = 0; c < KC; ++c) q[c] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int t = 0; t < VN; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    m = -INFINITY;
+    l = 0.0f;
+  }
+  __device__ inline void load_q(const uint8_t* row, int g) {
+#pragma unroll
+    for (int c = 0; c < KC; ++c) q[c] = *reinterpret_cast<const u32x4*>(row + q_at(c, g));
+  }
+
+  static __device__ inline void place(Tile& x, const Source& s, int tile, int entry, int lane) {
+    const int kb = tile * kTile, key = kb + (lane & (kTile - 1));
+    // -1 where the key's group of four (always on one page) has no key in [lo, hi) or the entry
+    // names no page: such rows are read from page 0 and then masked
+    const bool ok = (key | 3) >= s.lo && (key & ~3) < s.hi && (uint32_t)entry < (uint32_t)s.n_pages;
+    x.page = ok ? entry : -1;
+    x.kb = kb;
+    x.whole = kb >= s.lo && kb + kTile <= s.hi && __all(ok);
+  }
+  static __device__ inline void load_keys(Tile& x, const Source& s, int lane) {
+    const int g = lane >> 4, r = lane & 15, row_mask = (1 << s.page_shift) - 1;
+#pragma unroll
+    for (int h = 0; h < KH; ++h) {
+      const int pg = __shfl(x.page, 16 * h + r);
+      const int64_t row = (int64_t)(pg < 0 ? 0 : pg) * s.k_page +
+                          (int64_t)((x.kb + 16 * h + r) & row_mask) * s.k_row;
+      load_k(s.k + EB * row, g, x.k[h]);
+    }
+  }
+  static __device__ inline void load_values(Tile& x, const Source& s, int lane) {
+    const int g = lane >> 4, r = lane & 15, row_mask = (1 << s.page_shift) - 1;
+#pragma unroll
+    for (int h = 0; h < KH; ++h) {
+      const int pg = __shfl(x.page, 16 * h + 4 * g);
+      const int64_t row = (int64_t)(pg < 0 ? 0 : pg) * s.v_page +
+                          (int64_t)((x.kb + 16 * h + 4 * g) & row_mask) * s.v_row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        load_v(s.v + EB * (row + i * s.v_row), r, x.v[h / 2][4 * (h % 2) + i]);
+    }
+  }
+
+  // Scores of the tile's keys in base 2; a lane's are keys 16 h + 4 g + i of its head.
+  __device__ inline void score(const Tile& x, const Source& src, float p[4 * KH]) {
+#pragma unroll
+    for (int h = 0; h < KH; ++h) {
+      f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) s = Mma<T>::mul(k_step(x.k[h], c), q[c], s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[4 * h + i] = s[i] * src.to_log2;
+    }
+  }
+
+  // Masks keys that do not count: their scores and, since 0 * NaN is NaN, their values.
+  static __device__ inline void mask_out(Tile& x, const Source& src, int lane, float p[4 * KH]) {
+    const int g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < KH; ++h) {
+      const int pg = __shfl(x.page, 16 * h + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = x.kb + 16 * h + 4 * g + i;
+        const uint32_t keep = key >= src.lo && key < src.hi && pg >= 0 ? ~0u : 0u;
+        p[4 * h + i] = keep ? p[4 * h + i] : -INFINITY;
+#pragma unroll
+        for (int y = 0; y < VW; ++y) x.v[h / 2][4 * (h % 2) + i][y] &= keep;
+      }
+    }
+  }
+
+  // The softmax step and the product with the tile's values.
+  __device__ inline void take(Tile& x, const Source& src, int lane, float p[4 * KH]) {
+    if (!x.whole) mask_out(x, src, lane, p);
+    float top = p[0];
+#pragma unroll
+    for (int i = 1; i < 4 * KH; ++i) top = fmaxf(top, p[i]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any(top > m)) {
+      const float higher = fmaxf(m, top);
+      const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
+      m = higher;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < VN; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][i] *= f;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int v = 0; v < VH; ++v) {
+      u32x4 hi2, lo2;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(p[8 * v + i] - base);
+        const float p1 = __builtin_amdgcn_exp2f(p[8 * v + i + 1] - base);
+        l += p0 + p1;
+        typename Mma<T>::v2 h, rest;
+        h.x = (T)p0;
+        h.y = (T)p1;
+        rest.x = (T)(p0 - (float)h.x);
+        rest.y = (T)(p1 - (float)h.y);
+        hi2[i / 2] = __builtin_bit_cast(uint32_t, h);
+        lo2[i / 2] = __builtin_bit_cast(uint32_t, rest);
+      }
+      // 8 keys of each dim, pair by pair: byte permutes of two rows' words
+#pragma unroll
+      for (int t2 = 0; t2 < VN / 2; ++t2) {
+        uint32_t y[8];  // dims 2 t2 and 2 t2 + 1 of the 8 keys, 16-bit
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (NARROW)
+            y[i] = t2 % 2 ? Mma<T>::template widen<true>(x.v[v][i][t2 / 2])
+                          : Mma<T>::template widen<false>(x.v[v][i][t2 / 2]);
+          else
+            y[i] = x.v[v][i][t2];
+        }
+        u32x4 even, odd;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          even[i] = __builtin_amdgcn_perm(y[2 * i + 1], y[2 * i], 0x05040100u);
+          odd[i] = __builtin_amdgcn_perm(y[2 * i + 1], y[2 * i], 0x07060302u);
+        }
+        o[2 * t2] = Mma<T>::mul(even, hi2, o[2 * t2]);
+        o[2 * t2 + 1] = Mma<T>::mul(odd, hi2, o[2 * t2 + 1]);
+        o[2 * t2] = Mma<T>::mul(even, lo2, o[2 * t2]);
+        o[2 * t2 + 1] = Mma<T>::mul(odd, lo2, o[2 * t2 + 1]);
+      }
+    }
+  }
+};
+
+// The keys [lo, hi) of a sequence that count, and the tiles they lie in.
+struct Keys {
+  int lo, hi, first, tiles;
+};
+template <int TILE>
+__device__ inline Keys keys_of(const AttnArgs& a, int n) {
+  Keys k;
+  k.hi = n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+  k.lo = a.window > 0 && k.hi > a.window ? k.hi - a.window : 0;
+  k.first = k.lo / TILE;
+  k.tiles = (k.hi + TILE - 1) / TILE - k.first;
+  return k;
+}
+
+// The sequences laid end to end, each as kSeqCost units and then one per tile, cut into a.shares
+// equal shares (the units fit 31 bits).  Every wave finds its place by itself: lane l holds
+// sequence base + l, and a scan over the lanes gives where each ends.
+template <int TILE>
+struct Line {
+  int base, len;     // this lane's sequence: base + lane
+  int upto;          // units of the sequences before base + lane + 1
+  int last;          // upto of lane 63
+  int total, share;  // units in all and per share
+
+  __device__ inline void load(const AttnArgs& a, int lane, int from, int before) {
+    base = from;
+    const int s = base + lane;
+    len = s < a.n_seqs ? a.lens[s] : 0;
+    const int units = s < a.n_seqs ? kSeqCost + keys_of<TILE>(a, len).tiles : 0;
+    upto = before + mask::wave_scan(units);
+    last = __builtin_amdgcn_readlane(upto, 63);
+  }
+  __device__ inline void start(const AttnArgs& a, int lane) {
+    load(a, lane, 0, 0);
+    total = last;
+    if (a.n_seqs > 64) {
+      while (base + 64 < a.n_seqs) load(a, lane, base + 64, last);
+      total = last;
+      load(a, lane, 0, 0);
+    }
+    share = (int)(((uint32_t)total + (uint32_t)a.shares - 1u) / (uint32_t)a.shares);
+  }
+  // The lane whose sequence holds unit x < total, at or past the loaded block.
+  __device__ inline int find(const AttnArgs& a, int lane, int x) {
+    while (x >= last) load(a, lane, base + 64, last);
+    return __builtin_ctzll(__ballot(upto > x));
+  }
+  // Of the sequence in lane `who`.
+  __device__ inline int length(int who) const { return __builtin_amdgcn_readlane(len, who); }
+  __device__ inline int end(int who) const { return __builtin_amdgcn_readlane(upto, who); }
 };
 
 template <class T, bool NARROW, int D>
-__global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a) {
   using W = Wave<T, NARROW, D>;
-  constexpr int KC = W::KC, VN = W::VN, VW = W::VW, EB = W::EB;
+  constexpr int EB = W::EB, VN = W::VN, kTile = W::kTile;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
 
-  // work item: chunk fastest, so that the pieces of one sequence start together
-  int id = blockIdx.x;
-  const int chunk = id % a.max_chunks;
-  id /= a.max_chunks;
-  const int ht = id % a.head_tiles;
-  id /= a.head_tiles;
-  const int kvh = id % a.n_kv;
-  const int seq = id / a.n_kv;
-
-  int hi = a.lens[seq];
-  hi = hi < 0 ? 0 : hi > a.max_len ? a.max_len : hi;
-  const int lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-  const int first = lo / kTile, end = (hi + kTile - 1) / kTile;
-  const int chunks = (end - first + a.chunk_tiles - 1) / a.chunk_tiles;
-  if (chunk >= chunks && chunk > 0) return;
-  const int t0 = first + chunk * a.chunk_tiles;
-  const int t1 = t0 + a.chunk_tiles < end ? t0 + a.chunk_tiles : end;
+  // Work item: a share of the line for one key head (16 of its query heads).  Workgroups go to the
+  // 8 XCDs in turn; an XCD gets neighbouring items, so that the heads of a share, whose rows
+  // lie side by side in the cache, are read through the same caches and translations.
+  const int n_hh = a.n_kv * a.head_tiles;
+  const int per_xcd = gridDim.x >> 3;
+  const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  const int share = item / n_hh, hh = item % n_hh;
+  if (share >= a.shares) return;
+  const int kvh = hh / a.head_tiles, ht = hh % a.head_tiles;
   const int heads = a.group - 16 * ht < 16 ? a.group - 16 * ht : 16;  // of this workgroup
   const int head0 = kvh * a.group + 16 * ht;
 
-  W w;
-#pragma unroll
-  for (int c = 0; c < KC; ++c) w.q[c] = u32x4{0u, 0u, 0u, 0u};
-  if (r < heads) {
-    const uint8_t* qrow = (const uint8_t*)a.q + 2 * (seq * a.qs + (head0 + r) * a.qh);
-#pragma unroll
-    for (int c = 0; c < KC; ++c) w.q[c] = *reinterpret_cast<const u32x4*>(qrow + 64 * c + 16 * g);
-  }
-#pragma unroll
-  for (int t = 0; t < VN; ++t) w.o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  w.m = -INFINITY;
-  w.l = 0.0f;
-
-  float to_log2 = a.scale * kLog2e;
-  if constexpr (NARROW)
+  float to_log2 = a.scale * kLog2e, v_mul = 1.0f;
+  if constexpr (NARROW) {
     if (a.k_scale) to_log2 *= a.k_scale[kvh];
-
-  const int32_t* table = a.table + seq * a.table_stride;
+    if (a.v_scale) v_mul = a.v_scale[kvh];
+  }
   const uint8_t* kbase = (const uint8_t*)a.k + (int64_t)EB * kvh * a.k_head;
   const uint8_t* vbase = (const uint8_t*)a.v + (int64_t)EB * kvh * a.v_head;
-  const int row_mask = (1 << a.page_shift) - 1;
 
-  for (int tile = t0 + wave; tile < t1; tile += kAttnWaves) {
-    const int kb = tile * kTile;
-    // lane l looks up the page of key l % 32 (a key outside [lo, hi) that of the nearest inside)
-    int at = kb + (lane & 31);
-    at = at < lo ? lo : at >= hi ? hi - 1 : at;
-    const int entry = table[at >> a.page_shift];
-    const int page_ok = (uint32_t)entry < (uint32_t)a.n_pages;
-    const int page = page_ok ? entry : -1;
-    const bool whole = kb >= lo && kb + kTile <= hi && __all(page_ok);
+  Line<kTile> line;
+  line.start(a, lane);
+  int at = share * line.share;
+  const int stop = at + line.share < line.total ? at + line.share : line.total;
+  if (at >= stop) return;
+  int who = line.find(a, lane, at);
+  bool again = false;
+  while (at < stop) {
+    if (who == 64) who = line.find(a, lane, at);
+    const int seq = line.base + who;
+    const Keys x = keys_of<kTile>(a, line.length(who));
+    const int ends = line.end(who), begins = ends - x.tiles;  // of its tiles
+    ++who;
+    const bool whole_start = at <= begins - kSeqCost;  // its first unit is in this share
+    const int from = at > begins ? at : begins, to = ends < stop ? ends : stop;
+    at = ends;
+    // a sequence of no keys is answered where it begins; otherwise only tiles make a piece
+    if (x.tiles == 0 ? !whole_start : from >= to) continue;
+    const int t0 = x.first + from - begins;
+    const int t1 = x.tiles ? x.first + to - begins : t0;
 
-    u32x4 k[2][KC];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int pg = __shfl(page, 16 * half + r);
-      const int64_t row = (int64_t)(pg < 0 ? 0 : pg) * a.k_page +
-                          (int64_t)((kb + 16 * half + r) & row_mask) * a.k_row;
-      W::load_k(kbase + EB * row, g, k[half]);
-    }
-    uint32_t v[8][VW];
-    int vpage[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      vpage[half] = __shfl(page, 16 * half + 4 * g);
-      const int64_t row = (int64_t)(vpage[half] < 0 ? 0 : vpage[half]) * a.v_page +
-                          (int64_t)((kb + 16 * half + 4 * g) & row_mask) * a.v_row;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) W::load_v(vbase + EB * (row + i * a.v_row), r, v[4 * half + i]);
-    }
-
-    f32x4 s[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      s[half] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < KC; ++c) s[half] = Mma<T>::mul(W::widen_k(k[half][c]), w.q[c], s[half]);
-    }
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = s[i / 4][i % 4] * to_log2;
-    if (!whole) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = kb + 16 * (i / 4) + 4 * g + i % 4;
-        if (!(key >= lo && key < hi && vpage[i / 4] >= 0)) {
-          p[i] = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < VW; ++x) v[i][x] = 0u;
+    W w;
+    w.begin();
+    if (r < heads) w.load_q((const uint8_t*)a.q + 2 * (seq * a.qs + (head0 + r) * a.qh), g);
+    const typename W::Source src{a.table + seq * a.table_stride, kbase, vbase, a.k_page, a.k_row,
+                                 a.v_page, a.v_row, a.page_shift, a.n_pages, x.lo, x.hi, to_log2};
+    int tile = t0 + wave;
+    if (tile < t1) {
+      // The next tile's keys are loaded once this one's are used, its values likewise, so loads
+      // are in flight through all of the arithmetic.  Its table entry was loaded ahead of this
+      // tile, so it never waits behind one.
+      typename W::Tile z;
+      W::place(z, src, tile, src.look_up(tile, lane), lane);
+      int next = src.look_up(tile + kWaves, lane);
+      W::load_keys(z, src, lane);
+      W::load_values(z, src, lane);
+      for (;;) {
+        float p[4 * W::KH];
+        w.score(z, src, p);
+        tile += kWaves;
+        if (tile >= t1) {
+          w.take(z, src, lane, p);
+          break;
         }
+        typename W::Tile after;  // its k and v are z's registers
+        W::place(after, src, tile, next, lane);
+        next = src.look_up(tile + kWaves, lane);
+        W::load_keys(after, src, lane);
+        w.take(z, src, lane, p);
+        W::load_values(after, src, lane);
+        z = after;
       }
     }
-    float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])),
-                      fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    if (__any(top > w.m)) {
-      const float m = fmaxf(w.m, top);
-      const float f = m == w.m ? 1.0f : __builtin_amdgcn_exp2f(w.m - m);
-      w.m = m;
-      w.l *= f;
-#pragma unroll
-      for (int t = 0; t < VN; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w.o[t][i] *= f;
-    }
-    const float base = w.m == -INFINITY ? 0.0f : w.m;
-    u32x4 hi2, lo2;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float p0 = __builtin_amdgcn_exp2f(p[i] - base);
-      const float p1 = __builtin_amdgcn_exp2f(p[i + 1] - base);
-      w.l += p0 + p1;
-      typename Mma<T>::v2 h;
-      h.x = (T)p0;
-      h.y = (T)p1;
-      typename Mma<T>::v2 rest;
-      rest.x = (T)(p0 - (float)h.x);
-      rest.y = (T)(p1 - (float)h.y);
-      hi2[i / 2] = __builtin_bit_cast(uint32_t, h);
-      lo2[i / 2] = __builtin_bit_cast(uint32_t, rest);
-    }
-    // 8 keys of each dim, pair by pair: byte permutes of two rows' words
-#pragma unroll
-    for (int t2 = 0; t2 < VN / 2; ++t2) {
-      uint32_t x[8];  // dims 2 t2 and 2 t2 + 1 of the 8 keys, 16-bit
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (NARROW)
-          x[i] = t2 % 2 ? Mma<T>::template widen<true>(v[i][t2 / 2])
-                        : Mma<T>::template widen<false>(v[i][t2 / 2]);
-        else
-          x[i] = v[i][t2];
-      }
-      u32x4 even, odd;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        even[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
-        odd[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
-      }
-      w.o[2 * t2] = Mma<T>::mul(even, hi2, w.o[2 * t2]);
-      w.o[2 * t2 + 1] = Mma<T>::mul(odd, hi2, w.o[2 * t2 + 1]);
-      w.o[2 * t2] = Mma<T>::mul(even, lo2, w.o[2 * t2]);
-      w.o[2 * t2 + 1] = Mma<T>::mul(odd, lo2, w.o[2 * t2 + 1]);
-    }
-  }
 
-  // Join the waves: each puts m, l and o of the group's heads into LDS, dims a block at a time.
-  w.l += __shfl_xor(w.l, 16);
-  w.l += __shfl_xor(w.l, 32);
-  constexpr int n0 = VDims<D>::n0, n1 = VDims<D>::n1;
-  constexpr int kPad = 4;
-  constexpr int stride = 16 * n0 + kPad;  // n1 <= n0
-  float* ml = lds;                         // [wave][16][2]
-  float* ob = lds + kAttnWaves * 32;       // [wave][heads][stride]
-  if (g == 0) {
-    ml[(wave * 16 + r) * 2] = w.m;
-    ml[(wave * 16 + r) * 2 + 1] = w.l;
-  }
-  const bool last = chunks <= 1;
-  float v_mul = 1.0f;
-  if constexpr (NARROW)
-    if (a.v_scale) v_mul = a.v_scale[kvh];
-#pragma unroll
-  for (int block = 0; block < (n1 ? 2 : 1); ++block) {
-    const int n = block ? n1 : n0;
-    const int t_base = block ? n0 : 0;
-    if (block) __syncthreads();
-    if (r < heads) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < (n1 > n0 ? n1 : n0); ++t)
-          if (t < n) ob[(wave * heads + r) * stride + (4 * g + i) * n + t] = w.o[t_base + t][i];
+    // Join the waves: m and l through LDS, then o of a.lds_waves waves at a time, a block of dims
+    // at a time, each wave's scaled to the common maximum before it is stored.
+    if (again) __syncthreads();  // the last piece's are still being read
+    again = true;
+    w.l += __shfl_xor(w.l, 16);
+    w.l += __shfl_xor(w.l, 32);
+    constexpr int n0 = VDims<D>::n0, n1 = VDims<D>::n1;
+    constexpr int kStride = 16 * n0 + 4;  // n1 <= n0
+    constexpr int kPer = (16 * 4 * n0 + 64 * kWaves - 1) / (64 * kWaves);  // four-value items per thread
+    float* ml = lds;               // [wave][16][2]
+    float* ob = lds + kWaves * 32;     // [slot][heads][kStride]
+    if (g == 0) {
+      ml[(wave * 16 + r) * 2] = w.m;
+      ml[(wave * 16 + r) * 2 + 1] = w.l;
     }
     __syncthreads();
-    const int dims = 16 * n;
-    for (int e = threadIdx.x; e < heads * (dims / 4); e += kAttnThreads) {
-      const int h = e / (dims / 4), d = 4 * (e % (dims / 4));
-      float m = -INFINITY;
+    float m_all = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kAttnWaves; ++x) m = fmaxf(m, ml[(x * 16 + h) * 2]);
-      const float base = m == -INFINITY ? 0.0f : m;
-      float l = 0.0f;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int y = 0; y < kWaves; ++y) m_all = fmaxf(m_all, ml[(y * 16 + r) * 2]);
+    const float f_own = __builtin_amdgcn_exp2f(w.m - (m_all == -INFINITY ? 0.0f : m_all));
+    // the whole sequence, or the first or a later piece of it
+    const bool last = x.tiles == 0 || to - from == x.tiles;
+    const int which = from == begins;
 #pragma unroll
-      for (int x = 0; x < kAttnWaves; ++x) {
-        const float f = __builtin_amdgcn_exp2f(ml[(x * 16 + h) * 2] - base);
-        l += f * ml[(x * 16 + h) * 2 + 1];
-        const f32x4 o4 = *reinterpret_cast<const f32x4*>(&ob[(x * heads + h) * stride + d]);
+    for (int block = 0; block < (n1 ? 2 : 1); ++block) {
+      const int n = block ? n1 : n0;
+      const int t_base = block ? n0 : 0;
+      const int items = heads * 4 * n;  // four values of one head each
+      f32x4 sum[kPer];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += f * o4[i];
+      for (int y = 0; y < kPer; ++y) sum[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int from = 0; from < kWaves; from += a.lds_waves) {
+        if (block || from) __syncthreads();
+        if (r < heads && wave >= from && wave < from + a.lds_waves) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < n0; ++t)
+              if (t < n)
+                ob[((wave - from) * heads + r) * kStride + (4 * g + i) * n + t] =
+                    w.o[t_base + t < VN ? t_base + t : 0][i] * f_own;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+          const int e = threadIdx.x + y * 64 * kWaves;
+          if (e < items) {
+            const int h = e / (4 * n), d = 4 * (e % (4 * n));
+            for (int z = 0; z < a.lds_waves; ++z)
+              sum[y] += *reinterpret_cast<const f32x4*>(&ob[(z * heads + h) * kStride + d]);
+          }
+        }
       }
-      const int64_t row = (int64_t)seq * a.n_heads + head0 + h;
-      const int dim = (block ? 16 * n0 : 0) + d;
-      if (last) {
-        const float inv = v_mul / l;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = l == 0.0f ? 0.0f : sum[i] * inv;
-        store4((T*)a.out + seq * a.os + (head0 + h) * a.oh + dim, sum);
-        if (a.lse && dim == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-      } else {
-        const int64_t part = row * a.max_chunks + chunk;
-        *reinterpret_cast<f32x4*>(a.part_o + part * D + dim) =
-            f32x4{sum[0], sum[1], sum[2], sum[3]};
-        if (dim == 0) {
-          a.part_ml[2 * part] = m;
-          a.part_ml[2 * part + 1] = l;
+      for (int y = 0; y < kPer; ++y) {
+        const int e = threadIdx.x + y * 64 * kWaves;
+        if (e >= items) continue;
+        const int h = e / (4 * n), dim = (block ? 16 * n0 : 0) + 4 * (e % (4 * n));
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int z = 0; z < kWaves; ++z) m = fmaxf(m, ml[(z * 16 + h) * 2]);
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int z = 0; z < kWaves; ++z)
+          l += __builtin_amdgcn_exp2f(ml[(z * 16 + h) * 2] - base) * ml[(z * 16 + h) * 2 + 1];
+        if (last) {
+          const float inv = v_mul / l;
+          float out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[y][i] * inv;
+          store4((T*)a.out + seq * a.os + (head0 + h) * a.oh + dim, out);
+          if (a.lse && dim == 0)
+            a.lse[(int64_t)seq * a.n_heads + head0 + h] =
+                l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+          const int64_t part = 2 * ((int64_t)(head0 + h) * a.shares + share) + which;
+          *reinterpret_cast<f32x4*>(a.part_o + part * D + dim) = sum[y];
+          if (dim == 0) {
+            a.part_ml[2 * part] = m;
+            a.part_ml[2 * part + 1] = l;
+          }
         }
       }
     }
   }
 }
 
-// Joins the pieces of one (sequence, head) that was shared out: one workgroup each.
-template <class T, int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-  constexpr int kLanes = D / 4;            // threads per piece
-  constexpr int kAtOnce = 256 / kLanes;    // pieces in flight
+// Joins the pieces of a sequence that was cut: one workgroup per cut and head, of which that of
+// the sequence's first cut works.  A share writes at most two pieces of a head: the end of a
+// sequence (0) and the beginning of another (1).
+template <class T, bool NARROW, int D>
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
+  constexpr int kTile = tile_keys(NARROW, D);
+  constexpr int kLanes = D / 4;                     // threads per piece
+  constexpr int kAtOnce = kJoinThreads / kLanes;    // pieces per round
+  constexpr int kUnroll = 4;
   __shared__ float lds_o[kAtOnce][D];
-  __shared__ float lds_l[kAtOnce];
-  const int head = blockIdx.x % a.n_heads, seq = blockIdx.x / a.n_heads;
-  int hi = a.lens[seq];
-  hi = hi < 0 ? 0 : hi > a.max_len ? a.max_len : hi;
-  const int lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-  const int first = lo / kTile, end = (hi + kTile - 1) / kTile;
-  const int chunks = (end - first + a.chunk_tiles - 1) / a.chunk_tiles;
-  if (chunks <= 1) return;
-  const int64_t row = (int64_t)seq * a.n_heads + head;
-  const float* ml = a.part_ml + 2 * row * a.max_chunks;
-  const float* po = a.part_o + row * a.max_chunks * D;
-  float m = -INFINITY;
-  for (int c = 0; c < chunks; ++c) m = fmaxf(m, ml[2 * c]);
-  const float base = m == -INFINITY ? 0.0f : m;
-  const int part = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  float l = 0.0f;
-  if (part < kAtOnce) {
-    for (int c = part; c < chunks; c += kAtOnce) {
-      const float f = __builtin_amdgcn_exp2f(ml[2 * c] - base);
-      l += f * ml[2 * c + 1];
-      const f32x4 o = *reinterpret_cast<const f32x4*>(po + (int64_t)c * D + d);
+  __shared__ float lds_w[kMaxShares];
+  const int head = blockIdx.x % a.n_heads, cut = blockIdx.x / a.n_heads + 1;
+  const int tid = threadIdx.x, lane = tid & 63;
+  Line<kTile> line;
+  line.start(a, lane);
+  const int x = cut * line.share;
+  if (x >= line.total) return;
+  const int who = line.find(a, lane, x);
+  const int ends = line.end(who), begins = ends - keys_of<kTile>(a, line.length(who)).tiles;
+  if (x <= begins) return;
+  const int s0 = (int)((uint32_t)begins / (uint32_t)line.share);
+  if (s0 != cut - 1) return;
+  const int pieces = (int)((uint32_t)(ends - 1) / (uint32_t)line.share) - s0 + 1;
+  const int seq = line.base + who;
+
+  // piece c of this head: the beginning from share s0, the rest from the shares after it
+  const int64_t base = 2 * ((int64_t)head * a.shares + s0);
+  const auto place = [&](int c) { return base + (c ? 2 * c : 1); };
+  const int part = tid / kLanes, d = 4 * (tid % kLanes);
+  // every wave: the common maximum and the weights' sum (at most kMaxShares pieces)
+  float m = -INFINITY, l = 0.0f;
+  float pm[kMaxShares / 64], pl[kMaxShares / 64];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] += f * o[i];
+  for (int y = 0; y < kMaxShares / 64; ++y) {
+    const int c = lane + 64 * y;
+    pm[y] = -INFINITY;
+    pl[y] = 0.0f;
+    if (c < pieces) {
+      pm[y] = a.part_ml[2 * place(c)];
+      pl[y] = a.part_ml[2 * place(c) + 1];
     }
-    *reinterpret_cast<f32x4*>(&lds_o[part][d]) = f32x4{sum[0], sum[1], sum[2], sum[3]};
-    if (d == 0) lds_l[part] = l;
+    m = fmaxf(m, pm[y]);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  const float top = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+  for (int y = 0; y < kMaxShares / 64; ++y) {
+    const float f = __builtin_amdgcn_exp2f(pm[y] - top);
+    l += f * pl[y];
+    if (tid < 64) lds_w[lane + 64 * y] = f;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
+  __syncthreads();
+  if (part < kAtOnce) {
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float* p = a.part_o + d;
+    int c = part;
+    for (; c + (kUnroll - 1) * kAtOnce < pieces; c += kUnroll * kAtOnce) {
+      f32x4 o[kUnroll];
+#pragma unroll
+      for (int y = 0; y < kUnroll; ++y)
+        o[y] = *reinterpret_cast<const f32x4*>(p + place(c + y * kAtOnce) * D);
+#pragma unroll
+      for (int y = 0; y < kUnroll; ++y) sum += o[y] * lds_w[c + y * kAtOnce];
+    }
+    for (; c < pieces; c += kAtOnce)
+      sum += *reinterpret_cast<const f32x4*>(p + place(c) * D) * lds_w[c];
+    *reinterpret_cast<f32x4*>(&lds_o[part][d]) = sum;
   }
   __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  l = 0.0f;
-  float out[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int x = 0; x < kAtOnce; ++x) {
-    l += lds_l[x];
+  if (tid >= kLanes) return;
+  f32x4 total = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] += lds_o[x][d + i];
-  }
-  float v_mul = 1.0f;
-  if (a.v_scale) v_mul = a.v_scale[head / a.group];
-  const float inv = v_mul / l;
+  for (int y = 0; y < kAtOnce; ++y) total += *reinterpret_cast<const f32x4*>(&lds_o[y][d]);
+  const float inv = (a.v_scale ? a.v_scale[head / a.group] : 1.0f) / l;
+  float out[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : out[i] * inv;
+  for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : total[i] * inv;
   store4((T*)a.out + seq * a.os + head * a.oh + d, out);
   if (a.lse && d == 0)
-    a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    a.lse[(int64_t)seq * a.n_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <class T, bool NARROW, int D>
+void start(AttnArgs a, hipStream_t s) {
+  const int heads = a.group < 16 ? a.group : 16;
+  // as many waves' o at a time as fit 60 KB of LDS
+  const size_t per = sizeof(float) * (size_t)heads * (16 * VDims<D>::n0 + 4);
+  a.lds_waves = kWaves;
+  while (a.lds_waves > 1 && a.lds_waves * per > 60 * 1024) a.lds_waves /= 2;
+  const size_t lds = sizeof(float) * kWaves * 32 + a.lds_waves * per;
+  const unsigned items = (unsigned)(a.n_kv * a.head_tiles * a.shares);
+  const dim3 grid((items + 7) / 8 * 8);
+  hipLaunchKernelGGL((attention_kernel<T, NARROW, D>), grid, dim3(64 * kWaves), lds, s, a);
 }
 
 template <class T, bool NARROW, int D>
 int launch(const AttnArgs& a, const AttentionPlan& plan, hipStream_t s) {
-  const int heads = a.group < 16 ? a.group : 16;
-  const size_t lds =
-      sizeof(float) * kAttnWaves * (32 + (size_t)heads * (16 * VDims<D>::n0 + 4));
-  const dim3 grid((unsigned)((int64_t)a.n_seqs * a.n_kv * a.head_tiles * a.max_chunks));
-  hipLaunchKernelGGL((attention_kernel<T, NARROW, D>), grid, dim3(kAttnThreads), lds, s, a);
+  start<T, NARROW, D>(a, s);
   SPAX_HIP_CHECK(hipGetLastError());
-  if (a.max_chunks > 1) {
-    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(a.n_seqs * a.n_heads)),
-                       dim3(256), 0, s, a);
+  if (a.shares > 1) {
+    hipLaunchKernelGGL((attention_join_kernel<T, NARROW, D>), dim3((unsigned)((a.shares - 1) * a.n_heads)),
+                       dim3(kJoinThreads), 0, s, a);
     SPAX_HIP_CHECK(hipGetLastError());
   }
   return SPAX_OK;
@@ -453,20 +674,22 @@ AttentionPlan attention_plan(const spax_attention_args* a) {
   AttentionPlan p{};
   const int group = a->n_heads / c.n_kv_heads;
   p.head_tiles = (group + 15) / 16;
-  int64_t tiles = ((int64_t)a->max_len + kTile - 1) / kTile;
+  const int tile = tile_keys(c.type == SPAX_E4M3, c.head_dim);
+  int64_t tiles = ((int64_t)a->max_len + tile - 1) / tile;
   if (a->window > 0) {
-    const int64_t w = ((int64_t)a->window + kTile - 1) / kTile + 1;  // a window starts anywhere
+    const int64_t w = ((int64_t)a->window + tile - 1) / tile + 1;  // a window starts anywhere
     if (w < tiles) tiles = w;
   }
-  const int64_t rows = (int64_t)c.n_seqs * c.n_kv_heads * p.head_tiles;
-  int64_t chunk = (rows * tiles + 1023) / 1024;
-  chunk = (chunk + kAttnWaves - 1) / kAttnWaves * kAttnWaves;
-  if (chunk > 32) chunk = 32;
-  p.chunk_tiles = (int32_t)chunk;
-  p.max_chunks = (int32_t)((tiles + chunk - 1) / chunk);
-  if (p.max_chunks > 1)
-    p.ws_bytes = aligned_size((size_t)c.n_seqs * a->n_heads * p.max_chunks *
-                              ((size_t)c.head_dim + 2) * sizeof(float));
+  // One workgroup per compute unit (of 256), and at least four tiles a wave, below which a second
+  // launch to join the pieces costs more than it saves.
+  const int64_t items = (int64_t)c.n_kv_heads * p.head_tiles;
+  const int64_t most = (c.n_seqs * tiles + 4 * kWaves - 1) / (4 * kWaves);
+  int64_t shares = 256 / items;
+  shares = shares > most ? most : shares;
+  p.shares = (int32_t)(shares < 1 ? 1 : shares > kMaxShares ? kMaxShares : shares);
+  if (p.shares > 1)
+    p.ws_bytes = aligned_size((size_t)a->n_heads * p.shares * 2 * ((size_t)c.head_dim + 2) *
+                              sizeof(float));
   return p;
 }
 
@@ -485,9 +708,9 @@ int launch_attention(const spax_attention_args* p, void* ws, hipStream_t s) {
   a.head_tiles = plan.head_tiles; a.n_seqs = c.n_seqs; a.n_pages = c.n_pages;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   a.max_len = p->max_len; a.window = p->window; a.scale = p->scale;
-  a.chunk_tiles = plan.chunk_tiles; a.max_chunks = plan.max_chunks;
+  a.shares = plan.shares;
   a.part_o = (float*)ws;
-  a.part_ml = (float*)ws + (size_t)c.n_seqs * p->n_heads * plan.max_chunks * c.head_dim;
+  a.part_ml = (float*)ws + (size_t)2 * p->n_heads * plan.shares * c.head_dim;
   if (c.type == SPAX_E4M3)
     return p->type == SPAX_F16 ? launch_dim<f16, true>(a, plan, c.head_dim, s)
                                : launch_dim<bf16, true>(a, plan, c.head_dim, s);

@@ -34,12 +34,12 @@ int check_attention(const spax_attention_args* a, Spans* spans);
 int check_residual_norm(const spax_residual_norm_args* a, Spans* spans);
 int check_glu(const spax_glu_args* a, Spans* spans);
 
-// How an attention call shares out its keys: each workgroup takes chunk_tiles tiles of 32 keys
-// of one (sequence, key head, group of 16 query heads).
+// How an attention call shares out its keys: every key head's sequences, laid end to end, are cut
+// into `shares` equal shares (of the lengths at run time), one workgroup each.
 struct AttentionPlan {
   int32_t head_tiles;   // groups of 16 query heads per key head
-  int32_t chunk_tiles;
-  int32_t max_chunks;   // of the longest sequence the call allows
+  int32_t shares;
+  int64_t units;        // tiles and fixed costs of n_seqs sequences of max_len
   size_t ws_bytes;
 };
 AttentionPlan attention_plan(const spax_attention_args* a);
