@@ -529,7 +529,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a) {
           float out[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[y][i] * inv;
-          store4((T*)a.out + seq * a.os + (head0 + h) * a.oh + dim, out);
+          store_n<4>((T*)a.out + seq * a.os + (head0 + h) * a.oh + dim, out);
           if (a.lse && dim == 0)
             a.lse[(int64_t)seq * a.n_heads + head0 + h] =
                 l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -626,7 +626,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   float out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : total[i] * inv;
-  store4((T*)a.out + seq * a.os + head * a.oh + d, out);
+  store_n<4>((T*)a.out + seq * a.os + head * a.oh + d, out);
   if (a.lse && d == 0)
     a.lse[(int64_t)seq * a.n_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }

@@ -22,27 +22,26 @@ inline __host__ __device__ int bytes_of(int type) {
   return type == SPAX_F32 ? 4 : type == SPAX_E4M3 ? 1 : 2;
 }
 
-template <class T>
-__device__ inline float to_float(T v) {
-  return (float)v;
+// A vector at any address that is aligned to two bytes (global memory takes such accesses whole).
+template <class V>
+__device__ inline V load_any(const void* p) {
+  typedef V U __attribute__((aligned(2)));
+  return *reinterpret_cast<const U*>(p);
+}
+template <class V>
+__device__ inline void store_any(void* p, V v) {
+  typedef V U __attribute__((aligned(2)));
+  *reinterpret_cast<U*>(p) = v;
 }
 
-// Four values at p, which is aligned to four elements.
-template <class T>
-__device__ inline void load4(const T* p, float v[4]) {
-  typedef T T4 __attribute__((ext_vector_type(4)));
-  const T4 x = *reinterpret_cast<const T4*>(p);
+// N values from p (aligned to an element).
+template <int N, class T>
+__device__ inline void store_n(T* p, const float* v) {
+  typedef T TN __attribute__((ext_vector_type(N)));
+  TN x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (float)x[i];
-}
-
-template <class T>
-__device__ inline void store4(T* p, const float v[4]) {
-  typedef T T4 __attribute__((ext_vector_type(4)));
-  T4 x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = (T)v[i];
-  *reinterpret_cast<T4*>(p) = x;
+  for (int i = 0; i < N; ++i) x[i] = (T)v[i];
+  store_any(p, x);
 }
 
 // E4M3 values, kept as bytes: clamped to +-448 first (the conversion alone would turn a value
@@ -54,10 +53,19 @@ __device__ inline float clamp_e4m3(float v) {
   v = v > 448.0f ? 448.0f : v;
   return v < -448.0f ? -448.0f : v;
 }
-__device__ inline void store4(e4m3* p, const float v[4]) {
+__device__ inline uint32_t pack_e4m3(const float v[4]) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[0]), clamp_e4m3(v[1]), 0, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[2]), clamp_e4m3(v[3]), w, true);
-  *reinterpret_cast<int*>(p) = w;
+  return (uint32_t)w;
+}
+// N a multiple of four, p aligned to four bytes.
+template <int N>
+__device__ inline void store_n(e4m3* p, const float* v) {
+  typedef uint32_t W __attribute__((ext_vector_type(N / 4), aligned(4)));
+  W w;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) w[i] = pack_e4m3(v + 4 * i);
+  *reinterpret_cast<W*>(p) = w;
 }
 template <class T>
 __device__ inline void store1(T* p, float v) {

@@ -8,8 +8,9 @@
 //
 // Bound: bytes (each value is read once and written once) for prompts, launch latency for one
 // token.  A thread keeps one place in the head (four pairs, or eight copied values) and walks
-// over heads, so a token's sines are computed once per workgroup and live in registers.
+// over heads; a token's sines are computed once per workgroup, a pair per thread.
 #include "layer_ops.h"
+#include "mask_core.h"
 
 namespace spax {
 namespace {
@@ -17,6 +18,7 @@ namespace {
 using namespace elem;
 
 constexpr int kAppendThreads = 256;
+constexpr int kMaxPairs = 128;  // head_dim at most 256
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -55,22 +57,49 @@ __device__ inline void sine(int p, float inv_freq, float* sn, float* cs) {
   sincospif(2.0f * (float)(turns - rint(turns)), sn, cs);
 }
 
-// SRC: type of q, k, v; LOW: of q_out (and a 16-bit cache); C: of the cache.  VEC: eight values
-// per thread and head (rot a multiple of 8, rows aligned to four elements); otherwise one pair
-// or one copied value.
-template <class SRC, class LOW, class C, bool VEC>
+// Rotates N pairs: (x[i], y[i]), or, where the loaded values alternate between first and second,
+// (x[0], x[1]), (x[2], x[3]), .. (y[0], y[1]), ..
+template <int N>
+__device__ inline void turn(float x[N], float y[N], const float sn[N], const float cs[N],
+                            bool alternate) {
+  float u[N], w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float even = i < N / 2 ? x[2 * i % N] : y[2 * i % N];
+    const float odd = i < N / 2 ? x[(2 * i + 1) % N] : y[(2 * i + 1) % N];
+    const float px = alternate ? even : x[i], py = alternate ? odd : y[i];
+    u[i] = px * cs[i] - py * sn[i];
+    w[i] = px * sn[i] + py * cs[i];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int k = (N + i) / 2 % N;
+    x[i] = !alternate ? u[i] : i % 2 ? w[i / 2] : u[i / 2];
+    y[i] = !alternate ? w[i] : i % 2 ? w[k] : u[k];
+  }
+}
+
+template <int N, class T>
+__device__ inline void put(T* p, const float* v) {
+  if constexpr (N == 1)
+    store1(p, v[0]);
+  else
+    store_n<N>(p, v);
+}
+
+// SRC: type of q, k, v; LOW: of q_out (and a 16-bit cache); C: of the cache.  A thread's item is N
+// pairs of a head, or as many values that are copied: 2 N of them, one for N = 1.
+template <class SRC, class LOW, class C, int N>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
-  constexpr int N = VEC ? 4 : 1;  // pairs per item
+  constexpr int kCopied = N > 1 ? 2 * N : 1;
   const int t = blockIdx.x;
   const int pairs = a.rot / 2;
   // items of a head: pairs / N rotated ones, then the copied values
   const int turned = pairs / N;
-  const int items = turned + (a.dim - a.rot) / (VEC ? 8 : 1);
+  const int items = turned + (a.dim - a.rot) / kCopied;
   const int slot = threadIdx.x / items;
   const int j = threadIdx.x - slot * items;
-  if (slot >= a.heads_at_once) return;
   const int p = a.positions[t];
-  const Place to = place_of(a, t, p);
   const bool turns = j < turned;
   // element offsets of the item's first and second values
   int e0, e1;
@@ -78,123 +107,103 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     e0 = a.interleaved ? 2 * N * j : N * j;
     e1 = a.interleaved ? e0 + N : pairs + N * j;
   } else {
-    e0 = a.rot + (j - turned) * (VEC ? 8 : 1);
+    e0 = a.rot + (j - turned) * kCopied;
     e1 = e0 + N;
   }
-  const bool single = !VEC && !turns;  // one value, no second
-  float sn[N], cs[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    sn[i] = 0.0f;
-    cs[i] = 1.0f;
-    if (turns && p >= 0) sine(p, a.inv_freq[N * j + i], &sn[i], &cs[i]);
-  }
+  const bool single = N == 1 && !turns;  // one value, no second
+  // The token's sines, one thread per pair; the barrier orders LDS only, so the first heads'
+  // values, loaded before it, stay in flight.
+  __shared__ float sines[2][kMaxPairs];
+  const auto find_sines = [&] {
+    if ((int)threadIdx.x < pairs)
+      sine(p < 0 ? 0 : p, a.inv_freq[threadIdx.x], &sines[0][threadIdx.x],
+           &sines[1][threadIdx.x]);
+    mask::lds_barrier();
+  };
   const int n_heads = a.n_heads, n_kv = a.n_kv;
   const int h0 = blockIdx.y * a.heads_per_block;
   const int total = n_heads + 2 * n_kv;
   const int h1 = h0 + a.heads_per_block < total ? h0 + a.heads_per_block : total;
-  for (int h = h0 + slot; h < h1; h += a.heads_at_once) {
+  typedef SRC SN __attribute__((ext_vector_type(N)));
+  SN rx, ry;  // as loaded
+  const auto load = [&](int h) {
+    if (h >= h1) return;
+    const SRC* src = h < n_heads         ? (const SRC*)a.q + t * a.qt + h * a.qh
+                     : h < n_heads + n_kv ? (const SRC*)a.k + t * a.kt + (h - n_heads) * a.kh
+                                          : (const SRC*)a.v + t * a.vt + (h - n_heads - n_kv) * a.vh;
+    rx = load_any<SN>(src + e0);
+    if (!single) ry = load_any<SN>(src + e1);
+  };
+  const int mine = slot < a.heads_at_once ? h0 + slot : h1;  // threads past the last slot: none
+  load(mine);
+  const Place to = place_of(a, t, p);
+  find_sines();
+  float sn[N], cs[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    sn[i] = turns ? sines[0][N * j + i] : 0.0f;
+    cs[i] = turns ? sines[1][N * j + i] : 1.0f;
+  }
+  for (int h = mine; h < h1; h += a.heads_at_once) {
     const bool is_q = h < n_heads, is_v = h >= n_heads + n_kv;
-    const int hh = is_q ? h : is_v ? h - n_heads - n_kv : h - n_heads;
-    if (!is_q && !to.cached) continue;
-    const SRC* src = is_q   ? (const SRC*)a.q + t * a.qt + hh * a.qh
-                     : is_v ? (const SRC*)a.v + t * a.vt + hh * a.vh
-                            : (const SRC*)a.k + t * a.kt + hh * a.kh;
     float x[N], y[N];
-    if constexpr (VEC) {
-      load4(src + e0, x);
-      load4(src + e1, y);
-    } else {
-      x[0] = (float)src[e0];
-      y[0] = single ? 0.0f : (float)src[e1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = (float)rx[i];
+      y[i] = single ? 0.0f : (float)ry[i];
     }
-    if (turns && !is_v) {
-      float u[N], w[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        // neighbours: the loaded values alternate between first and second of a pair
-        float px, py;
-        if (VEC && a.interleaved) {
-          px = i < 2 ? x[2 * i % N] : y[(2 * i) % N];
-          py = i < 2 ? x[(2 * i + 1) % N] : y[(2 * i + 1) % N];
-        } else {
-          px = x[i];
-          py = y[i];
-        }
-        u[i] = px * cs[i] - py * sn[i];
-        w[i] = px * sn[i] + py * cs[i];
-      }
-      if (VEC && a.interleaved) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float f = i % 2 ? w[i / 2] : u[i / 2];
-          const float g = i % 2 ? w[(N + i) / 2 % N] : u[(N + i) / 2 % N];
-          x[i] = f;
-          y[i] = g;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          x[i] = u[i];
-          y[i] = w[i];
-        }
-      }
-    }
+    load(h + a.heads_at_once);  // ahead of this head's stores
+    if (turns && !is_v) turn<N>(x, y, sn, cs, N > 1 && a.interleaved);
     if (is_q) {
-      LOW* dst = (LOW*)a.q_out + t * a.ot + hh * a.oh;
+      LOW* dst = (LOW*)a.q_out + t * a.ot + h * a.oh;
       if (p < 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = y[i] = 0.0f;
       }
-      if constexpr (VEC) {
-        store4(dst + e0, x);
-        store4(dst + e1, y);
-      } else {
-        store1(dst + e0, x[0]);
-        if (!single) store1(dst + e1, y[0]);
-      }
-    } else {
+      put<N>(dst + e0, x);
+      if (!single) put<N>(dst + e1, y);
+    } else if (to.cached) {
+      const int hh = is_v ? h - n_heads - n_kv : h - n_heads;
       C* dst = is_v ? (C*)a.vc + to.v + hh * a.vc_head : (C*)a.kc + to.k + hh * a.kc_head;
       if constexpr (sizeof(C) == 1) {
+        // by the reciprocal: a division per value costs more than it adds (2^-24 before a rounding
+        // to 2^-4)
         const float* scale = is_v ? a.v_scale : a.k_scale;
         if (scale) {
-          const float f = scale[hh];
+          const float f = 1.0f / scale[hh];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            x[i] = x[i] / f;
-            y[i] = y[i] / f;
+            x[i] *= f;
+            y[i] *= f;
           }
         }
       }
-      if constexpr (VEC) {
-        store4(dst + e0, x);
-        store4(dst + e1, y);
-      } else {
-        store1(dst + e0, x[0]);
-        if (!single) store1(dst + e1, y[0]);
-      }
+      put<N>(dst + e0, x);
+      if (!single) put<N>(dst + e1, y);
     }
   }
 }
 
 template <class SRC, class LOW, class C>
-int launch(const AppendArgs& a, dim3 grid, bool vec, hipStream_t s) {
-  if (vec)
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, true>), grid, dim3(kAppendThreads), 0, s, a);
+int launch(const AppendArgs& a, dim3 grid, int pairs, hipStream_t s) {
+  const dim3 blk(kAppendThreads);
+  if (pairs == 8)
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 8>), grid, blk, 0, s, a);
+  else if (pairs == 4)
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 4>), grid, blk, 0, s, a);
   else
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, false>), grid, dim3(kAppendThreads), 0, s,
-                       a);
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 1>), grid, blk, 0, s, a);
   SPAX_HIP_CHECK(hipGetLastError());
   return SPAX_OK;
 }
 
 template <class SRC>
-int launch_src(const AppendArgs& a, int out_type, bool narrow, dim3 grid, bool vec,
+int launch_src(const AppendArgs& a, int out_type, bool narrow, dim3 grid, int pairs,
                hipStream_t s) {
   if (out_type == SPAX_F16)
-    return narrow ? launch<SRC, f16, e4m3>(a, grid, vec, s) : launch<SRC, f16, f16>(a, grid, vec, s);
-  return narrow ? launch<SRC, bf16, e4m3>(a, grid, vec, s)
-                : launch<SRC, bf16, bf16>(a, grid, vec, s);
+    return narrow ? launch<SRC, f16, e4m3>(a, grid, pairs, s) : launch<SRC, f16, f16>(a, grid, pairs, s);
+  return narrow ? launch<SRC, bf16, e4m3>(a, grid, pairs, s)
+                : launch<SRC, bf16, bf16>(a, grid, pairs, s);
 }
 
 }  // namespace
@@ -217,13 +226,9 @@ int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
   a.interleaved = p->interleaved != 0;
   a.n_seqs = c.n_seqs; a.n_pages = c.n_pages; a.max_pages = c.max_pages;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
-  // Four values at a time where every row starts on four elements (the cache's always do).
-  const size_t eb = 4 * (size_t)bytes_of(p->src_type);
-  bool vec = p->rot_dim % 8 == 0 && aligned(p->k, eb) && aligned(p->v, eb) &&
-             (a.kt | a.kh | a.vt | a.vh) % 4 == 0;
-  if (p->n_heads)
-    vec = vec && aligned(p->q, eb) && aligned(p->q_out, 8) && (a.qt | a.qh | a.ot | a.oh) % 4 == 0;
-  const int items = vec ? a.dim / 8 : p->rot_dim / 2 + a.dim - p->rot_dim;
+  // 16 bytes of a 16-bit head at a time where the rotated part divides into such pieces.
+  const int pairs = p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
+  const int items = pairs > 1 ? a.dim / (2 * pairs) : p->rot_dim / 2 + a.dim - p->rot_dim;
   a.heads_at_once = kAppendThreads / items;
   // One round of heads per workgroup while that keeps few of them: latency is then one load and
   // one store deep.  With many tokens a workgroup walks over all heads of its token.
@@ -233,9 +238,9 @@ int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
                   (unsigned)((total + a.heads_per_block - 1) / a.heads_per_block));
   const bool narrow = c.type == SPAX_E4M3;
   switch (p->src_type) {
-    case SPAX_F32: return launch_src<float>(a, p->out_type, narrow, grid, vec, s);
-    case SPAX_F16: return launch_src<f16>(a, p->out_type, narrow, grid, vec, s);
-    default: return launch_src<bf16>(a, p->out_type, narrow, grid, vec, s);
+    case SPAX_F32: return launch_src<float>(a, p->out_type, narrow, grid, pairs, s);
+    case SPAX_F16: return launch_src<f16>(a, p->out_type, narrow, grid, pairs, s);
+    default: return launch_src<bf16>(a, p->out_type, narrow, grid, pairs, s);
   }
 }
 

@@ -7,6 +7,7 @@
 // row in registers, so every value is read once and written once; the centred sum of squares
 // is a second pass over registers, with none of the cancellation of mean v^2 - mean^2.
 #include "layer_ops.h"
+#include "mask_core.h"
 
 namespace spax {
 namespace {
@@ -27,130 +28,128 @@ struct Raw {
   u32x4 a, b;
 };
 
-// Thread's item j: VEC: elements [e, e + 8), e = (j * threads + tid) * 8; otherwise element
-// (j * 8 + i) * threads + tid for i < 8.
-template <bool VEC>
+// Thread's item j: elements [e, e + 8), e = (j * threads + tid) * 8.  Rows need not start on
+// eight elements: the hardware reads 16 bytes from any address (of an element here).
+__device__ inline int first_of(int j) { return (j * (int)blockDim.x + (int)threadIdx.x) * 8; }
+
 __device__ inline void load_raw(const void* row, int type, int d, int j, Raw& w) {
-  w.a = w.b = u32x4{0u, 0u, 0u, 0u};
-  const int nt = blockDim.x;
-  if constexpr (VEC) {
-    const int e = (j * nt + threadIdx.x) * 8;
-    if (e + 8 <= d) {
-      if (type == SPAX_F32) {
-        w.a = *reinterpret_cast<const u32x4*>((const float*)row + e);
-        w.b = *reinterpret_cast<const u32x4*>((const float*)row + e + 4);
-      } else {
-        w.a = *reinterpret_cast<const u32x4*>((const uint16_t*)row + e);
-      }
-    } else if (e < d) {
-      for (int i = 0; i < d - e; ++i) {
-        if (type == SPAX_F32) {
-          const uint32_t u = ((const uint32_t*)row)[e + i];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (i == x) w.a[x] = u;
-            if (i == x + 4) w.b[x] = u;
-          }
-        } else {
-          const uint32_t u = (uint32_t)((const uint16_t*)row)[e + i] << (16 * (i & 1));
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (i / 2 == x) w.a[x] |= u;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = (j * 8 + i) * nt + (int)threadIdx.x;
-      if (e < d) {
-        if (type == SPAX_F32) {
-          const uint32_t u = ((const uint32_t*)row)[e];
-          if (i < 4) w.a[i % 4] = u; else w.b[i % 4] = u;
-        } else {
-          w.a[i / 2] |= (uint32_t)((const uint16_t*)row)[e] << (16 * (i & 1));
-        }
-      }
-    }
-  }
-}
-
-__device__ inline void unpack(const Raw& w, int type, float v[8]) {
-  if (type == SPAX_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __builtin_bit_cast(float, (uint32_t)w.a[i]);
-      v[4 + i] = __builtin_bit_cast(float, (uint32_t)w.b[i]);
-    }
-  } else if (type == SPAX_F16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f16x2 h = __builtin_bit_cast(f16x2, (uint32_t)w.a[i]);
-      v[2 * i] = (float)h.x;
-      v[2 * i + 1] = (float)h.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __builtin_bit_cast(float, (uint32_t)w.a[i] << 16);
-      v[2 * i + 1] = __builtin_bit_cast(float, (uint32_t)w.a[i] & 0xffff0000u);
-    }
-  }
-}
-
-template <class T, bool VEC>
-__device__ inline void store8(T* row, int d, int j, const float v[8]) {
-  const int nt = blockDim.x;
-  if constexpr (VEC) {
-    const int e = (j * nt + threadIdx.x) * 8;
-    if (e + 8 <= d) {
-      typedef T T8 __attribute__((ext_vector_type(8)));
-      T8 x;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
-      *reinterpret_cast<T8*>(row + e) = x;
+  const int e = first_of(j);
+  if (e + 8 <= d) {
+    if (type == SPAX_F32) {
+      w.a = load_any<u32x4>((const float*)row + e);
+      w.b = load_any<u32x4>((const float*)row + e + 4);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e + i < d) row[e + i] = (T)v[i];
+      w.a = load_any<u32x4>((const uint16_t*)row + e);
     }
-  } else {
+  } else if (e < d) {
+    // one value per dword, past the end the last one again: nothing here waits for a load
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = (j * 8 + i) * nt + (int)threadIdx.x;
-      if (e < d) row[e] = (T)v[i];
+    for (int i = 0; i < 7; ++i) {
+      const int k = e + i < d ? e + i : d - 1;
+      const uint32_t u =
+          type == SPAX_F32 ? ((const uint32_t*)row)[k] : (uint32_t)((const uint16_t*)row)[k];
+      if (i < 4) w.a[i % 4] = u; else w.b[i % 4] = u;
     }
   }
 }
 
-template <bool VEC>
+__device__ inline float from_bits(uint32_t u, int type) {
+  if (type == SPAX_F32) return __builtin_bit_cast(float, u);
+  if (type == SPAX_F16) return (float)__builtin_bit_cast(f16, (uint16_t)u);
+  return __builtin_bit_cast(float, u << 16);
+}
+
+// Item j's values as loaded by load_raw; zeros past the end.
+__device__ inline void unpack(const Raw& w, int type, int d, int j, float v[8]) {
+  const int n = d - first_of(j);
+  if (n < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = i < n && i < 7 ? from_bits(i < 4 ? w.a[i % 4] : w.b[i % 4], type) : 0.0f;
+  } else if (type == SPAX_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = from_bits(w.a[i], SPAX_F32);
+      v[4 + i] = from_bits(w.b[i], SPAX_F32);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (type == SPAX_F16) {
+        v[2 * i] = from_bits(w.a[i] & 0xffffu, SPAX_F16);
+        v[2 * i + 1] = from_bits(w.a[i] >> 16, SPAX_F16);
+      } else {
+        v[2 * i] = from_bits(w.a[i], SPAX_BF16);
+        v[2 * i + 1] = __builtin_bit_cast(float, (uint32_t)w.a[i] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+template <class T>
+__device__ inline void store8(T* row, int d, int j, const float v[8]) {
+  const int e = first_of(j);
+  if (e + 8 <= d) {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    T8 x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
+    store_any(row + e, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (e + i < d) row[e + i] = (T)v[i];
+  }
+}
+
 __device__ inline void store_row(void* p, int type, int64_t at, int d, int j, const float v[8]) {
-  if (type == SPAX_F32) store8<float, VEC>((float*)p + at, d, j, v);
-  else if (type == SPAX_F16) store8<f16, VEC>((f16*)p + at, d, j, v);
-  else store8<bf16, VEC>((bf16*)p + at, d, j, v);
+  if (type == SPAX_F32) store8<float>((float*)p + at, d, j, v);
+  else if (type == SPAX_F16) store8<f16>((f16*)p + at, d, j, v);
+  else store8<bf16>((bf16*)p + at, d, j, v);
 }
 
 __device__ inline const void* row_at(const void* p, int type, int64_t at) {
   return (const uint8_t*)p + at * (type == SPAX_F32 ? 4 : 2);
 }
 
-// Sum over the workgroup, the same bits in every thread.  slot: LDS of one float per wave, not
-// in use by an earlier sum of this row.
+// Sum over the lanes of a wave, in every lane (row shifts, then row broadcasts, as for a scan).
+__device__ inline float wave_sum(float v) {
+#define SPAX_STEP(ctrl, rows)                                                                  \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),    \
+                                                             ctrl, rows, 0xF, false))
+  SPAX_STEP(0x111, 0xF);
+  SPAX_STEP(0x112, 0xF);
+  SPAX_STEP(0x114, 0xF);
+  SPAX_STEP(0x118, 0xF);
+  SPAX_STEP(0x142, 0xA);
+  SPAX_STEP(0x143, 0xC);
+#undef SPAX_STEP
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Sum over the workgroup, the same bits in every thread.  slot: 16 floats of LDS that no wave may
+// still be reading.  The barrier orders LDS only, so loads stay in flight.
 __device__ inline float sum_all(float v, float* slot) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  const int waves = blockDim.x >> 6;
-  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < waves; ++w) s += slot[w];
-  return s;
+  v = wave_sum(v);
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+  if (lane == 0) slot[threadIdx.x >> 6] = v;
+  mask::lds_barrier();
+  // every row of 16 lanes adds up the waves' sums
+  v = (lane & 15) < waves ? slot[lane & 15] : 0.0f;
+#define SPAX_TURN(by)                                                                          \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),    \
+                                                             0x120 + by, 0xF, 0xF, false))
+  SPAX_TURN(8);
+  SPAX_TURN(4);
+  SPAX_TURN(2);
+  SPAX_TURN(1);
+#undef SPAX_TURN
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
 }
 
 // v <- norm(v) without weight; elements past d are 0 and stay out of the sums.
-template <int NV, bool VEC>
+template <int NV>
 __device__ inline void normalise(float (*v)[8], const NormArgs& a, float* slot) {
-  const int nt = blockDim.x;
   if (a.layer) {
     float s = 0.0f;
 #pragma unroll
@@ -161,10 +160,7 @@ __device__ inline void normalise(float (*v)[8], const NormArgs& a, float* slot) 
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = VEC ? (j * nt + (int)threadIdx.x) * 8 + i : (j * 8 + i) * nt + (int)threadIdx.x;
-        v[j][i] = e < a.d ? v[j][i] - mean : 0.0f;
-      }
+      for (int i = 0; i < 8; ++i) v[j][i] = first_of(j) + i < a.d ? v[j][i] - mean : 0.0f;
   }
   float s = 0.0f;
 #pragma unroll
@@ -178,96 +174,94 @@ __device__ inline void normalise(float (*v)[8], const NormArgs& a, float* slot) 
     for (int i = 0; i < 8; ++i) v[j][i] *= f;
 }
 
-template <int NV, bool VEC>
-__device__ inline void weigh(float (*v)[8], const Raw* w, const Raw* b, bool has_w, bool has_b) {
+// v <- v * weight + bias; w and b hold them (EARLY) or are loaded here, an item at a time.
+template <int NV, bool EARLY>
+__device__ inline void weigh(float (*v)[8], const NormArgs& a, const float* weight,
+                             const float* bias, Raw* w, Raw* b) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (has_w) {
-      float x[8];
-      unpack(w[j], SPAX_F32, x);
+    const int k = EARLY ? j : 0;
+    if (!EARLY && weight) load_raw(weight, SPAX_F32, a.d, j, w[k]);
+    if (!EARLY && bias) load_raw(bias, SPAX_F32, a.d, j, b[k]);
+    float x[8];
+    if (weight) {
+      unpack(w[k], SPAX_F32, a.d, j, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= x[i];
     }
-    if (has_b) {
-      float x[8];
-      unpack(b[j], SPAX_F32, x);
+    if (bias) {
+      unpack(b[k], SPAX_F32, a.d, j, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] += x[i];
     }
   }
 }
 
-template <int NV, bool VEC>
-__global__ void residual_norm_kernel(NormArgs a) {
-  __shared__ float slots[64];  // 16 waves x (post, pre) x (mean, square)
+__device__ inline void load_block(const NormArgs& a, int64_t row, int j, Raw& b) {
+  if (a.block) load_raw(row_at(a.block, a.b_type, row * a.b_stride), a.b_type, a.d, j, b);
+}
+__device__ inline void load_stream(const NormArgs& a, int64_t row, int j, Raw& r, Raw& g) {
+  if (a.residual) load_raw(row_at(a.residual, a.r_type, row * a.r_stride), a.r_type, a.d, j, r);
+  if (a.gate)
+    load_raw(row_at(a.gate, a.g_type, row * a.g_stride), a.g_type, a.d, j, g);
+}
+
+// One row per workgroup, NV items per thread.  Up to two items everything a row needs is loaded at
+// once; wider rows (128 registers for each of 1024 threads) load residual, gate and weights when
+// they are used.
+template <int NV, int T>
+__global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a) {
+  constexpr bool EARLY = NV <= 2;
+  __shared__ float slots[64];  // (post, pre) x (mean, square) x 16 waves
+  Raw rb[NV], rr[NV], rg[NV], w[NV], b[NV];
   const int64_t row = blockIdx.x;
-  Raw rb[NV], rr[NV], rg[NV], rw[NV], rc[NV];
-  float v[NV][8];
-  const void* pb = a.block ? row_at(a.block, a.b_type, row * a.b_stride) : nullptr;
-  const void* pr = a.residual ? row_at(a.residual, a.r_type, row * a.r_stride) : nullptr;
-  const void* pg = a.gate ? row_at(a.gate, a.g_type, row * a.g_stride) : nullptr;
+  const auto load_weights = [&](const float* weight, const float* bias) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (pb) load_raw<VEC>(pb, a.b_type, a.d, j, rb[j]);
-    if (pr) load_raw<VEC>(pr, a.r_type, a.d, j, rr[j]);
-    if (pg) load_raw<VEC>(pg, a.g_type, a.d, j, rg[j]);
-    if (a.post_w) load_raw<VEC>(a.post_w, SPAX_F32, a.d, j, rw[j]);
-    if (a.post_b) load_raw<VEC>(a.post_b, SPAX_F32, a.d, j, rc[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (pb) {
-      unpack(rb[j], a.b_type, v[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+    for (int j = 0; j < NV; ++j) {
+      if (weight) load_raw(weight, SPAX_F32, a.d, j, w[j]);
+      if (bias) load_raw(bias, SPAX_F32, a.d, j, b[j]);
     }
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_block(a, row, j, rb[j]);
+  if (EARLY) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_stream(a, row, j, rr[j], rg[j]);
+    load_weights(a.post_w, a.post_b);
   }
-  if (a.post_w && pb) {
-    normalise<NV, VEC>(v, a, slots);
-    weigh<NV, VEC>(v, rw, rc, true, a.post_b != nullptr);
-  }
+  float v[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (a.pre_w) load_raw<VEC>(a.pre_w, SPAX_F32, a.d, j, rw[j]);
-    if (a.pre_b) load_raw<VEC>(a.pre_b, SPAX_F32, a.d, j, rc[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+    if (a.block) unpack(rb[j], a.b_type, a.d, j, v[j]);
   }
+  if (a.post_w && a.block) {
+    normalise<NV>(v, a, slots);
+    weigh<NV, EARLY>(v, a, a.post_w, a.post_b, w, b);
+  }
+  if (EARLY) load_weights(a.pre_w, a.pre_b);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (pg) {
-      float x[8];
-      unpack(rg[j], a.g_type, x);
+    if (!EARLY) load_stream(a, row, j, rr[0], rg[0]);
+    float x[8];
+    if (a.gate) {
+      unpack(rg[EARLY ? j : 0], a.g_type, a.d, j, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= x[i];
     }
-    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (pr) unpack(rr[j], a.r_type, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    if (a.residual) unpack(rr[EARLY ? j : 0], a.r_type, a.d, j, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[j][i] = x[i] + a.scale * v[j][i];
-    if (a.residual_out)
-      store_row<VEC>(a.residual_out, a.r_type, row * a.ro_stride, a.d, j, v[j]);
+    if (a.residual_out) store_row(a.residual_out, a.r_type, row * a.ro_stride, a.d, j, v[j]);
   }
   if (!a.x) return;
-  normalise<NV, VEC>(v, a, slots + 32);
-  weigh<NV, VEC>(v, rw, rc, a.pre_w != nullptr, a.pre_b != nullptr);
+  normalise<NV>(v, a, slots + 32);
+  weigh<NV, EARLY>(v, a, a.pre_w, a.pre_b, w, b);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) store_row<VEC>(a.x, a.x_type, row * a.x_stride, a.d, j, v[j]);
-}
-
-template <int NV>
-int launch(const NormArgs& a, bool vec, unsigned rows, unsigned threads, hipStream_t s) {
-  if (vec)
-    hipLaunchKernelGGL((residual_norm_kernel<NV, true>), dim3(rows), dim3(threads), 0, s, a);
-  else
-    hipLaunchKernelGGL((residual_norm_kernel<NV, false>), dim3(rows), dim3(threads), 0, s, a);
-  SPAX_HIP_CHECK(hipGetLastError());
-  return SPAX_OK;
-}
-
-// A row can be read eight values at a time if every row of the buffer starts on eight.
-bool wide(const void* p, int type, int64_t stride) {
-  return !p || (aligned(p, 8 * (size_t)bytes_of(type) > 16 ? 16 : 8 * (size_t)bytes_of(type)) &&
-                stride % 8 == 0);
+  for (int j = 0; j < NV; ++j) store_row(a.x, a.x_type, row * a.x_stride, a.d, j, v[j]);
 }
 
 }  // namespace
@@ -284,20 +278,18 @@ int launch_residual_norm(const spax_residual_norm_args* p, hipStream_t s) {
   a.r_type = p->residual_type; a.b_type = p->block_type; a.g_type = p->gate_type;
   a.x_type = p->x_type; a.layer = p->kind == SPAX_NORM_LAYER; a.d = p->d;
   a.scale = p->scale; a.eps = p->eps; a.inv_d = 1.0f / (float)p->d;
-  const bool vec = wide(a.residual, a.r_type, a.r_stride) && wide(a.block, a.b_type, a.b_stride) &&
-                   wide(a.gate, a.g_type, a.g_stride) &&
-                   wide(a.residual_out, a.r_type, a.ro_stride) &&
-                   wide(a.x, a.x_type, a.x_stride) && wide(a.post_w, SPAX_F32, 0) &&
-                   wide(a.post_b, SPAX_F32, 0) && wide(a.pre_w, SPAX_F32, 0) &&
-                   wide(a.pre_b, SPAX_F32, 0);
   const int items = (p->d + 7) / 8;
   const int nv = items <= 1024 ? 1 : items <= 2048 ? 2 : 4;
   const unsigned threads = (unsigned)(((items + nv - 1) / nv + 63) / 64 * 64);
-  switch (nv) {
-    case 1: return launch<1>(a, vec, (unsigned)p->n_rows, threads, s);
-    case 2: return launch<2>(a, vec, (unsigned)p->n_rows, threads, s);
-    default: return launch<4>(a, vec, (unsigned)p->n_rows, threads, s);
-  }
+  const dim3 grid((unsigned)p->n_rows), block(threads);
+  if (nv == 1)
+    hipLaunchKernelGGL((residual_norm_kernel<1, 1024>), grid, block, 0, s, a);
+  else if (nv == 2)
+    hipLaunchKernelGGL((residual_norm_kernel<2, 1024>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((residual_norm_kernel<4, 1024>), grid, block, 0, s, a);
+  SPAX_HIP_CHECK(hipGetLastError());
+  return SPAX_OK;
 }
 
 }  // namespace spax
