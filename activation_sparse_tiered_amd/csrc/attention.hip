@@ -31,9 +31,12 @@ constexpr int tile_keys(bool narrow, int dim) { return (narrow ? dim / 2 : dim) 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kJoinThreads = 256;
-constexpr int kWaves = 8;        // per workgroup: two per SIMD leave a wave 256 registers
+// Waves per workgroup: two per SIMD leave a wave 256 registers, one leaves 512, which the widest
+// 16-bit heads need (32 keys and values of 192 dims and the sums are 200).
+constexpr int waves_of(bool narrow, int dim) { return !narrow && dim >= 192 ? 4 : 8; }
 constexpr int kMaxShares = 256;
 constexpr int kSeqCost = 4;      // what a sequence costs besides its keys, in tiles
+constexpr int kAlone = 4;        // tiles that a wave takes by itself rather than a workgroup
 
 struct AttnArgs {
   const void *q, *k, *v;
@@ -263,6 +266,20 @@ struct Wave {
     }
   }
 
+  // o * f as this head's result.  A lane has dims (4 g + i) n0 + t of the first block of 16 n0
+  // and, after o[n0 - 1], (4 g + i) n1 + t of the second.
+  __device__ inline void put(T* out, int g, float f) const {
+    constexpr int n0 = VDims<D>::n0, n1 = VDims<D>::n1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[VN];
+#pragma unroll
+      for (int t = 0; t < VN; ++t) x[t] = f == 0.0f ? 0.0f : o[t][i] * f;
+      store_n<n0>(out + (4 * g + i) * n0, x);
+      if constexpr (n1 > 0) store_n<n1>(out + 16 * n0 + (4 * g + i) * n1, x + n0);
+    }
+  }
+
   // The softmax step and the product with the tile's values.
   __device__ inline void take(Tile& x, const Source& src, int lane, float p[4 * KH]) {
     if (!x.whole) mask_out(x, src, lane, p);
@@ -342,9 +359,10 @@ __device__ inline Keys keys_of(const AttnArgs& a, int n) {
 // The sequences laid end to end, each as kSeqCost units and then one per tile, cut into a.shares
 // equal shares (the units fit 31 bits).  Every wave finds its place by itself: lane l holds
 // sequence base + l, and a scan over the lanes gives where each ends.
-template <int TILE>
+template <int TILE, int WAVES>
 struct Line {
   int base, len;     // this lane's sequence: base + lane
+  int units;         // its kSeqCost + tiles (0 past the last sequence)
   int upto;          // units of the sequences before base + lane + 1
   int last;          // upto of lane 63
   int total, share;  // units in all and per share
@@ -353,7 +371,7 @@ struct Line {
     base = from;
     const int s = base + lane;
     len = s < a.n_seqs ? a.lens[s] : 0;
-    const int units = s < a.n_seqs ? kSeqCost + keys_of<TILE>(a, len).tiles : 0;
+    units = s < a.n_seqs ? kSeqCost + keys_of<TILE>(a, len).tiles : 0;
     upto = before + mask::wave_scan(units);
     last = __builtin_amdgcn_readlane(upto, 63);
   }
@@ -372,15 +390,27 @@ struct Line {
     while (x >= last) load(a, lane, base + 64, last);
     return __builtin_ctzll(__ballot(upto > x));
   }
+  __device__ inline int share_of(int x) const { return (int)((uint32_t)x / (uint32_t)share); }
+  // How many sequences from lane `who` on (at most one per wave) are short and lie in [at, stop).
+  __device__ inline int short_run(int who, int at, int stop) const {
+    const uint64_t fits = __ballot(units > 0 && units <= kSeqCost + kAlone && upto <= stop &&
+                                   upto - units >= at);
+    const uint64_t rest = ~(fits >> who);
+    const int n = rest ? __builtin_ctzll(rest) : 64;
+    return n < WAVES ? n : WAVES;
+  }
   // Of the sequence in lane `who`.
   __device__ inline int length(int who) const { return __builtin_amdgcn_readlane(len, who); }
   __device__ inline int end(int who) const { return __builtin_amdgcn_readlane(upto, who); }
+  __device__ inline int begin(int who) const {  // of its tiles
+    return end(who) - __builtin_amdgcn_readlane(units, who) + kSeqCost;
+  }
 };
 
 template <class T, bool NARROW, int D>
-__global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(AttnArgs a) {
   using W = Wave<T, NARROW, D>;
-  constexpr int EB = W::EB, VN = W::VN, kTile = W::kTile;
+  constexpr int EB = W::EB, VN = W::VN, kTile = W::kTile, kWaves = waves_of(NARROW, D);
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
@@ -405,53 +435,62 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a) {
   const uint8_t* kbase = (const uint8_t*)a.k + (int64_t)EB * kvh * a.k_head;
   const uint8_t* vbase = (const uint8_t*)a.v + (int64_t)EB * kvh * a.v_head;
 
-  Line<kTile> line;
+  Line<kTile, kWaves> line;
   line.start(a, lane);
   int at = share * line.share;
   const int stop = at + line.share < line.total ? at + line.share : line.total;
-  if (at >= stop) return;
-  int who = line.find(a, lane, at);
+  int who = at < stop ? line.find(a, lane, at) : 0;
   bool again = false;
   while (at < stop) {
     if (who == 64) who = line.find(a, lane, at);
-    const int seq = line.base + who;
-    const Keys x = keys_of<kTile>(a, line.length(who));
-    const int ends = line.end(who), begins = ends - x.tiles;  // of its tiles
-    ++who;
-    const bool whole_start = at <= begins - kSeqCost;  // its first unit is in this share
+    // Short sequences that lie whole in this share go to one wave each, side by side.
+    const int run = line.short_run(who, at, stop);
+    const bool alone = run > 1;
+    if (alone && wave >= run) {
+      at = line.end(who + run - 1);
+      who += run;
+      continue;
+    }
+    const int mine = alone ? who + wave : who;
+    const int seq = line.base + mine;
+    const Keys x = keys_of<kTile>(a, line.length(mine));
+    const int ends = line.end(mine), begins = ends - x.tiles;  // of its tiles
+    const bool answers = at <= begins - kSeqCost;              // its first unit is in this share
     const int from = at > begins ? at : begins, to = ends < stop ? ends : stop;
-    at = ends;
+    who += alone ? run : 1;
+    at = line.end(who - 1);
     // a sequence of no keys is answered where it begins; otherwise only tiles make a piece
-    if (x.tiles == 0 ? !whole_start : from >= to) continue;
+    if (x.tiles == 0 ? !answers : from >= to) continue;
     const int t0 = x.first + from - begins;
     const int t1 = x.tiles ? x.first + to - begins : t0;
+    const int step = alone ? 1 : kWaves;
 
     W w;
     w.begin();
     if (r < heads) w.load_q((const uint8_t*)a.q + 2 * (seq * a.qs + (head0 + r) * a.qh), g);
     const typename W::Source src{a.table + seq * a.table_stride, kbase, vbase, a.k_page, a.k_row,
                                  a.v_page, a.v_row, a.page_shift, a.n_pages, x.lo, x.hi, to_log2};
-    int tile = t0 + wave;
+    int tile = alone ? t0 : t0 + wave;
     if (tile < t1) {
       // The next tile's keys are loaded once this one's are used, its values likewise, so loads
       // are in flight through all of the arithmetic.  Its table entry was loaded ahead of this
       // tile, so it never waits behind one.
       typename W::Tile z;
       W::place(z, src, tile, src.look_up(tile, lane), lane);
-      int next = src.look_up(tile + kWaves, lane);
+      int next = src.look_up(tile + step, lane);
       W::load_keys(z, src, lane);
       W::load_values(z, src, lane);
       for (;;) {
         float p[4 * W::KH];
         w.score(z, src, p);
-        tile += kWaves;
+        tile += step;
         if (tile >= t1) {
           w.take(z, src, lane, p);
           break;
         }
         typename W::Tile after;  // its k and v are z's registers
         W::place(after, src, tile, next, lane);
-        next = src.look_up(tile + kWaves, lane);
+        next = src.look_up(tile + step, lane);
         W::load_keys(after, src, lane);
         w.take(z, src, lane, p);
         W::load_values(after, src, lane);
@@ -459,12 +498,23 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a) {
       }
     }
 
+    w.l += __shfl_xor(w.l, 16);
+    w.l += __shfl_xor(w.l, 32);
+    if (alone) {
+      if (r < heads) {
+        T* out = (T*)a.out + seq * a.os + (head0 + r) * a.oh;
+        w.put(out, g, w.l == 0.0f ? 0.0f : v_mul / w.l);
+        if (a.lse && g == 0)
+          a.lse[(int64_t)seq * a.n_heads + head0 + r] =
+              w.l == 0.0f ? -INFINITY : (w.m + log2f(w.l)) * kLn2;
+      }
+      continue;
+    }
+
     // Join the waves: m and l through LDS, then o of a.lds_waves waves at a time, a block of dims
     // at a time, each wave's scaled to the common maximum before it is stored.
     if (again) __syncthreads();  // the last piece's are still being read
     again = true;
-    w.l += __shfl_xor(w.l, 16);
-    w.l += __shfl_xor(w.l, 32);
     constexpr int n0 = VDims<D>::n0, n1 = VDims<D>::n1;
     constexpr int kStride = 16 * n0 + 4;  // n1 <= n0
     constexpr int kPer = (16 * 4 * n0 + 64 * kWaves - 1) / (64 * kWaves);  // four-value items per thread
@@ -550,70 +600,63 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttnArgs a) {
 // the sequence's first cut works.  A share writes at most two pieces of a head: the end of a
 // sequence (0) and the beginning of another (1).
 template <class T, bool NARROW, int D>
-__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
-  constexpr int kTile = tile_keys(NARROW, D);
+__global__ __launch_bounds__(kJoinThreads, 8) void attention_join_kernel(AttnArgs a) {
   constexpr int kLanes = D / 4;                     // threads per piece
   constexpr int kAtOnce = kJoinThreads / kLanes;    // pieces per round
-  constexpr int kUnroll = 4;
+  constexpr int kFirst = 4;                         // rounds loaded before the weights are known
   __shared__ float lds_o[kAtOnce][D];
   __shared__ float lds_w[kMaxShares];
   const int head = blockIdx.x % a.n_heads, cut = blockIdx.x / a.n_heads + 1;
   const int tid = threadIdx.x, lane = tid & 63;
-  Line<kTile> line;
+  Line<tile_keys(NARROW, D), waves_of(NARROW, D)> line;
   line.start(a, lane);
   const int x = cut * line.share;
   if (x >= line.total) return;
   const int who = line.find(a, lane, x);
-  const int ends = line.end(who), begins = ends - keys_of<kTile>(a, line.length(who)).tiles;
-  if (x <= begins) return;
-  const int s0 = (int)((uint32_t)begins / (uint32_t)line.share);
-  if (s0 != cut - 1) return;
-  const int pieces = (int)((uint32_t)(ends - 1) / (uint32_t)line.share) - s0 + 1;
-  const int seq = line.base + who;
+  const int ends = line.end(who), begins = line.begin(who);
+  if (x <= begins || line.share_of(begins) != cut - 1) return;
+  const int pieces = line.share_of(ends - 1) - cut + 2, seq = line.base + who;
 
-  // piece c of this head: the beginning from share s0, the rest from the shares after it
-  const int64_t base = 2 * ((int64_t)head * a.shares + s0);
+  // piece c of this head: the beginning from the share before the cut, the rest from there on
+  const int64_t base = 2 * ((int64_t)head * a.shares + cut - 1);
   const auto place = [&](int c) { return base + (c ? 2 * c : 1); };
   const int part = tid / kLanes, d = 4 * (tid % kLanes);
-  // every wave: the common maximum and the weights' sum (at most kMaxShares pieces)
-  float m = -INFINITY, l = 0.0f;
-  float pm[kMaxShares / 64], pl[kMaxShares / 64];
+  // every wave: the common maximum, the weights and their sum, 64 pieces at a time
+  const float* ml = a.part_ml;
+  const bool has = lane < pieces;
+  const float m0 = has ? ml[2 * place(lane)] : -INFINITY;
+  const float l0 = has ? ml[2 * place(lane) + 1] : 0.0f;
+  const float* p = a.part_o + d;
+  f32x4 o[kFirst];
 #pragma unroll
-  for (int y = 0; y < kMaxShares / 64; ++y) {
-    const int c = lane + 64 * y;
-    pm[y] = -INFINITY;
-    pl[y] = 0.0f;
-    if (c < pieces) {
-      pm[y] = a.part_ml[2 * place(c)];
-      pl[y] = a.part_ml[2 * place(c) + 1];
-    }
-    m = fmaxf(m, pm[y]);
+  for (int y = 0; y < kFirst; ++y) {
+    const int c = part + y * kAtOnce;
+    if (part < kAtOnce && c < pieces) o[y] = *reinterpret_cast<const f32x4*>(p + place(c) * D);
   }
+  float m = m0;
+  for (int c = lane + 64; c < pieces; c += 64) m = fmaxf(m, ml[2 * place(c)]);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  for (int z = 32; z > 0; z >>= 1) m = fmaxf(m, __shfl_xor(m, z));
   const float top = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-  for (int y = 0; y < kMaxShares / 64; ++y) {
-    const float f = __builtin_amdgcn_exp2f(pm[y] - top);
-    l += f * pl[y];
-    if (tid < 64) lds_w[lane + 64 * y] = f;
+  const float f0 = __builtin_amdgcn_exp2f(m0 - top);
+  float l = f0 * l0;
+  if (tid < 64) lds_w[lane] = f0;
+  for (int c = lane + 64; c < pieces; c += 64) {
+    const float f = __builtin_amdgcn_exp2f(ml[2 * place(c)] - top);
+    l += f * ml[2 * place(c) + 1];
+    if (tid < 64) lds_w[c] = f;
   }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-  __syncthreads();
+  for (int z = 32; z > 0; z >>= 1) l += __shfl_xor(l, z);
+  mask::lds_barrier();
   if (part < kAtOnce) {
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float* p = a.part_o + d;
-    int c = part;
-    for (; c + (kUnroll - 1) * kAtOnce < pieces; c += kUnroll * kAtOnce) {
-      f32x4 o[kUnroll];
 #pragma unroll
-      for (int y = 0; y < kUnroll; ++y)
-        o[y] = *reinterpret_cast<const f32x4*>(p + place(c + y * kAtOnce) * D);
-#pragma unroll
-      for (int y = 0; y < kUnroll; ++y) sum += o[y] * lds_w[c + y * kAtOnce];
+    for (int y = 0; y < kFirst; ++y) {
+      const int c = part + y * kAtOnce;
+      if (c < pieces) sum += o[y] * lds_w[c];
     }
-    for (; c < pieces; c += kAtOnce)
+    for (int c = part + kFirst * kAtOnce; c < pieces; c += kAtOnce)
       sum += *reinterpret_cast<const f32x4*>(p + place(c) * D) * lds_w[c];
     *reinterpret_cast<f32x4*>(&lds_o[part][d]) = sum;
   }
@@ -633,6 +676,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
 
 template <class T, bool NARROW, int D>
 void start(AttnArgs a, hipStream_t s) {
+  constexpr int kWaves = waves_of(NARROW, D);
   const int heads = a.group < 16 ? a.group : 16;
   // as many waves' o at a time as fit 60 KB of LDS
   const size_t per = sizeof(float) * (size_t)heads * (16 * VDims<D>::n0 + 4);
@@ -674,17 +718,19 @@ AttentionPlan attention_plan(const spax_attention_args* a) {
   AttentionPlan p{};
   const int group = a->n_heads / c.n_kv_heads;
   p.head_tiles = (group + 15) / 16;
-  const int tile = tile_keys(c.type == SPAX_E4M3, c.head_dim);
+  const bool narrow = c.type == SPAX_E4M3;
+  const int tile = tile_keys(narrow, c.head_dim), waves = waves_of(narrow, c.head_dim);
   int64_t tiles = ((int64_t)a->max_len + tile - 1) / tile;
   if (a->window > 0) {
     const int64_t w = ((int64_t)a->window + tile - 1) / tile + 1;  // a window starts anywhere
     if (w < tiles) tiles = w;
   }
-  // One workgroup per compute unit (of 256), and at least four tiles a wave, below which a second
-  // launch to join the pieces costs more than it saves.
-  const int64_t items = (int64_t)c.n_kv_heads * p.head_tiles;
-  const int64_t most = (c.n_seqs * tiles + 4 * kWaves - 1) / (4 * kWaves);
-  int64_t shares = 256 / items;
+  // Joining the pieces is a second launch, about three steps of a wave: up to three steps for each
+  // wave of one workgroup are not shared out.  Past that one workgroup per compute unit (of
+  // 256), as long as each wave has a tile.
+  const int64_t all = c.n_seqs * tiles;
+  const int64_t most = all <= 3 * waves ? 1 : (all + waves - 1) / waves;
+  int64_t shares = 256 / ((int64_t)c.n_kv_heads * p.head_tiles);
   shares = shares > most ? most : shares;
   p.shares = (int32_t)(shares < 1 ? 1 : shares > kMaxShares ? kMaxShares : shares);
   if (p.shares > 1)
