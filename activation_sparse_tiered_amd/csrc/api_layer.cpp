@@ -170,7 +170,9 @@ int check_kv_append(const spax_kv_append_args* a, Spans* spans) {
                 c.head_dim);
   if (a->rot_dim > 0 && !a->inv_freq) return fail(SPAX_ERR_NULL, "inv_freq is required");
   const int64_t heads = (int64_t)a->n_heads + 2 * (int64_t)c.n_kv_heads;
-  if (heads > 65535) return fail(SPAX_ERR_SHAPE, "%lld heads", (long long)heads);
+  if (heads > 65535 || a->n_tokens >= 1 << 24)  // a grid holds 2^32 threads
+    return fail(SPAX_ERR_SHAPE, "%lld heads or %d tokens are too many", (long long)heads,
+                a->n_tokens);
   const size_t sb = (size_t)elem::bytes_of(a->src_type);
   if (!aligned(a->q, sb) || !aligned(a->k, sb) || !aligned(a->v, sb) || !aligned(a->q_out, 2) ||
       !aligned(a->positions, 4) || !aligned(a->seq, 4) || !aligned(a->inv_freq, 4))
@@ -237,7 +239,7 @@ int check_attention(const spax_attention_args* a, Spans* spans) {
   if ((st = check_rows2("q", n, a->q_seq_stride, a->n_heads, a->q_head_stride, d, false)) ||
       (st = check_rows2("out", n, a->out_seq_stride, a->n_heads, a->out_head_stride, d, true)))
     return st;
-  if (a->n_heads > 65535 || attention_plan(a).units > INT32_MAX)
+  if (a->n_heads > 65535 || a->max_len > (1 << 30) || attention_plan(a).units > (1 << 30))
     return fail(SPAX_ERR_SHAPE, "%d heads, or %d sequences of %d keys, are too many", a->n_heads,
                 c.n_seqs, a->max_len);
   Spans b;
@@ -268,6 +270,8 @@ int check_residual_norm(const spax_residual_norm_args* a, Spans* spans) {
   if (a->n_rows < 0) return fail(SPAX_ERR_SHAPE, "n_rows %d < 0", a->n_rows);
   if (a->d < 1 || a->d > SPAX_MAX_DIN)
     return fail(SPAX_ERR_SHAPE, "d %d outside 1..%d", a->d, SPAX_MAX_DIN);
+  if ((int64_t)a->n_rows * ((a->d + 7) / 8 + 63) >= (int64_t)1 << 32)  // a grid holds 2^32 threads
+    return fail(SPAX_ERR_SHAPE, "%d rows of %d are too many", a->n_rows, a->d);
   if (!std::isfinite(a->scale) || !std::isfinite(a->eps) || a->eps < 0.0f)
     return fail(SPAX_ERR_PARAM, "scale and eps must be finite and eps >= 0");
   if ((a->post_bias && !a->post_weight) || (a->pre_bias && !a->pre_weight))
@@ -335,7 +339,7 @@ int check_glu(const spax_glu_args* a, Spans* spans) {
     return fail(SPAX_ERR_UNSUPPORTED, "act %d", a->act);
   if (a->n_rows < 0 || a->d < 1 || a->d > (1 << 30))
     return fail(SPAX_ERR_SHAPE, "n_rows %d must be >= 0 and d %d in 1..2^30", a->n_rows, a->d);
-  if ((int64_t)a->n_rows * (((int64_t)a->d + 2047) / 2048) > INT32_MAX)
+  if ((int64_t)a->n_rows * (((int64_t)a->d + 2047) / 2048) >= 1 << 24)  // workgroups of 256
     return fail(SPAX_ERR_SHAPE, "%d rows of %d are too many", a->n_rows, a->d);
   const size_t sb = (size_t)elem::bytes_of(a->src_type);
   if (!aligned(a->gate, sb) || !aligned(a->up, sb) ||

@@ -505,7 +505,7 @@ typedef struct spax_kv_cache {
  * written).  Two tokens of one call on one row: the row then holds, value by value, either
  * token's.  n_tokens 0 does nothing.
  * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (head_dim, page_size, rot_dim odd or past head_dim, a
- * size < 1, n_tokens > n_seqs without seq); SPAX_ERR_UNSUPPORTED (types); SPAX_ERR_ALIGN
+ * size < 1, n_tokens > n_seqs without seq or 2^24 and more); SPAX_ERR_UNSUPPORTED (types); SPAX_ERR_ALIGN
  * (a pointer not aligned to its element, the cache as above); SPAX_ERR_PARAM (strides that
  * overlap, outputs that overlap); SPAX_ERR_HIP.
  */
@@ -541,7 +541,8 @@ int spax_kv_append(const spax_kv_append_args* a, hipStream_t stream);
  *   ws      : spax_attention_workspace_bytes(a) bytes (0: none needed), 256-byte aligned, any
  *             contents; calls that may run at the same time need a workspace each.
  * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (as for the cache; n_heads not a multiple of
- * n_kv_heads; max_len < 1 or past max_pages * page_size; window < 0); SPAX_ERR_UNSUPPORTED
+ * n_kv_heads; max_len < 1, past max_pages * page_size or past 2^30; 2^30 or more tiles of 32
+ * keys in n_seqs sequences of max_len; window < 0); SPAX_ERR_UNSUPPORTED
  * (types); SPAX_ERR_ALIGN; SPAX_ERR_PARAM (scale not finite, overlapping buffers);
  * SPAX_ERR_WORKSPACE; SPAX_ERR_HIP.
  */
@@ -574,7 +575,8 @@ enum { SPAX_NORM_RMS = 0, SPAX_NORM_LAYER = 1 };
  * may be block itself likewise.  gate: gate_type, one row (gate_stride 0) or one per row.
  * Weights and biases are fp32 rows of d (weight NULL: ones for pre, no norm for post).
  *   residual, residual_out : residual_type; block : block_type (SPAX_F32, SPAX_F16, SPAX_BF16);
- *   x : x_type (the same three).  1 <= d <= 32768; n_rows 0 does nothing.
+ *   x : x_type (the same three).  1 <= d <= 32768; n_rows 0 does nothing, and 2^32 threads of
+ *   eight values (rows rounded up to 64 of them) are the most.
  * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE; SPAX_ERR_UNSUPPORTED (types, kind); SPAX_ERR_ALIGN (a
  * pointer not aligned to its element); SPAX_ERR_PARAM (scale or eps not finite, eps < 0, a
  * stride below d, a bias without its weight, overlapping buffers); SPAX_ERR_HIP.
@@ -603,8 +605,8 @@ enum { SPAX_ACT_SILU = 0, SPAX_ACT_GELU_TANH = 1 };
 
 /*
  * x = act(gate) * up, row by row (gate and up: src_type, usually the two halves of a gate|up
- * projection's row; x: x_type; types SPAX_F32, SPAX_F16, SPAX_BF16).  Any d >= 1; n_rows 0 does
- * nothing.  x may be gate or up itself (type and stride alike).
+ * projection's row; x: x_type; types SPAX_F32, SPAX_F16, SPAX_BF16).  Any d from 1 to 2^30, fewer than
+ * 2^24 pieces of 2048 values of a row; n_rows 0 does nothing.  x may be gate or up itself (type and stride alike).
  * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE; SPAX_ERR_UNSUPPORTED (types, act); SPAX_ERR_ALIGN;
  * SPAX_ERR_PARAM (a stride below d, overlapping buffers); SPAX_ERR_HIP.
  */

@@ -339,6 +339,42 @@ def test_attention(env, case, far):
     assert torch.equal(out, again)
 
 
+def _many(n, longest, seed):
+    r = np.random.default_rng(seed)
+    lens = np.exp(r.uniform(0, np.log(longest), n)).astype(int)
+    lens[r.random(n) < 0.15] = 0
+    return [int(v) for v in lens]
+
+
+@pytest.mark.parametrize("n,longest,hq,hk,dim,window,ct", [
+    (64, 700, 4, 2, 64, 0, "fp16"), (65, 700, 4, 2, 64, 0, "fp16"), (130, 300, 2, 1, 128, 0, "fp16"),
+    (200, 2000, 4, 4, 64, 50, "fp16"), (257, 90, 8, 8, 64, 0, "fp16"), (70, 900, 3, 1, 96, 0, "e4m3"),
+    (300, 40, 2, 1, 256, 0, "fp16"), (129, 1500, 2, 2, 192, 400, "fp16"), (90, 500, 34, 2, 64, 0, "fp16"),
+])
+def test_attention_many_sequences(env, n, longest, hq, hk, dim, window, ct):
+    """More sequences than a wave has lanes, of all lengths and in any order: some go to one wave
+    each, some are cut, some are empty."""
+    torch, spax, dev = env
+    for seed in range(2):
+        lens = _many(n, longest, seed * 1000 + n)
+        if seed:
+            lens = [0] * 70 + lens[70:] if n > 70 else [0] * (n - 1) + [longest]
+        q, kc, vc, table, ln, scales = _attention_inputs(env, lens, hq, hk, dim, 16, "fp16", ct,
+                                                         "heads", seed + n)
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full((n, hq), float("nan"), device=dev)
+        a = spax.make_attention(spax.make_kv_cache(kc, vc, table, *scales), q, ln, out,
+                                window=window, lse=lse)
+        need = spax.spax_attention_workspace_bytes(a)
+        print(f"[attention] {n} sequences up to {longest}, workspace {need}", flush=True)
+        spax.spax_paged_attention(a, torch.empty(max(1, need), dtype=torch.uint8, device=dev))
+        torch.cuda.synchronize()
+        ref, ref_lse, mass, reach = _attention_ref(q, kc, vc, table, ln, scales, scale=dim ** -0.5,
+                                                   window=window)
+        _check(_f64(out), ref, _attention_tol(ref, mass, reach, dim, "fp16", 300), "out")
+        assert np.array_equal(np.isfinite(_f64(lse)), np.isfinite(ref_lse))
+
+
 @pytest.mark.parametrize("n", [40, 4000])
 def test_attention_scores_at_the_edges(env, n):
     """Large scores of both signs, a negative and a zero scale, keys that are -inf, entries that

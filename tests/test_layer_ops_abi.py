@@ -109,6 +109,7 @@ APPEND_BAD = [
     (dict(k=0), N), (dict(v=0), N), (dict(positions=0), N), (dict(q=0), N), (dict(q_out=0), N),
     (dict(n_heads=0), N), (dict(inv_freq=0), N), (dict(src_type=spax.TYPE_E4M3), U),
     (dict(out_type=spax.TYPE_F32), U), (dict(out_type=spax.TYPE_BF16), U), (dict(n_tokens=-1), S),
+    (dict(n_tokens=1 << 24, seq=FAKE + 206 * MB), S), (dict(n_heads=1 << 16), S),
     (dict(n_tokens=4), S), (dict(rot_dim=130), S), (dict(rot_dim=63), S), (dict(rot_dim=-2), S),
     (dict(q=FAKE + 200 * MB + 1), A), (dict(positions=FAKE + 2), A),
     (dict(out_token_stride=512), P), (dict(q_token_stride=-8), P), (dict(k_head_stride=-1), P),
@@ -157,6 +158,17 @@ def test_attention_refusals(kw, status):
 
 
 @needs_no_gpu
+def test_attention_of_too_much():
+    huge = dict(n_pages=1, page_size=65536, max_pages=16385, table_stride=16385, k_page_stride=1 << 30,
+                k_head_stride=1 << 25, v_page_stride=1 << 30, v_head_stride=1 << 25)
+    call = _lib.lib.spax_paged_attention
+    assert call(_attention(_cache(**huge), max_len=(1 << 30) + 1), 0, 0, 0) == S
+    assert call(_attention(_cache(n_seqs=1 << 20, **huge), max_len=1 << 30), 0, 0, 0) == S
+    # one that long sequence is fine, and asks for its workspace
+    assert call(_attention(_cache(n_seqs=1, **huge), max_len=1 << 30), 0, 0, 0) == N
+
+
+@needs_no_gpu
 def test_attention_workspace():
     c = _cache(max_pages=4096, table_stride=4096)
     a = _attention(c, max_len=65536)
@@ -176,7 +188,7 @@ def test_attention_workspace():
 NORM_BAD = [
     (dict(residual=0, block=0), N), (dict(residual_out=0, x=0), N),
     (dict(residual_type=spax.TYPE_E4M3), U), (dict(x_type=9), U), (dict(block_type=3), U),
-    (dict(kind=2), U), (dict(n_rows=-1), S), (dict(d=0), S), (dict(d=32769), S),
+    (dict(kind=2), U), (dict(n_rows=1 << 30), S), (dict(n_rows=-1), S), (dict(d=0), S), (dict(d=32769), S),
     (dict(scale=float("nan")), P), (dict(eps=-1.0), P), (dict(eps=float("inf")), P),
     (dict(pre_bias=FAKE + 9 * MB), P), (dict(post_bias=FAKE + 9 * MB), P),
     (dict(block=0, gate=FAKE + 9 * MB), P), (dict(block_stride=99), P),
