@@ -725,6 +725,7 @@ AttentionPlan attention_plan(const spax_attention_args* a) {
     const int64_t w = ((int64_t)a->window + tile - 1) / tile + 1;  // a window starts anywhere
     if (w < tiles) tiles = w;
   }
+  p.units = c.n_seqs * (tiles + kSeqCost);
   // Joining the pieces is a second launch, about three steps of a wave: up to three steps for each
   // wave of one workgroup are not shared out.  Past that one workgroup per compute unit (of
   // 256), as long as each wave has a tile.
