@@ -47,7 +47,7 @@ struct AttnArgs {
   int64_t qs, qh, os, oh;
   int64_t k_page, k_head, k_row, v_page, v_head, v_row, table_stride;
   int32_t n_heads, n_kv, group, head_tiles, n_seqs, n_pages, page_shift;
-  int32_t max_len, window, shares, lds_waves;
+  int32_t max_len, window, shares, lds_waves, k_lds;
   float scale;
 };
 
@@ -116,25 +116,24 @@ struct Wave {
   f32x4 o[VN];
   float m, l;  // of head lane % 16: the running max (scaled to log2), this lane's part of the sum
 
-  // A lane's part of the K rows of 16 keys, as stored.  Which dims a lane holds for which step is
-  // free as long as Q's are the same: 16 bytes per load, so a step of 32 dims of a 16-bit row
-  // (dims 32 c + 8 g ..), or two steps of an 8-bit row (64 c + 16 g .. for steps 2c and 2c + 1;
-  // a last single step by 8 bytes).
+  // K rows are loaded whole, 16 bytes a lane, and laid out in LDS (the wave's own, rows padded by
+  // 16 bytes against bank conflicts): read straight into the first operand's layout, adjacent
+  // lanes would ask for different rows, and the address unit takes four times as long.
+  static constexpr int RB = D * EB;                    // bytes of a row
+  static constexpr int kChunks = RB / 16, kRowLds = RB + 16;
+  // Which dims a lane holds for which step is free as long as Q's are the same: 16 bytes per
+  // read, so a step of 32 dims of a 16-bit row (dims 32 c + 8 g ..), or two steps of an 8-bit row
+  // (64 c + 16 g .. for steps 2c and 2c + 1; a last single step by 8 bytes).
   static constexpr int kPairs = NARROW ? KC / 2 : 0;
-  static constexpr int KW = NARROW ? kPairs + (KC & 1) : KC;  // loads
-  static __device__ inline void load_k(const uint8_t* row, int g, u32x4 k[KW]) {
-    if constexpr (!NARROW) {
+  static constexpr int KW = NARROW ? kPairs + (KC & 1) : KC;  // reads
+  static __device__ inline void read_k(const uint8_t* row, int g, u32x4 k[KW]) {
 #pragma unroll
-      for (int c = 0; c < KC; ++c) k[c] = load16(row + 64 * c + 16 * g);
-    } else {
-#pragma unroll
-      for (int c = 0; c < kPairs; ++c) k[c] = load16(row + 64 * c + 16 * g);
-      if constexpr (KC & 1) {
-        uint32_t w[2];
-        load_words<2>(row + 64 * kPairs + 8 * g, w);
-        k[kPairs].x = w[0];
-        k[kPairs].y = w[1];
-      }
+    for (int c = 0; c < (NARROW ? kPairs : KC); ++c)
+      k[c] = *reinterpret_cast<const u32x4*>(row + 64 * c + 16 * g);
+    if constexpr (NARROW && (KC & 1)) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(row + 64 * kPairs + 8 * g);
+      k[kPairs].x = w.x;
+      k[kPairs].y = w.y;
     }
   }
   // Step c's operand.
@@ -183,9 +182,9 @@ struct Wave {
   };
   // A tile's keys and values, 16 keys per K operand and 32 per V operand.
   static constexpr int kTile = tile_keys(NARROW, D);
-  static constexpr int KH = kTile / 16, VH = kTile / 32;
+  static constexpr int KH = kTile / 16, VH = kTile / 32, KI = kTile * kChunks / 64;
   struct Tile {
-    u32x4 k[KH][KW];
+    u32x4 k[KI];  // chunk (64 i + lane) % kChunks of row (64 i + lane) / kChunks
     uint32_t v[VH][8][VW];
     int page;  // of key lane % kTile, or -1 (see place)
     int kb;
@@ -215,13 +214,14 @@ struct Wave {
     x.whole = kb >= s.lo && kb + kTile <= s.hi && __all(ok);
   }
   static __device__ inline void load_keys(Tile& x, const Source& s, int lane) {
-    const int g = lane >> 4, r = lane & 15, row_mask = (1 << s.page_shift) - 1;
+    const int row_mask = (1 << s.page_shift) - 1;
 #pragma unroll
-    for (int h = 0; h < KH; ++h) {
-      const int pg = __shfl(x.page, 16 * h + r);
-      const int64_t row = (int64_t)(pg < 0 ? 0 : pg) * s.k_page +
-                          (int64_t)((x.kb + 16 * h + r) & row_mask) * s.k_row;
-      load_k(s.k + EB * row, g, x.k[h]);
+    for (int i = 0; i < KI; ++i) {
+      const int row = (64 * i + lane) / kChunks, chunk = (64 * i + lane) % kChunks;
+      const int pg = __shfl(x.page, row);
+      const int64_t at = (int64_t)(pg < 0 ? 0 : pg) * s.k_page +
+                         (int64_t)((x.kb + row) & row_mask) * s.k_row;
+      x.k[i] = load16(s.k + EB * at + 16 * chunk);
     }
   }
   static __device__ inline void load_values(Tile& x, const Source& s, int lane) {
@@ -238,12 +238,20 @@ struct Wave {
   }
 
   // Scores of the tile's keys in base 2; a lane's are keys 16 h + 4 g + i of its head.
-  __device__ inline void score(const Tile& x, const Source& src, float p[4 * KH]) {
+  __device__ inline void score(const Tile& x, const Source& src, uint8_t* rows, int lane,
+                               float p[4 * KH]) {
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const int row = (64 * i + lane) / kChunks, chunk = (64 * i + lane) % kChunks;
+      *reinterpret_cast<u32x4*>(rows + row * kRowLds + 16 * chunk) = x.k[i];
+    }
 #pragma unroll
     for (int h = 0; h < KH; ++h) {
+      u32x4 k[KW];
+      read_k(rows + (16 * h + (lane & 15)) * kRowLds, lane >> 4, k);
       f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < KC; ++c) s = Mma<T>::mul(k_step(x.k[h], c), q[c], s);
+      for (int c = 0; c < KC; ++c) s = Mma<T>::mul(k_step(k, c), q[c], s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[4 * h + i] = s[i] * src.to_log2;
     }
@@ -435,6 +443,7 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
   const uint8_t* kbase = (const uint8_t*)a.k + (int64_t)EB * kvh * a.k_head;
   const uint8_t* vbase = (const uint8_t*)a.v + (int64_t)EB * kvh * a.v_head;
 
+  uint8_t* k_rows = reinterpret_cast<uint8_t*>(lds) + a.k_lds + wave * (kTile * W::kRowLds);
   Line<kTile, kWaves> line;
   line.start(a, lane);
   int at = share * line.share;
@@ -482,7 +491,7 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
       W::load_values(z, src, lane);
       for (;;) {
         float p[4 * W::KH];
-        w.score(z, src, p);
+        w.score(z, src, k_rows, lane, p);
         tile += step;
         if (tile >= t1) {
           w.take(z, src, lane, p);
@@ -682,7 +691,8 @@ void start(AttnArgs a, hipStream_t s) {
   const size_t per = sizeof(float) * (size_t)heads * (16 * VDims<D>::n0 + 4);
   a.lds_waves = kWaves;
   while (a.lds_waves > 1 && a.lds_waves * per > 60 * 1024) a.lds_waves /= 2;
-  const size_t lds = sizeof(float) * kWaves * 32 + a.lds_waves * per;
+  a.k_lds = (int32_t)(sizeof(float) * kWaves * 32 + a.lds_waves * per);
+  const size_t lds = a.k_lds + (size_t)kWaves * tile_keys(NARROW, D) * (D * (NARROW ? 1 : 2) + 16);
   const unsigned items = (unsigned)(a.n_kv * a.head_tiles * a.shares);
   const dim3 grid((items + 7) / 8 * 8);
   hipLaunchKernelGGL((attention_kernel<T, NARROW, D>), grid, dim3(64 * kWaves), lds, s, a);
