@@ -237,14 +237,15 @@ struct Wave {
     }
   }
 
-  // Scores of the tile's keys in base 2; a lane's are keys 16 h + 4 g + i of its head.
-  __device__ inline void score(const Tile& x, const Source& src, uint8_t* rows, int lane,
-                               float p[4 * KH]) {
+  static __device__ inline void lay_out_keys(const Tile& x, uint8_t* rows, int lane) {
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
       const int row = (64 * i + lane) / kChunks, chunk = (64 * i + lane) % kChunks;
       *reinterpret_cast<u32x4*>(rows + row * kRowLds + 16 * chunk) = x.k[i];
     }
+  }
+  // Scores of the tile's keys in base 2; a lane's are keys 16 h + 4 g + i of its head.
+  __device__ inline void score(const uint8_t* rows, const Source& src, int lane, float p[4 * KH]) {
 #pragma unroll
     for (int h = 0; h < KH; ++h) {
       u32x4 k[KW];
@@ -491,9 +492,10 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
       W::load_values(z, src, lane);
       for (;;) {
         float p[4 * W::KH];
-        w.score(z, src, k_rows, lane, p);
+        W::lay_out_keys(z, k_rows, lane);
         tile += step;
         if (tile >= t1) {
+          w.score(k_rows, src, lane, p);
           w.take(z, src, lane, p);
           break;
         }
@@ -501,6 +503,7 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
         W::place(after, src, tile, next, lane);
         next = src.look_up(tile + step, lane);
         W::load_keys(after, src, lane);
+        w.score(k_rows, src, lane, p);
         w.take(z, src, lane, p);
         W::load_values(after, src, lane);
         z = after;
