@@ -5,7 +5,14 @@
 //
 // Bound: bytes for many rows, the latency of two reductions for one.  A workgroup holds a whole
 // row in registers, so every value is read once and written once; the centred sum of squares
-// is a second pass over registers, with none of the cancellation of mean v^2 - mean^2.
+// is a second pass over registers, with none of the cancellation of mean v^2 - mean^2.  One row
+// per workgroup: walking over several rows with the weights in registers was slower (17.7 to 23 us
+// against 15.8 for 2048 rows).
+//
+// Measured: 2048 x 4096 bf16, norms before and after and a gate: 15.9 us, 67 MB, 4.2 TB/s (a large
+// copy reaches 5.1).  333 x 5003, layer norms, rows that start anywhere: 11.1 us, four sums one after
+// another; at an earlier step rows of 5000 took 9.7 and of 5003 11.4.  1 x 4096: 2.4 us on the
+// device.
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -278,8 +285,12 @@ int launch_residual_norm(const spax_residual_norm_args* p, hipStream_t s) {
   a.r_type = p->residual_type; a.b_type = p->block_type; a.g_type = p->gate_type;
   a.x_type = p->x_type; a.layer = p->kind == SPAX_NORM_LAYER; a.d = p->d;
   a.scale = p->scale; a.eps = p->eps; a.inv_d = 1.0f / (float)p->d;
+  // Items of a thread: one while 1024 threads hold the row (333 x 5003: 11.2 us, 12.5 with two);
+  // then two while a compute unit has one row (1 x 12891: 8.2 us, 10.1 with four), else four,
+  // whose fewer threads let a unit hold more rows (256 x 16384: 13.0 with two, 14.0 with four;
+  // 257: 18.4 and 15.7; 2048: 109 and 94).
   const int items = (p->d + 7) / 8;
-  const int nv = items <= 1024 ? 1 : items <= 2048 ? 2 : 4;
+  const int nv = items <= 1024 ? 1 : items <= 2048 && p->n_rows <= 256 ? 2 : 4;
   const unsigned threads = (unsigned)(((items + nv - 1) / nv + 63) / 64 * 64);
   const dim3 grid((unsigned)p->n_rows), block(threads);
   if (nv == 1)
