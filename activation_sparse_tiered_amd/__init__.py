@@ -1,7 +1,8 @@
 """Python binding of libspax: three-tier activation-sparse decoding GEMV on MI355X (gfx950).
 
 Thin argument marshalling over the C ABI in ``include/spax.h``: every step of the path
-(packing, tier masks, tiered GEMV, decode step) runs in the HIP kernels of libspax.so.
+(packing, tier masks, tiered GEMV, decode step, and the cache append, attention, norms and gated
+activation between the projections) runs in the HIP kernels of libspax.so.
 torch is used only for device memory (tensors are passed by ``data_ptr()``) and streams
 (``torch.cuda.current_stream()`` by default).  The names match the C entry points.
 """

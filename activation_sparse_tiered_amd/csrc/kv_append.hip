@@ -9,6 +9,10 @@
 // Bound: bytes (each value is read once and written once) for prompts, launch latency for one
 // token.  A thread keeps one place in the head (four pairs, or eight copied values) and walks
 // over heads; a token's sines are computed once per workgroup, a pair per thread.
+//
+// Measured: 4099 tokens of 32 + 8 + 8 heads of 128, fp16 to e4m3, 92 MB: 20 us, 4.6 TB/s (a large
+// copy reaches 5.1); one token: 3.0 us on the device, a load of the position and one of the page
+// before the stores can go.
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -226,12 +230,14 @@ int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
   a.interleaved = p->interleaved != 0;
   a.n_seqs = c.n_seqs; a.n_pages = c.n_pages; a.max_pages = c.max_pages;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
-  // 16 bytes of a 16-bit head at a time where the rotated part divides into such pieces.
+  // 16 bytes of a 16-bit head at a time where the rotated part divides into such pieces (the
+  // prompts of 4099 tokens: 20.0 us with pieces of eight pairs, 21.1 of four, 51 of one).
   const int pairs = p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
   const int items = pairs > 1 ? a.dim / (2 * pairs) : p->rot_dim / 2 + a.dim - p->rot_dim;
   a.heads_at_once = kAppendThreads / items;
-  // One round of heads per workgroup while that keeps few of them: latency is then one load and
-  // one store deep.  With many tokens a workgroup walks over all heads of its token.
+  // One round of heads per workgroup while there are few tokens: latency is then one load and one
+  // store deep.  With many a workgroup walks over all heads of its token.  128 tokens: 4.65 us by
+  // rounds, 4.9 walking; 511: equal; 1000: 8.4 and 7.5; 4099: 22.9 and 20.0.
   const int total = a.n_heads + 2 * a.n_kv;
   a.heads_per_block = p->n_tokens < 512 ? a.heads_at_once : total;
   const dim3 grid((unsigned)p->n_tokens,

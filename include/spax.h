@@ -17,6 +17,10 @@
  *
  *   y[r] = sum_{j in FULL} x[j] * W[r][j]  +  sum_{j in APPROX} x[j] * What[r][j]
  *
+ * and what stands between two such products in a decoder layer: the append to a paged key-value
+ * cache with its rotation, the attention of the new token, the residual add with its norms, and
+ * the gated activation ("between the projections" below).
+ *
  * Conventions shared by every entry point:
  *   - Return SPAX_OK (0) or a negative spax_status.  All argument validation happens on
  *     the host before anything is enqueued; on error nothing runs and no output buffer
