@@ -1,6 +1,7 @@
 // Entry points of the operators between the projections: argument validation, then launches.
 // Every check runs before anything is enqueued; on error no output is touched.
 #include <cmath>
+#include <cstring>
 #include <utility>
 
 #include "layer_ops.h"
@@ -58,7 +59,10 @@ int check_rows2(const char* name, int64_t n0, int64_t s0, int64_t n1, int64_t s1
   return SPAX_OK;
 }
 
+bool is(const Span& x, const char* name) { return strcmp(x.name, name) == 0; }
+
 // No output shares a byte with another buffer, save pairs that allowed(output, other) excuses.
+// It goes by their names: another input may start at the same address with other strides.
 template <class F>
 int check_overlaps(const Spans& b, F&& allowed) {
   for (int i = 0; i < b.n; ++i)
@@ -204,8 +208,8 @@ int check_kv_append(const spax_kv_append_args* a, Spans* spans) {
                         a->q_token_stride == a->out_token_stride &&
                         a->q_head_stride == a->out_head_stride;
   st = check_overlaps(b, [&](const Span& x, const Span& y) {
-    if (x.p == a->q_out && y.p == a->q && !y.out) return in_place;
-    return x.p == c.k && y.p == c.v && y.out && c.k != c.v;  // interleaved, see add_cache
+    if (is(x, "q_out") && is(y, "q")) return in_place;
+    return is(x, "cache k") && is(y, "cache v") && c.k != c.v;  // interleaved, see add_cache
   });
   if (st) return st;
   if (spans) *spans = b;
@@ -321,8 +325,8 @@ int check_residual_norm(const spax_residual_norm_args* a, Spans* spans) {
   const bool over = a->block && a->block == a->x && a->block_type == a->x_type &&
                     (n == 1 || a->block_stride == a->x_stride);
   const int st = check_overlaps(b, [&](const Span& x, const Span& y) {
-    return (stream && x.p == a->residual_out && y.p == a->residual && !y.out) ||
-           (over && x.p == a->x && y.p == a->block && !y.out);
+    return (stream && is(x, "residual_out") && is(y, "residual")) ||
+           (over && is(x, "x") && is(y, "block"));
   });
   if (st) return st;
   if (spans) *spans = b;
@@ -361,7 +365,7 @@ int check_glu(const spax_glu_args* a, Spans* spans) {
   const bool on_gate = same && a->x == a->gate && (n == 1 || a->x_stride == a->gate_stride);
   const bool on_up = same && a->x == a->up && (n == 1 || a->x_stride == a->up_stride);
   const int st = check_overlaps(b, [&](const Span&, const Span& y) {
-    return (y.p == a->gate && on_gate) || (y.p == a->up && on_up);
+    return is(y, "gate") ? on_gate : on_up;
   });
   if (st) return st;
   if (spans) *spans = b;

@@ -222,6 +222,31 @@ def test_glu_refusals(kw, status):
 
 
 @needs_no_gpu
+def test_an_output_in_place_of_one_input_is_refused_where_another_shares_its_address():
+    """Only the input that the output stands in for, value by value, may share its bytes: another
+    with the same first address and other strides or types is read by other threads meanwhile."""
+    q, x, r, h = FAKE + 200 * MB, FAKE + 3 * MB, FAKE + MB, FAKE
+    bad = [
+        # q rotated in place, and the keys read from the same rows
+        _lib.lib.spax_kv_append(_append(q_out=q, k=q), 0),
+        _lib.lib.spax_kv_append(_append(q_out=q, v=q), 0),
+        # x over block, whose first row gates every row
+        _lib.lib.spax_residual_norm(_norm(block=x, x=x, block_type=spax.TYPE_F16,
+                                          x_type=spax.TYPE_F16, gate=x, gate_stride=0,
+                                          gate_type=spax.TYPE_F16), 0),
+        # the stream over itself, whose first row gates every row, or whose rows are the block's
+        _lib.lib.spax_residual_norm(_norm(residual=h, residual_out=h, gate=h, gate_stride=0,
+                                          gate_type=spax.TYPE_F32), 0),
+        _lib.lib.spax_residual_norm(_norm(residual=h, residual_out=h, block=h, block_stride=200,
+                                          block_type=spax.TYPE_F32), 0),
+        # x over gate, and up the same address with rows twice as far apart
+        _lib.lib.spax_glu(_glu(gate=r, up=r, x=r, x_type=0, gate_stride=100, x_stride=100,
+                               up_stride=200), 0),
+    ]
+    assert bad == [P] * len(bad)
+
+
+@needs_no_gpu
 def test_norm_and_glu_of_nothing():
     assert _lib.lib.spax_residual_norm(_norm(n_rows=0), 0) == _lib.SPAX_OK
     assert _lib.lib.spax_glu(_glu(n_rows=0), 0) == _lib.SPAX_OK
