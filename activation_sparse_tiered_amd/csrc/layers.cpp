@@ -26,6 +26,17 @@ int part_fail(int st, int layer, const char* part) {
   return fail(st, "layer %d, %s: %s", layer, part, msg);
 }
 
+// Two descriptions find the same values of one sequence.
+bool same_cache(const spax_kv_cache& x, const spax_kv_cache& y) {
+  return x.k == y.k && x.v == y.v && x.page_table == y.page_table && x.k_scale == y.k_scale &&
+         x.v_scale == y.v_scale && x.type == y.type && x.n_pages == y.n_pages &&
+         x.page_size == y.page_size && x.n_kv_heads == y.n_kv_heads &&
+         x.head_dim == y.head_dim && x.k_page_stride == y.k_page_stride &&
+         x.k_head_stride == y.k_head_stride && x.k_row_stride == y.k_row_stride &&
+         x.v_page_stride == y.v_page_stride && x.v_head_stride == y.v_head_stride &&
+         x.v_row_stride == y.v_row_stride;
+}
+
 // The operators after each phase, with the buffers they touch.
 struct Parts {
   Spans append, attention, attn_norm, glu, mlp_norm;
@@ -63,8 +74,7 @@ int check_parts(const spax_decoder_layer& L, int i, Parts* b) {
   if ((st = wired(ok, "append", "qkv's y"))) return st;
   ok = at.q == ap.q_out && at.type == ap.out_type && at.n_heads == ap.n_heads &&
        (at.n_heads == 1 || at.q_head_stride == ap.out_head_stride) &&
-       at.cache->k == ap.cache->k && at.cache->v == ap.cache->v &&
-       at.cache->page_table == ap.cache->page_table;
+       same_cache(*at.cache, *ap.cache);
   if ((st = wired(ok, "attention", "append's q_out and cache"))) return st;
   ok = (const void*)L.o->x == at.out && at.type == SPAX_F16 &&
        (at.n_heads == 1 || at.out_head_stride == dim) &&

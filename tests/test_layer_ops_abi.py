@@ -353,6 +353,23 @@ def test_layer_refusals_of_the_whole():
     assert spax.spax_layers_workspace_bytes((spax.DecoderLayer * 1)(_layer(0, skip=("o",))[0])) == 0
 
 
+@needs_no_gpu
+@pytest.mark.parametrize("kw", [
+    dict(page_size=8), dict(n_pages=4), dict(type=spax.TYPE_E4M3), dict(v_page_stride=8192),
+    dict(k_row_stride=64, k_head_stride=1024, k_page_stride=8192)])
+def test_layer_refuses_an_attention_that_reads_the_cache_otherwise_than_it_is_written(kw):
+    layer, _ = _layer(0)
+    other = spax.KvCache.from_buffer_copy(layer._keep[1])
+    for name, v in kw.items():
+        setattr(other, name, v)
+    layer._keep[0]["attention"].cache = C.pointer(other)
+    # the attention of that description is a call of its own right
+    if kw.get("type") != spax.TYPE_E4M3:
+        layer._keep[0]["attention"].max_len = 8
+    assert _run_layers([layer]) == P, _lib.lib.spax_last_error()
+    assert b"attention is not wired" in _lib.lib.spax_last_error()
+
+
 # ------------------------------------------------------------------ tensor descriptions
 
 def _tensors(dtype=torch.float16):
