@@ -24,7 +24,7 @@
 // workgroup per compute unit.  Fixed pieces of a longest possible sequence instead left the
 // chip to the long ones (48 sequences of 0 to 8192 keys, when it was changed: 94 us to 50).
 //
-// Measured (one MI355X; plain reads reach 7.2 TB/s): 32 x 32768 keys, 8 heads of 128, e4m3: 323 us,
+// Measured (one MI355X; plain reads reach 7.2 TB/s): 32 x 32768 keys, 8 heads of 128, e4m3: 324 us,
 // 6.6 TB/s.  1 x 32768, fp16: 27.6 us, of which 24 the shares and 4.6 the join where each is timed by
 // itself; 18.6 at the read rate.  48 sequences of 0 to 8192, bf16: 41.5 us, 4.7 TB/s, with the rows
 // of a token's heads side by side, 39.5 with each head's rows together.  1 x 509 keys, 32 heads:
@@ -38,8 +38,8 @@ namespace {
 
 using namespace elem;
 
-// Keys that a wave takes per step.  64 of the narrower rows were no faster: 32 x 32768 e4m3 325 us
-// (32: 323), 1 x 2000 of dim 64 11.8 (10.8).
+// Keys that a wave takes per step.  64 of the narrower rows were no faster: 32 x 32768 e4m3 325.7 us
+// (32: 323.5), 1 x 2000 of dim 64 11.8 (10.8).
 constexpr int kTile = 32;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;

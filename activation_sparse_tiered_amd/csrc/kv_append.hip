@@ -7,11 +7,11 @@
 // turn) for sine and cosine.
 //
 // Bound: bytes (each value is read once and written once) for prompts, launch latency for one
-// token.  A thread keeps one place in the head (four pairs, or eight copied values) and walks
+// token.  A thread keeps one place in the head (up to eight pairs, or 16 copied values) and walks
 // over heads; a token's sines are computed once per workgroup, a pair per thread.
 //
-// Measured: 4099 tokens of 32 + 8 + 8 heads of 128, fp16 to e4m3, 92 MB: 20 us, 4.6 TB/s (a large
-// copy reaches 5.1); one token: 3.0 us on the device, a load of the position and one of the page
+// Measured: 4099 tokens of 32 + 8 + 8 heads of 128, fp16 to e4m3, 92 MB: 19.6 us, 4.7 TB/s (a large
+// copy reaches 5.1); one token: 2.9 us on the device, a load of the position and one of the page
 // before the stores can go.
 #include "layer_ops.h"
 #include "mask_core.h"

@@ -9,9 +9,9 @@
 // per workgroup: walking over several rows with the weights in registers was slower (17.7 to 23 us
 // against 15.8 for 2048 rows).
 //
-// Measured: 2048 x 4096 bf16, norms before and after and a gate: 15.9 us, 67 MB, 4.2 TB/s (a large
-// copy reaches 5.1).  333 x 5003, layer norms, rows that start anywhere: 11.1 us, four sums one after
-// another; at an earlier step rows of 5000 took 9.7 and of 5003 11.4.  1 x 4096: 2.4 us on the
+// Measured: 2048 x 4096 bf16, norms before and after and a gate: 15.3 us, 67 MB, 4.4 TB/s (a large
+// copy reaches 5.1).  333 x 5003, layer norms, rows that start anywhere: 11.0 us, four sums one after
+// another; at an earlier step rows of 5000 took 9.7 and of 5003 11.4.  1 x 4096: 2.6 us on the
 // device.
 #include "layer_ops.h"
 #include "mask_core.h"
