@@ -9,10 +9,9 @@
 // per workgroup: walking over several rows with the weights in registers was slower (17.7 to 23 us
 // against 15.8 for 2048 rows).
 //
-// Measured: 2048 x 4096 bf16, norms before and after and a gate: 15.3 us, 67 MB, 4.4 TB/s (a large
-// copy reaches 5.1).  333 x 5003, layer norms, rows that start anywhere: 11.0 us, four sums one after
-// another; at an earlier step rows of 5000 took 9.7 and of 5003 11.4.  1 x 4096: 2.6 us on the
-// device.
+// Measured: 2048 x 4096 bf16, norms before and after and a gate: 15.2 us, 67 MB, 4.4 TB/s (a large
+// copy reaches 5.1).  333 x 5003, layer norms, rows that start anywhere: 9.1 us, four sums one after
+// another (256 rows 6.3 us: the rest is units that have two rows).  1 x 4096: 2.6 us on the device.
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -35,28 +34,44 @@ struct Raw {
   u32x4 a, b;
 };
 
-// Thread's item j: elements [e, e + 8), e = (j * threads + tid) * 8.  Rows need not start on
-// eight elements: the hardware reads 16 bytes from any address (of an element here).
-__device__ inline int first_of(int j) { return (j * (int)blockDim.x + (int)threadIdx.x) * 8; }
+// Thread's item j: eight values from element `at`, of which those before `lo` are not its own.
+// Rows need not start on eight elements: the hardware reads 16 bytes from any address (of an
+// element here).  The last item of a row whose width is not a multiple of eight is the row's last
+// eight values, the first ones its neighbour's: those count as 0 in sums and are not stored, so it
+// does not matter if the neighbour has overwritten them.  (With its own values read one by one,
+// 333 x 5003 took 11.0 us.)  Items past the row own nothing (lo 8).  A row of fewer than eight
+// values (TINY) is one item that starts at 0 and ends at d.
+struct Item {
+  int at, lo;
+};
+template <bool TINY>
+__device__ inline Item item_of(int d, int j) {
+  const int e = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
+  if (TINY) return Item{0, e ? 8 : 0};
+  const int at = e + 8 <= d ? e : d - 8;
+  return Item{at, e >= d ? 8 : e - at};
+}
 
-__device__ inline void load_raw(const void* row, int type, int d, int j, Raw& w) {
-  const int e = first_of(j);
-  if (e + 8 <= d) {
-    if (type == SPAX_F32) {
-      w.a = load_any<u32x4>((const float*)row + e);
-      w.b = load_any<u32x4>((const float*)row + e + 4);
-    } else {
-      w.a = load_any<u32x4>((const uint16_t*)row + e);
-    }
-  } else if (e < d) {
-    // one value per dword, past the end the last one again: nothing here waits for a load
+template <bool TINY>
+__device__ inline void load_raw(const void* row, int type, int d, const Item& it, Raw& w) {
+  if (it.lo == 8) return;
+  if constexpr (TINY) {
 #pragma unroll
     for (int i = 0; i < 7; ++i) {
-      const int k = e + i < d ? e + i : d - 1;
+      const int k = i < d ? i : d - 1;
       const uint32_t u =
           type == SPAX_F32 ? ((const uint32_t*)row)[k] : (uint32_t)((const uint16_t*)row)[k];
-      if (i < 4) w.a[i % 4] = u; else w.b[i % 4] = u;
+      if (type == SPAX_F32) {
+        if (i < 4) w.a[i % 4] = u; else w.b[i % 4] = u;
+      } else {
+        w.a[i / 2] = i % 2 ? w.a[i / 2] | u << 16 : u;
+      }
     }
+  } else if (type == SPAX_F32) {
+    w.a = load_any<u32x4>((const float*)row + it.at);
+    w.b = load_any<u32x4>((const float*)row + it.at + 4);
+  } else {
+    w.a = load_any<u32x4>((const uint16_t*)row + it.at);
   }
 }
 
@@ -66,14 +81,9 @@ __device__ inline float from_bits(uint32_t u, int type) {
   return __builtin_bit_cast(float, u << 16);
 }
 
-// Item j's values as loaded by load_raw; zeros past the end.
-__device__ inline void unpack(const Raw& w, int type, int d, int j, float v[8]) {
-  const int n = d - first_of(j);
-  if (n < 8) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = i < n && i < 7 ? from_bits(i < 4 ? w.a[i % 4] : w.b[i % 4], type) : 0.0f;
-  } else if (type == SPAX_F32) {
+// An item's values as loaded by load_raw, those that are not its own included.
+__device__ inline void unpack(const Raw& w, int type, float v[8]) {
+  if (type == SPAX_F32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = from_bits(w.a[i], SPAX_F32);
@@ -93,26 +103,39 @@ __device__ inline void unpack(const Raw& w, int type, int d, int j, float v[8]) 
   }
 }
 
-template <class T>
-__device__ inline void store8(T* row, int d, int j, const float v[8]) {
-  const int e = first_of(j);
-  if (e + 8 <= d) {
+// Zeros in place of values that are not the item's.
+template <bool TINY>
+__device__ inline void keep_own(float v[8], int d, const Item& it) {
+  if constexpr (TINY) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = it.lo == 0 && i < d ? v[i] : 0.0f;
+  } else if (it.lo) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i >= it.lo ? v[i] : 0.0f;
+  }
+}
+
+template <class T, bool TINY>
+__device__ inline void store8(T* row, int d, const Item& it, const float v[8]) {
+  if (!TINY && it.lo == 0) {
     typedef T T8 __attribute__((ext_vector_type(8)));
     T8 x;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
-    store_any(row + e, x);
+    store_any(row + it.at, x);
   } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (e + i < d) row[e + i] = (T)v[i];
+    for (int i = 0; i < 8; ++i)
+      if (i >= it.lo && (!TINY || i < d)) row[it.at + i] = (T)v[i];
   }
 }
 
-__device__ inline void store_row(void* p, int type, int64_t at, int d, int j, const float v[8]) {
-  if (type == SPAX_F32) store8<float>((float*)p + at, d, j, v);
-  else if (type == SPAX_F16) store8<f16>((f16*)p + at, d, j, v);
-  else store8<bf16>((bf16*)p + at, d, j, v);
+template <bool TINY>
+__device__ inline void store_row(void* p, int type, int64_t at, int d, const Item& it,
+                                 const float v[8]) {
+  if (type == SPAX_F32) store8<float, TINY>((float*)p + at, d, it, v);
+  else if (type == SPAX_F16) store8<f16, TINY>((f16*)p + at, d, it, v);
+  else store8<bf16, TINY>((bf16*)p + at, d, it, v);
 }
 
 __device__ inline const void* row_at(const void* p, int type, int64_t at) {
@@ -154,9 +177,11 @@ __device__ inline float sum_all(float v, float* slot) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
 }
 
-// v <- norm(v) without weight; elements past d are 0 and stay out of the sums.
-template <int NV>
-__device__ inline void normalise(float (*v)[8], const NormArgs& a, float* slot) {
+// v <- norm(v) without weight; values that are not the items' own become 0.
+template <int NV, bool TINY>
+__device__ inline void normalise(float (*v)[8], const NormArgs& a, const Item* it, float* slot) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) keep_own<TINY>(v[j], a.d, it[j]);
   if (a.layer) {
     float s = 0.0f;
 #pragma unroll
@@ -165,9 +190,11 @@ __device__ inline void normalise(float (*v)[8], const NormArgs& a, float* slot) 
       for (int i = 0; i < 8; ++i) s += v[j][i];
     const float mean = sum_all(s, slot) * a.inv_d;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = first_of(j) + i < a.d ? v[j][i] - mean : 0.0f;
+      for (int i = 0; i < 8; ++i) v[j][i] -= mean;
+      keep_own<TINY>(v[j], a.d, it[j]);
+    }
   }
   float s = 0.0f;
 #pragma unroll
@@ -182,58 +209,64 @@ __device__ inline void normalise(float (*v)[8], const NormArgs& a, float* slot) 
 }
 
 // v <- v * weight + bias; w and b hold them (EARLY) or are loaded here, an item at a time.
-template <int NV, bool EARLY>
-__device__ inline void weigh(float (*v)[8], const NormArgs& a, const float* weight,
+template <int NV, bool EARLY, bool TINY>
+__device__ inline void weigh(float (*v)[8], const NormArgs& a, const Item* it, const float* weight,
                              const float* bias, Raw* w, Raw* b) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int k = EARLY ? j : 0;
-    if (!EARLY && weight) load_raw(weight, SPAX_F32, a.d, j, w[k]);
-    if (!EARLY && bias) load_raw(bias, SPAX_F32, a.d, j, b[k]);
+    if (!EARLY && weight) load_raw<TINY>(weight, SPAX_F32, a.d, it[j], w[k]);
+    if (!EARLY && bias) load_raw<TINY>(bias, SPAX_F32, a.d, it[j], b[k]);
     float x[8];
     if (weight) {
-      unpack(w[k], SPAX_F32, a.d, j, x);
+      unpack(w[k], SPAX_F32, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= x[i];
     }
     if (bias) {
-      unpack(b[k], SPAX_F32, a.d, j, x);
+      unpack(b[k], SPAX_F32, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] += x[i];
     }
   }
 }
 
-__device__ inline void load_block(const NormArgs& a, int64_t row, int j, Raw& b) {
-  if (a.block) load_raw(row_at(a.block, a.b_type, row * a.b_stride), a.b_type, a.d, j, b);
+template <bool TINY>
+__device__ inline void load_block(const NormArgs& a, int64_t row, const Item& it, Raw& b) {
+  if (a.block)
+    load_raw<TINY>(row_at(a.block, a.b_type, row * a.b_stride), a.b_type, a.d, it, b);
 }
-__device__ inline void load_stream(const NormArgs& a, int64_t row, int j, Raw& r, Raw& g) {
-  if (a.residual) load_raw(row_at(a.residual, a.r_type, row * a.r_stride), a.r_type, a.d, j, r);
-  if (a.gate)
-    load_raw(row_at(a.gate, a.g_type, row * a.g_stride), a.g_type, a.d, j, g);
+template <bool TINY>
+__device__ inline void load_stream(const NormArgs& a, int64_t row, const Item& it, Raw& r, Raw& g) {
+  if (a.residual)
+    load_raw<TINY>(row_at(a.residual, a.r_type, row * a.r_stride), a.r_type, a.d, it, r);
+  if (a.gate) load_raw<TINY>(row_at(a.gate, a.g_type, row * a.g_stride), a.g_type, a.d, it, g);
 }
 
 // One row per workgroup, NV items per thread.  Up to two items everything a row needs is loaded at
 // once; wider rows (128 registers for each of 1024 threads) load residual, gate and weights when
 // they are used.
-template <int NV, int T>
-__global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a) {
+template <int NV, bool TINY>
+__global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
   constexpr bool EARLY = NV <= 2;
   __shared__ float slots[64];  // (post, pre) x (mean, square) x 16 waves
   Raw rb[NV], rr[NV], rg[NV], w[NV], b[NV];
+  Item it[NV];
   const int64_t row = blockIdx.x;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) it[j] = item_of<TINY>(a.d, j);
   const auto load_weights = [&](const float* weight, const float* bias) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (weight) load_raw(weight, SPAX_F32, a.d, j, w[j]);
-      if (bias) load_raw(bias, SPAX_F32, a.d, j, b[j]);
+      if (weight) load_raw<TINY>(weight, SPAX_F32, a.d, it[j], w[j]);
+      if (bias) load_raw<TINY>(bias, SPAX_F32, a.d, it[j], b[j]);
     }
   };
 #pragma unroll
-  for (int j = 0; j < NV; ++j) load_block(a, row, j, rb[j]);
+  for (int j = 0; j < NV; ++j) load_block<TINY>(a, row, it[j], rb[j]);
   if (EARLY) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_stream(a, row, j, rr[j], rg[j]);
+    for (int j = 0; j < NV; ++j) load_stream<TINY>(a, row, it[j], rr[j], rg[j]);
     load_weights(a.post_w, a.post_b);
   }
   float v[NV][8];
@@ -241,34 +274,36 @@ __global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a) {
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-    if (a.block) unpack(rb[j], a.b_type, a.d, j, v[j]);
+    if (a.block) unpack(rb[j], a.b_type, v[j]);
   }
   if (a.post_w && a.block) {
-    normalise<NV>(v, a, slots);
-    weigh<NV, EARLY>(v, a, a.post_w, a.post_b, w, b);
+    normalise<NV, TINY>(v, a, it, slots);
+    weigh<NV, EARLY, TINY>(v, a, it, a.post_w, a.post_b, w, b);
   }
   if (EARLY) load_weights(a.pre_w, a.pre_b);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (!EARLY) load_stream(a, row, j, rr[0], rg[0]);
+    if (!EARLY) load_stream<TINY>(a, row, it[j], rr[0], rg[0]);
     float x[8];
     if (a.gate) {
-      unpack(rg[EARLY ? j : 0], a.g_type, a.d, j, x);
+      unpack(rg[EARLY ? j : 0], a.g_type, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] *= x[i];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-    if (a.residual) unpack(rr[EARLY ? j : 0], a.r_type, a.d, j, x);
+    if (a.residual) unpack(rr[EARLY ? j : 0], a.r_type, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[j][i] = x[i] + a.scale * v[j][i];
-    if (a.residual_out) store_row(a.residual_out, a.r_type, row * a.ro_stride, a.d, j, v[j]);
+    if (a.residual_out)
+      store_row<TINY>(a.residual_out, a.r_type, row * a.ro_stride, a.d, it[j], v[j]);
   }
   if (!a.x) return;
-  normalise<NV>(v, a, slots + 32);
-  weigh<NV, EARLY>(v, a, a.pre_w, a.pre_b, w, b);
+  normalise<NV, TINY>(v, a, it, slots + 32);
+  weigh<NV, EARLY, TINY>(v, a, it, a.pre_w, a.pre_b, w, b);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) store_row(a.x, a.x_type, row * a.x_stride, a.d, j, v[j]);
+  for (int j = 0; j < NV; ++j)
+    store_row<TINY>(a.x, a.x_type, row * a.x_stride, a.d, it[j], v[j]);
 }
 
 }  // namespace
@@ -293,12 +328,14 @@ int launch_residual_norm(const spax_residual_norm_args* p, hipStream_t s) {
   const int nv = items <= 1024 ? 1 : items <= 2048 && p->n_rows <= 256 ? 2 : 4;
   const unsigned threads = (unsigned)(((items + nv - 1) / nv + 63) / 64 * 64);
   const dim3 grid((unsigned)p->n_rows), block(threads);
-  if (nv == 1)
-    hipLaunchKernelGGL((residual_norm_kernel<1, 1024>), grid, block, 0, s, a);
+  if (p->d < 8)
+    hipLaunchKernelGGL((residual_norm_kernel<1, true>), grid, block, 0, s, a);
+  else if (nv == 1)
+    hipLaunchKernelGGL((residual_norm_kernel<1, false>), grid, block, 0, s, a);
   else if (nv == 2)
-    hipLaunchKernelGGL((residual_norm_kernel<2, 1024>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((residual_norm_kernel<2, false>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((residual_norm_kernel<4, 1024>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((residual_norm_kernel<4, false>), grid, block, 0, s, a);
   SPAX_HIP_CHECK(hipGetLastError());
   return SPAX_OK;
 }
