@@ -9,9 +9,9 @@
 // per workgroup: walking over several rows with the weights in registers was slower (17.7 to 23 us
 // against 15.8 for 2048 rows).
 //
-// Measured: 2048 x 4096 bf16, norms before and after and a gate: 15.2 us, 67 MB, 4.4 TB/s (a large
+// Measured: 2048 x 4096 bf16, norms before and after and a gate: 14.6 us, 67 MB, 4.6 TB/s (a large
 // copy reaches 5.1).  333 x 5003, layer norms, rows that start anywhere: 9.1 us, four sums one after
-// another (256 rows 6.3 us: the rest is units that have two rows).  1 x 4096: 2.6 us on the device.
+// another (256 rows 6.3 us: the rest is units that have two rows).  1 x 4096: 2.4 us on the device.
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -320,10 +320,10 @@ int launch_residual_norm(const spax_residual_norm_args* p, hipStream_t s) {
   a.r_type = p->residual_type; a.b_type = p->block_type; a.g_type = p->gate_type;
   a.x_type = p->x_type; a.layer = p->kind == SPAX_NORM_LAYER; a.d = p->d;
   a.scale = p->scale; a.eps = p->eps; a.inv_d = 1.0f / (float)p->d;
-  // Items of a thread: one while 1024 threads hold the row (333 x 5003: 11.2 us, 12.5 with two);
-  // then two while a compute unit has one row (1 x 12891: 8.2 us, 10.1 with four), else four,
-  // whose fewer threads let a unit hold more rows (256 x 16384: 13.0 with two, 14.0 with four;
-  // 257: 18.4 and 15.7; 2048: 109 and 94).
+  // Items of a thread: one while 1024 threads hold the row (333 x 5003: 9.2 us, 12.1 with two);
+  // then two while a compute unit has one row (1 x 12891: 6.2 us, 7.7 with four), else four,
+  // whose fewer threads let a unit hold more rows (256 x 16384: 12.7 with two, 13.5 with four;
+  // 257 x 12891: 16.5 and 13.3; 2048 x 16384: 106 and 94).
   const int items = (p->d + 7) / 8;
   const int nv = items <= 1024 ? 1 : items <= 2048 && p->n_rows <= 256 ? 2 : 4;
   const unsigned threads = (unsigned)(((items + nv - 1) / nv + 63) / 64 * 64);
