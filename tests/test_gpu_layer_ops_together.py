@@ -134,3 +134,30 @@ def test_many_wide_rows_in_place(env):
 ])
 def test_windows_over_an_eight_bit_cache(env, n, longest, hq, hk, dim, window, ct):
     ops.test_attention_many_sequences(env, n, longest, hq, hk, dim, window, ct)
+
+
+# Widths around the eight values of a thread: the last item of a row then begins inside its
+# neighbour's, or the row is shorter than an item.
+@pytest.mark.parametrize("layout", ["plain", "odd"])
+@pytest.mark.parametrize("d", [2, 6, 8, 9, 15, 17, 511, 513, 8191, 8193, 16383])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_widths_around_a_thread(env, d, kind, layout):
+    t = ("fp32", "fp16", "bf16")
+    ops.test_norm(env, (5, d, kind, t[d % 3], t[(d + 1) % 3], t[(d + 2) % 3], True, "row", 1.0),
+                  layout)
+
+
+@pytest.mark.parametrize("d", [1, 5, 9, 15, 513, 4103, 8201, 16391, 32761])
+def test_odd_widths_in_place(env, d):
+    torch, spax, dev = env
+    g = ops._gen(torch, d)
+    for dtype in (torch.float32, torch.bfloat16):
+        r, b, e = (ops._randn(torch, g, (7, d), dtype) for _ in range(3))
+        w = 1 + 0.1 * torch.randn(d, generator=g, device=dev)
+        h, x = torch.empty_like(r), torch.empty_like(b)
+        spax.spax_residual_norm(spax.make_residual_norm(r, b, h, x, pre_weight=w, post_weight=w,
+                                                        gate=e))
+        spax.spax_residual_norm(spax.make_residual_norm(r, b, r, b, pre_weight=w, post_weight=w,
+                                                        gate=e))
+        torch.cuda.synchronize()
+        assert torch.equal(r, h) and torch.equal(b, x) and bool(torch.isfinite(x).all())
