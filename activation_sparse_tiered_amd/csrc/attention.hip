@@ -15,7 +15,10 @@
 //   * O^T = V^T P^T: a lane reads whole pieces of the rows of its 8 keys (16 lanes cover a row),
 //     and swaps 2x2 blocks of 16-bit values with byte permutes to get 8 keys of one dim.
 //   * p is split into two 16-bit values, p = hi + lo, each multiplied: rounding p to 16 bits
-//     would cost as much error again as rounding the result.
+//     would cost as much error again as rounding the result.  hi + lo keeps p to 2^-17 of itself in
+//     bf16 and, since fp16 ends at 2^-24, p 2^15 instead of p (Mma::kLift), in fp16 to the larger of
+//     2^-22 of itself and 2^-40 of the largest p.  p itself in fp16 lost what was below 2^-25 of one
+//     large key while l kept it: 508 keys at e^-18 of it came out an eighth low, 99 in one wave as 0.
 //   * Keys go through LDS, values do not: see Wave.  The next tile's loads are in flight through
 //     all of a tile's arithmetic.
 //
@@ -71,10 +74,13 @@ struct AttnArgs {
   float scale;
 };
 
+// kLift: the exponentials are taken of s - m + kLift (base 2), so the largest is 2^kLift, the most
+// that fp16 holds with room for its rounding.  It cancels in o / l, and lse takes it off again.
 template <class T>
 struct Mma;
 template <>
 struct Mma<f16> {
+  static constexpr float kLift = 15.0f, kUnlift = 0x1p-15f;
   typedef f16 v8 __attribute__((ext_vector_type(8)));
   static __device__ inline f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a),
@@ -89,6 +95,7 @@ struct Mma<f16> {
 };
 template <>
 struct Mma<bf16> {
+  static constexpr float kLift = 0.0f, kUnlift = 1.0f;
   typedef bf16 v8 __attribute__((ext_vector_type(8)));
   static __device__ inline f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a),
@@ -100,6 +107,12 @@ struct Mma<bf16> {
   }
   typedef bf16x2 v2;
 };
+
+// ln of the sum of exponentials whose largest exponent is m (base 2) and whose lifted sum is l.
+template <class T>
+__device__ inline float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l * Mma<T>::kUnlift)) * kLn2;
+}
 
 // The cache is read once, so its loads are marked as not worth keeping: 1 x 32768 keys 31.0 us
 // without, 27.6 with; 48 ragged 45.7 and 41.5; 32 x 32768 e4m3 330 and 325.
@@ -329,7 +342,7 @@ struct Wave {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][i] *= f;
     }
-    const float base = m == -INFINITY ? 0.0f : m;
+    const float base = (m == -INFINITY ? 0.0f : m) - Mma<T>::kLift;
     u32x4 hi2, lo2;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -535,8 +548,7 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
         T* out = (T*)a.out + seq * a.os + (head0 + r) * a.oh;
         w.put(out, g, w.l == 0.0f ? 0.0f : v_mul / w.l);
         if (a.lse && g == 0)
-          a.lse[(int64_t)seq * a.n_heads + head0 + r] =
-              w.l == 0.0f ? -INFINITY : (w.m + log2f(w.l)) * kLn2;
+          a.lse[(int64_t)seq * a.n_heads + head0 + r] = lse_of<T>(w.m, w.l);
       }
       continue;
     }
@@ -611,8 +623,7 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
           for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[y][i] * inv;
           store_n<4>((T*)a.out + seq * a.os + (head0 + h) * a.oh + dim, out);
           if (a.lse && dim == 0)
-            a.lse[(int64_t)seq * a.n_heads + head0 + h] =
-                l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            a.lse[(int64_t)seq * a.n_heads + head0 + h] = lse_of<T>(m, l);
         } else {
           const int64_t part = 2 * ((int64_t)(head0 + h) * a.shares + share) + which;
           *reinterpret_cast<f32x4*>(a.part_o + part * D + dim) = sum[y];
@@ -703,7 +714,7 @@ __global__ __launch_bounds__(kJoinThreads, 8) void attention_join_kernel(AttnArg
   for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : total[i] * inv;
   store_n<4>((T*)a.out + seq * a.os + head * a.oh + d, out);
   if (a.lse && d == 0)
-    a.lse[(int64_t)seq * a.n_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    a.lse[(int64_t)seq * a.n_heads + head] = lse_of<T>(m, l);
 }
 
 template <class T, bool NARROW, int D>

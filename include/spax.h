@@ -540,7 +540,8 @@ int spax_kv_append(const spax_kv_append_args* a, hipStream_t stream);
  * whatever they hold.  A sequence with no keys, or whose scores are all -inf, gives zeros and
  * lse -inf.  q, out : `type` (SPAX_F16 or SPAX_BF16), the cache's type or the cache E4M3; 16-byte
  * aligned with strides a multiple of 8 elements.  Probabilities enter the product with v as the
- * sum of two `type` values, so they carry twice its precision.
+ * sum of two `type` values: within 2^-17 of themselves in BF16, and in F16 within 2^-22 of
+ * themselves or 2^-40 of the sequence's largest.
  *   max_len : host bound on lens; sets how the keys are shared out, and the workspace.
  *   ws      : spax_attention_workspace_bytes(a) bytes (0: none needed), 256-byte aligned, any
  *             contents; calls that may run at the same time need a workspace each.
