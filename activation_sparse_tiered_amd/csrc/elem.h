@@ -44,18 +44,19 @@ __device__ inline void store_n(T* p, const float* v) {
   store_any(p, x);
 }
 
-// E4M3 values, kept as bytes: clamped to +-448 first (the conversion alone would turn a value
-// past the range into NaN); NaN passes.
+// E4M3 values, kept as bytes.  Stored values are clamped to +-448 before (the conversion alone would
+// turn a value past the range into NaN); NaN passes.
 struct e4m3 {
   uint8_t bits;
 };
+constexpr float kE4m3Max = 448.0f;
 __device__ inline float clamp_e4m3(float v) {
-  v = v > 448.0f ? 448.0f : v;
-  return v < -448.0f ? -448.0f : v;
+  v = v > kE4m3Max ? kE4m3Max : v;
+  return v < -kE4m3Max ? -kE4m3Max : v;
 }
 __device__ inline uint32_t pack_e4m3(const float v[4]) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[0]), clamp_e4m3(v[1]), 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v[2]), clamp_e4m3(v[3]), w, true);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
   return (uint32_t)w;
 }
 // N a multiple of four, p aligned to four bytes.
@@ -72,7 +73,7 @@ __device__ inline void store1(T* p, float v) {
   *p = (T)v;
 }
 __device__ inline void store1(e4m3* p, float v) {
-  p->bits = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(v), 0.0f, 0, false);
+  p->bits = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.0f, 0, false);
 }
 
 }  // namespace elem

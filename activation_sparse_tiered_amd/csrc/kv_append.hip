@@ -91,6 +91,29 @@ __device__ inline void put(T* p, const float* v) {
     store_n<N>(p, v);
 }
 
+// x / scale, rounded to nearest, then clamped.  With r = 1 / s and p = x r the remainder x - p s is exact
+// and p + (x - p s) r is the quotient; the rounded reciprocal alone puts ties of e4m3 on the wrong
+// side.  p decides what is clamped, so an infinity never gets as far as its remainder.
+template <int N>
+__device__ inline void divide_e4m3(float v[N], float scale) {
+  // scales near the ends of the range, whose reciprocal leaves it, come back with their values
+  const float size = fabsf(scale);
+  if (!(size >= 0x1p-64f && size <= 0x1p64f)) {
+    const float t = size < 1.0f ? 0x1p64f : 0x1p-64f;
+    scale *= t;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= t;
+  }
+  const float r = 1.0f / scale;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float p = v[i] * r;
+    float x = fmaf(fmaf(-p, scale, v[i]), r, p);
+    x = p > kE4m3Max ? kE4m3Max : x;
+    v[i] = p < -kE4m3Max ? -kE4m3Max : x;
+  }
+}
+
 // SRC: type of q, k, v; LOW: of q_out (and a 16-bit cache); C: of the cache.  A thread's item is N
 // pairs of a head, or as many values that are copied: 2 N of them, one for N = 1.
 template <class SRC, class LOW, class C, int N>
@@ -170,15 +193,16 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
       const int hh = is_v ? h - n_heads - n_kv : h - n_heads;
       C* dst = is_v ? (C*)a.vc + to.v + hh * a.vc_head : (C*)a.kc + to.k + hh * a.kc_head;
       if constexpr (sizeof(C) == 1) {
-        // by the reciprocal: a division per value costs more than it adds (2^-24 before a rounding
-        // to 2^-4)
         const float* scale = is_v ? a.v_scale : a.k_scale;
         if (scale) {
-          const float f = 1.0f / scale[hh];
+          const float by = scale[hh];
+          divide_e4m3<N>(x, by);
+          divide_e4m3<N>(y, by);
+        } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            x[i] *= f;
-            y[i] *= f;
+            x[i] = clamp_e4m3(x[i]);
+            y[i] = clamp_e4m3(y[i]);
           }
         }
       }

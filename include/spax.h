@@ -499,7 +499,7 @@ typedef struct spax_kv_cache {
  * inv_freq[i] (product and reduction by whole turns in 64 bits),
  *   (x, y) -> (x cos a - y sin a, x sin a + y cos a),
  * pair i being (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved; later values and v are
- * copied.  E4M3: x times the reciprocal of its scale, clamped to +-448 (NaN stays NaN).
+ * copied.  E4M3: x / scale (rounded to 32 bits), clamped to +-448 (NaN stays NaN).
  *   q, k, v : src_type; token t, head h starts at t * token_stride + h * head_stride (a fused
  *             q|k|v row is three pointers into it).  q and q_out may both be NULL (n_heads 0).
  *   q_out   : out_type (SPAX_F16 or SPAX_BF16).  May be q itself, if type and strides agree.
