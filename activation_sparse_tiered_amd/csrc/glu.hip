@@ -20,14 +20,18 @@ struct GluArgs {
   int32_t d, gelu, blocks_per_row;
 };
 
-__device__ inline float act(float g, bool gelu) {
+// act(g) * up.  With h = exp(-|u| / 2), 1 / (1 + exp(-u)) is 1 / (1 + h h) above zero and
+// h h / (1 + h h) below, where one h goes to each factor: exp(-u) itself overflows at u = -88, where act(g)
+// is still 2^-121, and h h alone ends there.  1 + h h is in [1, 2], where the hardware's reciprocal
+// is good to 2^-23 of itself.
+__device__ inline float act_mul(float g, float up, bool gelu) {
   float u = g;
   if (gelu) {
     constexpr float kTwoRootTwoOverPi = 1.59576912160573071176f;
     u = kTwoRootTwoOverPi * (g + 0.044715f * g * g * g);
   }
-  // exp(-u) overflows to inf below u = -88: g / inf = -0, the limit
-  return g / (1.0f + expf(-u));
+  const float h = expf(-0.5f * fabsf(u)), f = u < 0.0f ? h : 1.0f;
+  return g * f * __builtin_amdgcn_rcpf(1.0f + h * h) * (up * f);
 }
 
 // Eight values per thread; rows need not start on eight (see load_any).
@@ -45,10 +49,10 @@ __global__ __launch_bounds__(kGluThreads) void glu_kernel(GluArgs a) {
     const S8 g = load_any<S8>(gate + e), u = load_any<S8>(up + e);
     X8 y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = (X)(act((float)g[i], a.gelu) * (float)u[i]);
+    for (int i = 0; i < 8; ++i) y[i] = (X)act_mul((float)g[i], (float)u[i], a.gelu);
     store_any(x + e, y);
   } else {
-    for (int i = e; i < a.d; ++i) x[i] = (X)(act((float)gate[i], a.gelu) * (float)up[i]);
+    for (int i = e; i < a.d; ++i) x[i] = (X)act_mul((float)gate[i], (float)up[i], a.gelu);
   }
 }
 
