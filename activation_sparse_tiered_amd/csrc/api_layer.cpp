@@ -26,7 +26,7 @@ void add_rows(Spans* b, const void* p, int64_t n0, int64_t s0, int64_t n1, int64
 // Strides of n0 x n1 x ... rows of d values do not make rows overlap: sorted by stride, each
 // axis steps past everything the axes below it cover.
 bool strides_ok(const int64_t* n, const int64_t* s, int axes, int64_t d) {
-  int order[3] = {0, 1, 2};
+  int order[4] = {0, 1, 2, 3};
   for (int i = 0; i < axes; ++i)
     for (int k = i + 1; k < axes; ++k)
       if (s[order[k]] < s[order[i]]) std::swap(order[i], order[k]);
@@ -117,22 +117,40 @@ int check_cache(const spax_kv_cache* c) {
   return SPAX_OK;
 }
 
-// The cache's buffers (out: it is written).  k and v may be interleaved in one allocation, page
-// by page or row by row: their spans then overlap without sharing a value, so they are not held
-// against each other.
+// Keys or values: p's pages from the first to the last byte of each.
+Span pages_of(const spax_kv_cache* c, const void* p, int64_t page, int64_t head, int64_t row,
+              bool out, const char* name) {
+  const size_t eb = (size_t)elem::bytes_of(c->type);
+  const int64_t n = (c->n_kv_heads - 1) * head + (c->page_size - 1) * row + c->head_dim;
+  const bool many = c->n_pages > 1;
+  return Span{p, (size_t)((c->n_pages - 1) * page + n) * eb, out, name,
+              many ? (size_t)n * eb : 0, many ? (size_t)page * eb : 0};
+}
+
+// The cache's buffers (out: it is written).
 void add_cache(const spax_kv_cache* c, bool out, Spans* b) {
-  const int64_t k = (int64_t)(c->n_pages - 1) * c->k_page_stride +
-                    (int64_t)(c->n_kv_heads - 1) * c->k_head_stride +
-                    (int64_t)(c->page_size - 1) * c->k_row_stride + c->head_dim;
-  const int64_t v = (int64_t)(c->n_pages - 1) * c->v_page_stride +
-                    (int64_t)(c->n_kv_heads - 1) * c->v_head_stride +
-                    (int64_t)(c->page_size - 1) * c->v_row_stride + c->head_dim;
-  b->add(c->k, (size_t)k * elem::bytes_of(c->type), out, "cache k");
-  b->add(c->v, (size_t)v * elem::bytes_of(c->type), out, "cache v");
+  b->s[b->n++] = pages_of(c, c->k, c->k_page_stride, c->k_head_stride, c->k_row_stride, out,
+                          "cache k");
+  b->s[b->n++] = pages_of(c, c->v, c->v_page_stride, c->v_head_stride, c->v_row_stride, out,
+                          "cache v");
   b->add(c->page_table, 4 * (size_t)((int64_t)(c->n_seqs - 1) * c->table_stride + c->max_pages),
          false, "page_table");
   b->add(c->k_scale, 4 * (size_t)c->n_kv_heads, false, "k_scale");
   b->add(c->v_scale, 4 * (size_t)c->n_kv_heads, false, "v_scale");
+}
+
+// Whether k and v, interleaved in one allocation so that their pages' spans meet, still have no
+// row in common: with equal strides, the distance from one to the other is then the stride of one
+// more axis, of length two.
+bool rows_apart(const spax_kv_cache& c) {
+  if (c.k_page_stride != c.v_page_stride || c.k_head_stride != c.v_head_stride ||
+      c.k_row_stride != c.v_row_stride)
+    return false;
+  const uintptr_t k = (uintptr_t)c.k, v = (uintptr_t)c.v;
+  const int64_t n[4] = {c.n_pages, c.n_kv_heads, c.page_size, 2};
+  const int64_t s[4] = {c.k_page_stride, c.k_head_stride, c.k_row_stride,
+                        (int64_t)((v > k ? v - k : k - v) / (size_t)elem::bytes_of(c.type))};
+  return strides_ok(n, s, 4, c.head_dim);
 }
 
 }  // namespace
@@ -209,7 +227,7 @@ int check_kv_append(const spax_kv_append_args* a, Spans* spans) {
                         a->q_head_stride == a->out_head_stride;
   st = check_overlaps(b, [&](const Span& x, const Span& y) {
     if (is(x, "q_out") && is(y, "q")) return in_place;
-    return is(x, "cache k") && is(y, "cache v") && c.k != c.v;  // interleaved, see add_cache
+    return is(x, "cache k") && is(y, "cache v") && rows_apart(c);
   });
   if (st) return st;
   if (spans) *spans = b;

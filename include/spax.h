@@ -475,7 +475,10 @@ enum { SPAX_F32 = 0, SPAX_F16 = 1, SPAX_BF16 = 2, SPAX_E4M3 = 3 };
  * nothing is read or written there.
  *   E4M3: a stored value q of head h stands for q * k_scale[h] (v_scale[h]); NULL means 1.
  * Limits: head_dim 64, 96, 128, 192 or 256; page_size a power of two, 4..65536; k and v 16-byte
- * aligned and their strides a multiple of 16 bytes (rows may not overlap, nor k's with v's).
+ * aligned and their strides a multiple of 16 bytes.  Rows may not overlap, nor, where the cache is
+ * written, k's with v's.  In one allocation k and v may be interleaved: page by page (equal page
+ * strides, each page's rows in any order), or with equal strides throughout by heads, rows or
+ * any other axis.
  */
 typedef struct spax_kv_cache {
   void* k;
