@@ -118,6 +118,15 @@ __device__ inline float lse_of(float m, float l) {
 // without, 27.6 with; 48 ragged 45.7 and 41.5; 32 x 32768 e4m3 330 and 325.
 __device__ inline u32x4 load16(const void* p) { return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)); }
 
+// Orders a wave's own LDS accesses between its lanes: what was written before is read after, and
+// nothing read before is overwritten.  The wave's LDS accesses run in order, so this is for the
+// compiler and costs no instruction.
+__device__ inline void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // N dwords at p (aligned to their own size, at most 16 bytes; 3 dwords never occur).
 template <int N>
 __device__ inline void load_words(const void* p, uint32_t* w) {
@@ -523,7 +532,9 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
       W::load_values(z, src, lane);
       for (;;) {
         float p[4 * W::KH];
+        wave_lds_order();  // the last tile's rows have been read
         W::lay_out_keys(z, k_rows, lane);
+        wave_lds_order();
         tile += step;
         if (tile >= t1) {
           w.score(k_rows, src, lane, p);
