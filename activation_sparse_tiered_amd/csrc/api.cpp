@@ -13,10 +13,11 @@ using namespace spax;
 namespace {
 
 // Prefix the current thread-local message with the phase number.
-int phase_fail(int st, int i) {
-  char msg[400];
+int phase_fail(int st, int i, PhaseName name) {
+  char msg[400], who[64];
   snprintf(msg, sizeof(msg), "%s", spax_last_error());
-  return fail(st, "phase %d: %s", i, msg);
+  name(i, who, sizeof(who));
+  return fail(st, "%s: %s", who, msg);
 }
 
 int check_tier_outputs(const uint16_t* x, int32_t d_in, const int32_t* full_idx,
@@ -141,10 +142,12 @@ int check_gemv_args(const spax_layout* L, const void* packed, const uint16_t* x,
 
 namespace spax {
 
+void numbered_phase(int i, char* out, size_t n) { snprintf(out, n, "phase %d", i); }
+
 // Every check of spax_decode_step_projections, before anything is enqueued.  noalloc: the
 // workspace is not used (the batched form's tables go to the static scratch, whose size
 // bounds the number of phases).
-int validate_step(const spax_step* step, bool noalloc) {
+int validate_step(const spax_step* step, bool noalloc, PhaseName name) {
   if (!step || !step->phases) return fail(SPAX_ERR_NULL, "step and step->phases are required");
   if (step->n_phases < 1) return fail(SPAX_ERR_SHAPE, "n_phases %d < 1", step->n_phases);
   if (step->flags & ~(SPAX_STEP_SEPARATE | SPAX_STEP_BATCHED | SPAX_STEP_DETERMINISTIC))
@@ -161,18 +164,19 @@ int validate_step(const spax_step* step, bool noalloc) {
   const size_t ws_bytes = noalloc ? 0 : step->ws_bytes;
   for (int i = 0; i < step->n_phases; ++i) {
     const spax_phase& ph = step->phases[i];
-    if (!ph.layout) return fail(SPAX_ERR_NULL, "phase %d: layout is NULL", i);
-    int st = check_tier_outputs(ph.x, ph.layout->d_in, ph.full_idx, ph.approx_idx, ph.counts);
-    if (st) return phase_fail(st, i);
+    int st = ph.layout ? SPAX_OK : fail(SPAX_ERR_NULL, "layout is NULL");
+    if (st) return phase_fail(st, i, name);
+    st = check_tier_outputs(ph.x, ph.layout->d_in, ph.full_idx, ph.approx_idx, ph.counts);
+    if (st) return phase_fail(st, i, name);
     TierArgs a;
     st = tier_args_from_params(&ph.params, ph.layout->d_in, &a);
-    if (st) return phase_fail(st, i);
+    if (st) return phase_fail(st, i, name);
     GemvPlan plan;
     st = check_gemv_args(ph.layout, ph.packed, ph.x, ph.full_idx, ph.approx_idx, ph.counts, ph.y,
                          ws, ws_bytes, &plan);
-    if (st) return phase_fail(st, i);
+    if (st) return phase_fail(st, i, name);
     st = check_phase_aliasing(ph);
-    if (st) return phase_fail(st, i);
+    if (st) return phase_fail(st, i, name);
   }
   if (deterministic) {
     const size_t need = deterministic_workspace_bytes(step->phases, step->n_phases);
@@ -180,8 +184,11 @@ int validate_step(const spax_step* step, bool noalloc) {
       return fail(SPAX_ERR_WORKSPACE, "SPAX_STEP_DETERMINISTIC needs a workspace of %zu bytes",
                   need);
     for (int i = 0; i < step->n_phases; ++i)
-      if (need > 0 && phase_touches(step->phases[i], step->ws, need))
-        return fail(SPAX_ERR_PARAM, "the workspace overlaps a buffer of phase %d", i);
+      if (need > 0 && phase_touches(step->phases[i], step->ws, need)) {
+        char who[64];
+        name(i, who, sizeof(who));
+        return fail(SPAX_ERR_PARAM, "the workspace overlaps a buffer of %s", who);
+      }
   }
   if (batched) {
     const size_t need = batched_workspace_bytes(step->n_phases);

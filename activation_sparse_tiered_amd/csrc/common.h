@@ -128,8 +128,11 @@ struct StepHooks {
   // Whether what follows phase i reads or writes a byte of [p, p + n).
   virtual bool touches_after(int i, const void* p, size_t n) const = 0;
 };
+// Writes how an error names phase i of a step.
+using PhaseName = void (*)(int i, char* out, size_t n);
+void numbered_phase(int i, char* out, size_t n);  // "phase 3"
 // Every check of spax_decode_step_projections (noalloc: with no workspace).
-int validate_step(const spax_step* step, bool noalloc);
+int validate_step(const spax_step* step, bool noalloc, PhaseName name = numbered_phase);
 // Enqueue a validated step; noalloc: the batched form takes its tables from the static scratch;
 // hooks (not with the batched form): called after each phase.
 int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc,

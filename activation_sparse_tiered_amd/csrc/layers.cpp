@@ -8,11 +8,16 @@ using namespace spax;
 
 namespace {
 
-constexpr int kPhases = 4;  // qkv, o, gate_up, down
+constexpr int kPhases = 4;
+const char* const kPhaseName[kPhases] = {"qkv", "o", "gate_up", "down"};
 
 const spax_phase* phase_of(const spax_decoder_layer& L, int k) {
   const spax_phase* p[kPhases] = {L.qkv, L.o, L.gate_up, L.down};
   return p[k];
+}
+
+void phase_name(int i, char* out, size_t n) {
+  snprintf(out, n, "layer %d, %s", i / kPhases, kPhaseName[i % kPhases]);
 }
 
 bool inside(const void* p, size_t n, const void* base, size_t size) {
@@ -54,7 +59,7 @@ int check_parts(const spax_decoder_layer& L, int i, Parts* b) {
   if ((st = check_residual_norm(L.mlp_norm, &b->mlp_norm))) return part_fail(st, i, "mlp_norm");
   for (int k = 0; k < kPhases; ++k)
     if (!phase_of(L, k)->layout)
-      return fail(SPAX_ERR_NULL, "layer %d: the layout of phase %d is NULL", i, k);
+      return part_fail(fail(SPAX_ERR_NULL, "layout is NULL"), i, kPhaseName[k]);
   const auto wired = [&](bool ok, const char* part, const char* to) {
     return ok ? SPAX_OK : fail(SPAX_ERR_PARAM, "layer %d: %s is not wired to %s", i, part, to);
   };
@@ -167,14 +172,7 @@ int decode_layers(const spax_decoder_layer* layers, int32_t n, int32_t flags, vo
   step.phases = phases.data();
   step.ws = ws;
   step.ws_bytes = ws_bytes;
-  if ((st = validate_step(&step, false))) {
-    char msg[400];
-    snprintf(msg, sizeof(msg), "%s", spax_last_error());
-    int phase = 0, at = 0;
-    if (sscanf(msg, "phase %d: %n", &phase, &at) < 1) return st;
-    static const char* const name[kPhases] = {"qkv", "o", "gate_up", "down"};
-    return fail(st, "layer %d, %s: %s", phase / kPhases, name[phase % kPhases], msg + at);
-  }
+  if ((st = validate_step(&step, false, phase_name))) return st;
   if (flags & SPAX_STEP_DETERMINISTIC) {
     const size_t det = deterministic_workspace_bytes(phases.data(), step.n_phases);
     need = det > need ? det : need;
