@@ -744,7 +744,7 @@ void start(AttnArgs a, hipStream_t s) {
 }
 
 template <class T, bool NARROW, int D>
-int launch(const AttnArgs& a, const AttentionPlan& plan, hipStream_t s) {
+int launch(const AttnArgs& a, hipStream_t s) {
   start<T, NARROW, D>(a, s);
   SPAX_HIP_CHECK(hipGetLastError());
   if (a.shares > 1) {
@@ -756,13 +756,13 @@ int launch(const AttnArgs& a, const AttentionPlan& plan, hipStream_t s) {
 }
 
 template <class T, bool NARROW>
-int launch_dim(const AttnArgs& a, const AttentionPlan& plan, int dim, hipStream_t s) {
+int launch_dim(const AttnArgs& a, int dim, hipStream_t s) {
   switch (dim) {
-    case 64: return launch<T, NARROW, 64>(a, plan, s);
-    case 96: return launch<T, NARROW, 96>(a, plan, s);
-    case 128: return launch<T, NARROW, 128>(a, plan, s);
-    case 192: return launch<T, NARROW, 192>(a, plan, s);
-    default: return launch<T, NARROW, 256>(a, plan, s);
+    case 64: return launch<T, NARROW, 64>(a, s);
+    case 96: return launch<T, NARROW, 96>(a, s);
+    case 128: return launch<T, NARROW, 128>(a, s);
+    case 192: return launch<T, NARROW, 192>(a, s);
+    default: return launch<T, NARROW, 256>(a, s);
   }
 }
 
@@ -815,10 +815,10 @@ int launch_attention(const spax_attention_args* p, void* ws, hipStream_t s) {
   a.part_o = (float*)ws;
   a.part_ml = (float*)ws + (size_t)2 * p->n_heads * plan.shares * c.head_dim;
   if (c.type == SPAX_E4M3)
-    return p->type == SPAX_F16 ? launch_dim<f16, true>(a, plan, c.head_dim, s)
-                               : launch_dim<bf16, true>(a, plan, c.head_dim, s);
-  return p->type == SPAX_F16 ? launch_dim<f16, false>(a, plan, c.head_dim, s)
-                             : launch_dim<bf16, false>(a, plan, c.head_dim, s);
+    return p->type == SPAX_F16 ? launch_dim<f16, true>(a, c.head_dim, s)
+                               : launch_dim<bf16, true>(a, c.head_dim, s);
+  return p->type == SPAX_F16 ? launch_dim<f16, false>(a, c.head_dim, s)
+                             : launch_dim<bf16, false>(a, c.head_dim, s);
 }
 
 }  // namespace spax
