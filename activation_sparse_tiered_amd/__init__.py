@@ -309,6 +309,14 @@ def _flat(t, name, n, dtype):
     return t
 
 
+def _int32(n, name) -> int:
+    """n for a 32-bit field, which would cut it off without a word."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} {n} does not fit 32 bits")
+    return n
+
+
 def _same_shape(t, name, shape):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
@@ -379,13 +387,15 @@ def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None) -> KvCache:
         raise TypeError(f"page_table is {page_table.dtype}, not torch.int32")
     c = KvCache()
     c.type = _type_of(k)
-    c.n_pages, c.n_kv_heads, c.page_size, c.head_dim = (int(n) for n in k.shape)
+    for name, n in zip(("n_pages", "n_kv_heads", "page_size", "head_dim"), k.shape):
+        setattr(c, name, _int32(n, name))
     c.k, c.v, c.page_table = k.data_ptr(), v.data_ptr(), page_table.data_ptr()
     c.k_scale = _ptr(_flat(k_scale, "k_scale", k.shape[1], "torch.float32"))
     c.v_scale = _ptr(_flat(v_scale, "v_scale", k.shape[1], "torch.float32"))
     c.k_page_stride, c.k_head_stride, c.k_row_stride = k.stride()[:3]
     c.v_page_stride, c.v_head_stride, c.v_row_stride = v.stride()[:3]
-    c.n_seqs, c.max_pages = (int(n) for n in page_table.shape)
+    c.n_seqs = _int32(page_table.shape[0], "n_seqs")
+    c.max_pages = _int32(page_table.shape[1], "max_pages")
     c.table_stride = page_table.stride(0)
     return _keep(c, k, v, page_table, k_scale, v_scale)
 
@@ -398,7 +408,7 @@ def make_kv_append(cache: KvCache, q, k, v, positions, q_out, seq=None, inv_freq
     (None: token t belongs to sequence t), inv_freq fp32 [rot_dim / 2] (None: no rotation)."""
     _rows(k, "k", 3)
     _rows(v, "v", 3)
-    n = int(k.shape[0])
+    n = _int32(k.shape[0], "n_tokens")
     shape = (n, cache.n_kv_heads, cache.head_dim)
     _same_shape(k, "k", shape)
     _same_shape(v, "v", shape)
@@ -413,7 +423,7 @@ def make_kv_append(cache: KvCache, q, k, v, positions, q_out, seq=None, inv_freq
         _same_shape(q, "q", (n, q.shape[1], cache.head_dim))
         _rows(q_out, "q_out", 3)
         _same_shape(q_out, "q_out", q.shape)
-        a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), int(q.shape[1])
+        a.q, a.q_out, a.n_heads = q.data_ptr(), q_out.data_ptr(), _int32(q.shape[1], "n_heads")
         a.q_token_stride, a.q_head_stride = q.stride()[:2]
         a.out_token_stride, a.out_head_stride = q_out.stride()[:2]
         a.out_type = _type_of(q_out)
@@ -429,7 +439,7 @@ def make_kv_append(cache: KvCache, q, k, v, positions, q_out, seq=None, inv_freq
     a.seq = _ptr(_flat(seq, "seq", n, "torch.int32"))
     if inv_freq is not None:
         a.inv_freq = _ptr(_flat(inv_freq, "inv_freq", inv_freq.numel(), "torch.float32"))
-        a.rot_dim = 2 * inv_freq.numel()
+        a.rot_dim = _int32(2 * inv_freq.numel(), "rot_dim")
     a.interleaved = int(bool(interleaved))
     return _keep(a, q, k, v, positions, q_out, seq, inv_freq, parts=(cache,))
 
@@ -451,14 +461,15 @@ def make_attention(cache: KvCache, q, lens, out, max_len: int | None = None,
         raise TypeError(f"out is {out.dtype}, q is {q.dtype}")
     a = AttentionArgs()
     a.cache = C.pointer(cache)
-    a.q, a.out, a.type, a.n_heads = q.data_ptr(), out.data_ptr(), _type_of(q), int(q.shape[1])
+    a.q, a.out, a.type = q.data_ptr(), out.data_ptr(), _type_of(q)
+    a.n_heads = _int32(q.shape[1], "n_heads")
     a.q_seq_stride, a.q_head_stride = q.stride()[:2]
     a.out_seq_stride, a.out_head_stride = out.stride()[:2]
     a.lens = _ptr(_flat(lens, "lens", cache.n_seqs, "torch.int32"))
     a.lse = _ptr(_flat(lse, "lse", cache.n_seqs * a.n_heads, "torch.float32"))
-    a.max_len = int(cache.max_pages * cache.page_size if max_len is None else max_len)
+    a.max_len = _int32(cache.max_pages * cache.page_size if max_len is None else max_len, "max_len")
     a.scale = float(cache.head_dim ** -0.5 if scale is None else scale)
-    a.window = int(window)
+    a.window = _int32(window, "window")
     return _keep(a, q, lens, out, lse, parts=(cache,))
 
 
@@ -498,7 +509,7 @@ def make_residual_norm(residual, block, residual_out, x, kind: str = "rms", pre_
         setattr(a, name + "_stride", t.stride(0))
     if shape is None:
         raise ValueError("no rows given")
-    a.n_rows, a.d = (int(n) for n in shape)
+    a.n_rows, a.d = _int32(shape[0], "n_rows"), _int32(shape[1], "d")
     if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
         raise TypeError(f"residual_out is {residual_out.dtype}, residual is {residual.dtype}")
     stream_type = residual if residual is not None else residual_out
@@ -536,7 +547,7 @@ def make_glu(gate, up, x, act: str = "silu") -> GluArgs:
     if gate.dtype != up.dtype:
         raise TypeError(f"up is {up.dtype}, gate is {gate.dtype}")
     a.src_type, a.x_type, a.act = _type_of(gate), _type_of(x), _ACTS.get(act, act)
-    a.n_rows, a.d = (int(n) for n in gate.shape)
+    a.n_rows, a.d = _int32(gate.shape[0], "n_rows"), _int32(gate.shape[1], "d")
     return _keep(a, gate, up, x)
 
 
