@@ -338,6 +338,17 @@ def _on(struct, device):
     return struct
 
 
+def _workspace(ws, desc):
+    """A workspace tensor is in one piece on the device of the tensors described."""
+    device = getattr(ws, "device", None)
+    if device is None:      # an address, or none needed
+        return
+    if not ws.is_contiguous():
+        raise ValueError("the workspace is not contiguous")
+    if device != desc._device and ws.numel():
+        raise ValueError(f"the workspace is on {device}, the tensors are on {desc._device}")
+
+
 def _fast(name, slow):
     """torch's own C function for `slow`, where this torch has it (a microsecond a call less)."""
     import torch
@@ -479,6 +490,7 @@ def spax_attention_workspace_bytes(args: AttentionArgs) -> int:
 
 def spax_paged_attention(args: AttentionArgs, ws=None, ws_bytes: int | None = None,
                          stream=None) -> None:
+    _workspace(ws, args)
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
     _call(lib.spax_paged_attention, "spax_paged_attention", args, stream, args, _ptr(ws),
@@ -566,6 +578,8 @@ def make_layer(qkv: Phase, append: KvAppendArgs, attention: AttentionArgs, o: Ph
         setattr(L, name, C.pointer(p))
     L._keep = parts
     devices = {p._device for p in (append, attention, attn_norm, glu, mlp_norm)}
+    for p in (qkv, o, gate_up, down):
+        devices |= {t.device for t in getattr(p, "_keep", ()) if hasattr(t, "device")}
     if len(devices) > 1:
         raise ValueError(f"parts on different devices: {sorted(map(str, devices))}")
     return _on(L, next(iter(devices)))
@@ -590,6 +604,7 @@ def spax_decode_layers(layers, ws, ws_bytes: int | None = None, flags: int = 0,
     """A whole batch-one decode step through decoder layers: their projections with the operators
     between them.  layers: make_layer structs, or their layer_array."""
     arr = layers if isinstance(layers, C.Array) else layer_array(layers)
+    _workspace(ws, arr)
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
     _call(lib.spax_decode_layers, "spax_decode_layers", arr, stream, arr, len(arr),
