@@ -5,8 +5,10 @@
 //   l <- l exp(m_old - m) + sum p,   o <- o exp(m_old - m) + sum p v,   out = o / l.
 // Pieces of a sequence (m, l, o) join by the same rule.
 //
-// Bound: the cache's bytes, each read once (counted: 1.00 of them come from memory).  A wave takes
-// a tile of 32 keys at a time:
+// Bound: the cache's bytes, each read once for up to 16 query heads of a key head (counted: 1.00 to 1.02
+// of them come from memory).  Every further 16 ask for them again, at the same time on the same XCD,
+// mostly from its L2: 20 and 48 heads on one key head fetch 1.02 and 1.10 of them.  A wave takes a tile
+// of 32 keys at a time:
 //   * S^T = K Q^T by 16x16x32 matrix instructions, keys as rows and the group's query heads as
 //     columns (16 columns are computed whatever the group; the matrix units have the room).
 //   * S^T's layout (lane: one head, keys 4g..4g+3 of each half) is already that of the second
@@ -27,9 +29,9 @@
 // workgroup per compute unit.  Fixed pieces of a longest possible sequence instead left the
 // chip to the long ones (48 sequences of 0 to 8192 keys, when it was changed: 94 us to 50).
 //
-// Measured (one MI355X; plain reads reach 7.2 TB/s): 32 x 32768 keys, 8 heads of 128, e4m3: 324 us,
-// 6.6 TB/s.  1 x 32768, fp16: 27.6 us, of which 24 the shares and 4.6 the join where each is timed by
-// itself; 18.6 at the read rate.  48 sequences of 0 to 8192, bf16: 41.5 us, 4.7 TB/s, with the rows
+// Measured (one MI355X; plain reads reach 7.2 TB/s): 32 x 32768 keys, 8 heads of 128, e4m3: 323 us,
+// 6.7 TB/s.  1 x 32768, fp16: 27.4 us, of which 24 the shares and 4.6 the join where each is timed by
+// itself; 18.6 at the read rate.  48 sequences of 0 to 8192, bf16: 41 us, 4.7 TB/s, with the rows
 // of a token's heads side by side, 39.5 with each head's rows together.  1 x 509 keys, 32 heads:
 // 8.7 us, latency (time stamps of one workgroup: first loads out at 3.0, first tile done at 5.8,
 // the second at 7.0, waves joined and stored at 8.6).
@@ -49,8 +51,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kJoinThreads = 256;
 // Waves per workgroup: two per SIMD leave a wave 256 registers, one leaves 512, which the widest
 // 16-bit heads need: 8 x 8192 keys of 256 took 30 us with four waves and 55 with eight, which
-// spill (before keys went through LDS, where those of eight would not fit).  The others lose
-// with four where latency counts (1 x 509 keys 8.7 to 11.4 us, 256 x 64 18.5 to 19.8) and gain 1 to
+// spill (before keys went through LDS, where those of eight would not fit).  8-bit heads of 192 and 256
+// keep six to eight registers in scratch with eight waves (28 to 36 bytes a lane; 8 x 8192 keys 21.2 and
+// 24.3 us); four were not timed for them.  The others lose with four where latency counts (1 x 509 keys 8.7 to 11.4 us, 256 x 64 18.5 to 19.8) and gain 1 to
 // 2% at best (32 x 32768 e4m3 325 to 321).
 constexpr int waves_of(bool narrow, int dim) { return !narrow && dim >= 192 ? 4 : 8; }
 constexpr int kMaxShares = 256;
@@ -407,7 +410,9 @@ __device__ inline Keys keys_of(const AttnArgs& a, int n) {
 
 // The sequences laid end to end, each as kSeqCost units and then one per tile, cut into a.shares
 // equal shares (the units fit 31 bits).  Every wave finds its place by itself: lane l holds
-// sequence base + l, and a scan over the lanes gives where each ends.
+// sequence base + l, and a scan over the lanes gives where each ends.  Past 64 sequences that is a
+// chain of loads, one for every 64, in each wave of both launches: 1024 sequences of 32 keys (one key
+// head of 64) take 19 us, 4096 take 60, 16384 take 283, a microsecond for every 64.
 template <int WAVES>
 struct Line {
   int base, len;     // this lane's sequence: base + lane
@@ -651,7 +656,8 @@ __global__ __launch_bounds__(64 * waves_of(NARROW, D)) void attention_kernel(Att
 // Joins the pieces of a sequence that was cut: one workgroup per cut and head, of which that of
 // the sequence's first cut works.  A launch of its own, 4 us: joined by the last workgroup to
 // arrive, through a counter and writes past the L2s, 1 x 32768 took 29.6 us against 28.4, and the
-// workspace would have to be kept zeroed.  A share writes at most two pieces of a head: the end of a
+// workspace would have to be kept zeroed.  Heads of 64 keep eight registers in scratch under the
+// launch bound.  A share writes at most two pieces of a head: the end of a
 // sequence (0) and the beginning of another (1).
 template <class T, bool NARROW, int D>
 __global__ __launch_bounds__(kJoinThreads, 8) void attention_join_kernel(AttnArgs a) {

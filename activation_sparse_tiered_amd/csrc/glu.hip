@@ -3,7 +3,7 @@
 // The tanh form is the same with another argument: (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), so
 // act(g) = g / (1 + exp(-2u)), u = sqrt(2/pi) (g + 0.044715 g^3): no cancellation near tanh = -1.
 // Bound: bytes (three rows move, nothing is reused) or, for one row, launch latency.  Measured: 2048
-// x 14336 bf16: 33.9 us, 5.2 TB/s (a large copy reaches 5.1); 1 x 11008: 2.5 us on the device.
+// x 14336 bf16: 32.6 us, 5.4 TB/s (a large copy reaches 5.1); 1 x 11008: 2.4 us on the device.
 #include "layer_ops.h"
 
 namespace spax {

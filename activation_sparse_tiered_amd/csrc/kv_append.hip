@@ -11,7 +11,7 @@
 // over heads; a token's sines are computed once per workgroup, a pair per thread.
 //
 // Measured: 4099 tokens of 32 + 8 + 8 heads of 128, fp16 to e4m3, 92 MB: 19.6 us, 4.7 TB/s (a large
-// copy reaches 5.1); one token: 2.9 us on the device, a load of the position and one of the page
+// copy reaches 5.1); one token: 2.8 us on the device, a load of the position and one of the page
 // before the stores can go.
 #include "layer_ops.h"
 #include "mask_core.h"
@@ -255,7 +255,8 @@ int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
   a.n_seqs = c.n_seqs; a.n_pages = c.n_pages; a.max_pages = c.max_pages;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   // 16 bytes of a 16-bit head at a time where the rotated part divides into such pieces (the
-  // prompts of 4099 tokens: 20.0 us with pieces of eight pairs, 21.1 of four, 51 of one).
+  // prompts of 4099 tokens: 20.0 us with pieces of eight pairs, 20.6 of four, where 40 values are
+  // rotated, and 59 of one, where 20 are).
   const int pairs = p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
   const int items = pairs > 1 ? a.dim / (2 * pairs) : p->rot_dim / 2 + a.dim - p->rot_dim;
   a.heads_at_once = kAppendThreads / items;

@@ -549,8 +549,9 @@ int spax_kv_append(const spax_kv_append_args* a, hipStream_t stream);
  *   ws      : spax_attention_workspace_bytes(a) bytes (0: none needed), 256-byte aligned, any
  *             contents; calls that may run at the same time need a workspace each.
  * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (as for the cache; n_heads not a multiple of
- * n_kv_heads; max_len < 1, past max_pages * page_size or past 2^30; 2^30 or more tiles of 32
- * keys in n_seqs sequences of max_len; window < 0); SPAX_ERR_UNSUPPORTED
+ * n_kv_heads or past 65535; max_len < 1, past max_pages * page_size or past 2^30; more than 2^30
+ * tiles of 32 keys in n_seqs sequences of max_len, or of window, each counted as four tiles more;
+ * window < 0); SPAX_ERR_UNSUPPORTED
  * (types); SPAX_ERR_ALIGN; SPAX_ERR_PARAM (scale not finite, overlapping buffers);
  * SPAX_ERR_WORKSPACE; SPAX_ERR_HIP.
  */
@@ -581,7 +582,8 @@ enum { SPAX_NORM_RMS = 0, SPAX_NORM_LAYER = 1 };
  * residual_out gets h, x the normed row; either may be NULL, not both.  residual or block may be
  * NULL (0 is taken), not both; residual_out may be residual itself (type and stride alike), x
  * may be block itself likewise.  gate: gate_type, one row (gate_stride 0) or one per row.
- * Weights and biases are fp32 rows of d (weight NULL: ones for pre, no norm for post).
+ * Weights and biases are fp32 rows of d (weight NULL: ones for pre, no norm for post).  Squares are
+ * summed in 32 bits: values of 2^56 and more (with eps 0 also rows below 2^-56) are past a norm's range.
  *   residual, residual_out : residual_type; block : block_type (SPAX_F32, SPAX_F16, SPAX_BF16);
  *   x : x_type (the same three).  1 <= d <= 32768; n_rows 0 does nothing, and 2^32 threads of
  *   eight values (rows rounded up to 64 of them) are the most.
