@@ -53,8 +53,8 @@ constexpr int kJoinThreads = 256;
 // 16-bit heads need: 8 x 8192 keys of 256 took 30 us with four waves and 55 with eight, which
 // spill (before keys went through LDS, where those of eight would not fit).  8-bit heads of 192 and 256
 // keep six to eight registers in scratch with eight waves (28 to 36 bytes a lane; 8 x 8192 keys 21.2 and
-// 24.3 us); four were not timed for them.  The others lose with four where latency counts (1 x 509 keys 8.7 to 11.4 us, 256 x 64 18.5 to 19.8) and gain 1 to
-// 2% at best (32 x 32768 e4m3 325 to 321).
+// 24.3 us); four were not timed for them.  The others lose with four where latency counts (1 x 509
+// keys 8.7 to 11.4 us, 256 x 64 18.5 to 19.8) and gain 1 to 2% at best (32 x 32768 e4m3 325 to 321).
 constexpr int waves_of(bool narrow, int dim) { return !narrow && dim >= 192 ? 4 : 8; }
 constexpr int kMaxShares = 256;
 // What a sequence costs besides its keys, in tiles, and the most tiles of a sequence that a wave
