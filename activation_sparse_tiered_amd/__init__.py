@@ -16,6 +16,8 @@ STEP_DEFAULT, STEP_SEPARATE, STEP_BATCHED, STEP_DETERMINISTIC = 0, 1, 2, 4
 from ._lib import (ACT_GELU_TANH, ACT_SILU, NORM_LAYER, NORM_RMS, TYPE_BF16,  # noqa: F401
                    TYPE_E4M3, TYPE_F16, TYPE_F32, AttentionArgs, DecoderLayer, GluArgs,
                    KvAppendArgs, KvCache, ResidualNormArgs)
+from ._lib import (GEMM_ACT, GEMM_GATED, GEMM_PLAIN, ChunkAttentionArgs,  # noqa: F401
+                   HeadNorm, PackedGemmArgs)
 from ._lib import (FMT_FP16, FMT_INT4, MAX_DIN, MAX_MATS, MODE_THRESHOLD, MODE_TOPK,  # noqa: F401
                    MODE_TOPK_GUIDED, TIER_APPROX, TIER_FULL, TIER_SKIP, BLOCK_ERROR_FN,
                    SPAX_ERR_WORKSPACE, Layout, MoveStats, Phase, SpaxError, Step, StorageStats,
@@ -37,6 +39,10 @@ __all__ = [
     "make_kv_cache", "make_kv_append", "make_attention", "make_residual_norm", "make_glu",
     "make_layer", "layer_array", "KvCache", "KvAppendArgs", "AttentionArgs", "ResidualNormArgs",
     "GluArgs", "DecoderLayer",
+    "spax_kv_append_normed", "spax_chunk_attention_workspace_bytes", "spax_chunk_attention",
+    "spax_packed_gemm_workspace_bytes", "spax_packed_gemm", "make_head_norm",
+    "make_chunk_attention", "make_packed_gemm", "HeadNorm", "ChunkAttentionArgs",
+    "PackedGemmArgs",
 ]
 
 
@@ -459,6 +465,52 @@ def spax_kv_append(args: KvAppendArgs, stream=None) -> None:
     _call(lib.spax_kv_append, "spax_kv_append", args, stream, args)
 
 
+def make_head_norm(q_weight, k_weight, q_bias=None, k_bias=None, kind: str = "rms",
+                   eps: float = 1e-6) -> HeadNorm:
+    """The norm of every query and key head before its rotation: weights fp32 [head_dim] for all
+    heads or [n_heads, head_dim] (None: those heads are not normed), biases shaped like their
+    weights.  kind: 'rms' or 'layer'."""
+    m = HeadNorm()
+    m._shapes = {}
+    for part, weight, bias in (("q", q_weight, q_bias), ("k", k_weight, k_bias)):
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t is None:
+                continue
+            if str(t.dtype) != "torch.float32":
+                raise TypeError(f"{part}_{name} is {t.dtype}, not torch.float32")
+            _rows(t, f"{part}_{name}", 1 if t.dim() == 1 else 2)
+            if weight is None:
+                raise ValueError(f"{part}_bias without {part}_weight")
+            _same_shape(t, f"{part}_{name}", weight.shape)
+            if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != weight.stride(0):
+                raise ValueError(f"{part}_bias and {part}_weight have different strides")
+            setattr(m, f"{part}_{name}", t.data_ptr())
+        if weight is not None:
+            each = weight.dim() == 2 and weight.shape[0] > 1
+            setattr(m, f"{part}_stride", weight.stride(0) if each else 0)
+            m._shapes[part] = tuple(weight.shape)
+    if not m._shapes:
+        raise ValueError("no weights given")
+    m.kind, m.eps = _NORMS.get(kind, kind), float(eps)
+    return _keep(m, q_weight, k_weight, q_bias, k_bias)
+
+
+def _norm_fits(norm: HeadNorm, args: KvAppendArgs) -> None:
+    cache = args._keep[1][0]
+    for part, shape in norm._shapes.items():
+        heads = args.n_heads if part == "q" else cache.n_kv_heads
+        if shape[-1] != cache.head_dim or (len(shape) == 2 and shape[0] != heads):
+            raise ValueError(f"{part}_weight has shape {shape}, for {heads} heads of "
+                             f"{cache.head_dim}")
+    if norm._device != args._device:
+        raise ValueError(f"the norm is on {norm._device}, the tensors are on {args._device}")
+
+
+def spax_kv_append_normed(args: KvAppendArgs, norm: HeadNorm, stream=None) -> None:
+    _norm_fits(norm, args)
+    _call(lib.spax_kv_append_normed, "spax_kv_append_normed", args, stream, args, norm)
+
+
 def make_attention(cache: KvCache, q, lens, out, max_len: int | None = None,
                    scale: float | None = None, window: int = 0, lse=None) -> AttentionArgs:
     """q and out [n_seqs, n_heads, head_dim], lens int32 [n_seqs] (keys of each sequence, the new
@@ -494,6 +546,48 @@ def spax_paged_attention(args: AttentionArgs, ws=None, ws_bytes: int | None = No
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
     _call(lib.spax_paged_attention, "spax_paged_attention", args, stream, args, _ptr(ws),
+          ws_bytes)
+
+
+def make_chunk_attention(cache: KvCache, q, starts, lens, out, max_len: int | None = None,
+                         scale: float | None = None, window: int = 0,
+                         lse=None) -> ChunkAttentionArgs:
+    """q and out [n_tokens, n_heads, head_dim], the new tokens of all sequences one after another;
+    starts int32 [n_seqs + 1] (where each sequence's begin, and where the last one's end), lens
+    int32 [n_seqs] (keys of each sequence, its new tokens' own among them), lse fp32
+    [n_tokens, n_heads] or None.  max_len: bound on lens (default: what the page table holds);
+    scale: default 1 / sqrt(head_dim)."""
+    _rows(q, "q", 3)
+    _rows(out, "out", 3)
+    _same_shape(q, "q", (q.shape[0], q.shape[1], cache.head_dim))
+    _same_shape(out, "out", q.shape)
+    if q.dtype != out.dtype:
+        raise TypeError(f"out is {out.dtype}, q is {q.dtype}")
+    a = ChunkAttentionArgs()
+    a.cache = C.pointer(cache)
+    a.q, a.out, a.type = q.data_ptr(), out.data_ptr(), _type_of(q)
+    a.n_tokens, a.n_heads = _int32(q.shape[0], "n_tokens"), _int32(q.shape[1], "n_heads")
+    a.q_token_stride, a.q_head_stride = q.stride()[:2]
+    a.out_token_stride, a.out_head_stride = out.stride()[:2]
+    a.starts = _ptr(_flat(starts, "starts", cache.n_seqs + 1, "torch.int32"))
+    a.lens = _ptr(_flat(lens, "lens", cache.n_seqs, "torch.int32"))
+    a.lse = _ptr(_flat(lse, "lse", a.n_tokens * a.n_heads, "torch.float32"))
+    a.max_len = _int32(cache.max_pages * cache.page_size if max_len is None else max_len, "max_len")
+    a.scale = float(cache.head_dim ** -0.5 if scale is None else scale)
+    a.window = _int32(window, "window")
+    return _keep(a, q, starts, lens, out, lse, parts=(cache,))
+
+
+def spax_chunk_attention_workspace_bytes(args: ChunkAttentionArgs) -> int:
+    return int(lib.spax_chunk_attention_workspace_bytes(C.byref(args)))
+
+
+def spax_chunk_attention(args: ChunkAttentionArgs, ws=None, ws_bytes: int | None = None,
+                         stream=None) -> None:
+    _workspace(ws, args)
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    _call(lib.spax_chunk_attention, "spax_chunk_attention", args, stream, args, _ptr(ws),
           ws_bytes)
 
 
@@ -567,16 +661,70 @@ def spax_glu(args: GluArgs, stream=None) -> None:
     _call(lib.spax_glu, "spax_glu", args, stream, args)
 
 
+def make_packed_gemm(layout: Layout, packed, x, y, bias=None, act: str | None = None,
+                     gated: bool = False, residual=None, scale: float = 1.0) -> PackedGemmArgs:
+    """y = residual + scale * u, u from t = x W^T + bias by the blob's original columns: t itself,
+    act(t), or, gated, act of the first matrix's columns times the second's.  x float16
+    [n_rows, d_in] (rows on 16 bytes), y and residual [n_rows, d_out_total], or d_out[0] columns
+    gated, bias fp32 [d_out_total], packed a uint8 tensor of the layout's bytes."""
+    _rows(x, "x", 2)
+    _rows(y, "y", 2)
+    if str(x.dtype) != "torch.float16":
+        raise TypeError(f"x is {x.dtype}, not torch.float16")
+    if gated and act is None:
+        raise ValueError("gated needs an activation")
+    total = int(layout.d_out_total)
+    width = int(layout.d_out[0]) if gated else total
+    _same_shape(x, "x", (x.shape[0], layout.d_in))
+    _same_shape(y, "y", (x.shape[0], width))
+    if not packed.is_contiguous() or _nbytes(packed) < layout.total_bytes:
+        raise ValueError(f"packed is not a contiguous tensor of {int(layout.total_bytes)} bytes")
+    a = PackedGemmArgs()
+    a.layout = C.pointer(layout)
+    a.packed, a.x, a.y = packed.data_ptr(), x.data_ptr(), y.data_ptr()
+    a.x_stride, a.y_stride = x.stride(0), y.stride(0)
+    a.bias = _ptr(_flat(bias, "bias", total, "torch.float32"))
+    a.y_type = _type_of(y)
+    if residual is not None:
+        _rows(residual, "residual", 2)
+        _same_shape(residual, "residual", y.shape)
+        a.residual, a.residual_type = residual.data_ptr(), _type_of(residual)
+        a.residual_stride = residual.stride(0)
+    a.n_rows = _int32(x.shape[0], "n_rows")
+    a.form = GEMM_GATED if gated else GEMM_PLAIN if act is None else GEMM_ACT
+    a.act = ACT_SILU if act is None else _ACTS.get(act, act)
+    a.scale = float(scale)
+    _keep(a, packed, x, y, bias, residual)
+    a._layout = layout
+    return a
+
+
+def spax_packed_gemm_workspace_bytes(args: PackedGemmArgs) -> int:
+    return int(lib.spax_packed_gemm_workspace_bytes(C.byref(args)))
+
+
+def spax_packed_gemm(args: PackedGemmArgs, ws=None, ws_bytes: int | None = None,
+                     stream=None) -> None:
+    _workspace(ws, args)
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    _call(lib.spax_packed_gemm, "spax_packed_gemm", args, stream, args, _ptr(ws), ws_bytes)
+
+
 def make_layer(qkv: Phase, append: KvAppendArgs, attention: AttentionArgs, o: Phase,
                attn_norm: ResidualNormArgs, gate_up: Phase, glu: GluArgs, down: Phase,
-               mlp_norm: ResidualNormArgs) -> DecoderLayer:
-    """One decoder layer of spax_decode_layers, in the order in which its parts run."""
+               mlp_norm: ResidualNormArgs, head_norm: HeadNorm | None = None) -> DecoderLayer:
+    """One decoder layer of spax_decode_layers, in the order in which its parts run; head_norm: of
+    the append's query and key heads (make_head_norm)."""
     parts = dict(qkv=qkv, append=append, attention=attention, o=o, attn_norm=attn_norm,
                  gate_up=gate_up, glu=glu, down=down, mlp_norm=mlp_norm)
     L = DecoderLayer()
     for name, p in parts.items():
         setattr(L, name, C.pointer(p))
     L._keep = parts
+    L._norm = head_norm
+    if head_norm is not None:
+        _norm_fits(head_norm, append)
     devices = {p._device for p in (append, attention, attn_norm, glu, mlp_norm)}
     for p in (qkv, o, gate_up, down):
         devices |= {t.device for t in getattr(p, "_keep", ()) if hasattr(t, "device")}
@@ -588,6 +736,12 @@ def make_layer(qkv: Phase, append: KvAppendArgs, attention: AttentionArgs, o: Ph
 def layer_array(layers):
     arr = (DecoderLayer * len(layers))(*layers)
     arr._keep = [L._keep for L in layers]
+    norms = [getattr(L, "_norm", None) for L in layers]
+    arr._norms = None
+    if any(m is not None for m in norms):
+        arr._norms = (C.POINTER(HeadNorm) * len(layers))(
+            *[C.POINTER(HeadNorm)() if m is None else C.pointer(m) for m in norms])
+        arr._keep_norms = norms
     devices = {L._device for L in layers}
     if len(devices) != 1:
         raise ValueError(f"{len(layers)} layers on {len(devices)} devices")
@@ -607,6 +761,11 @@ def spax_decode_layers(layers, ws, ws_bytes: int | None = None, flags: int = 0,
     _workspace(ws, arr)
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
+    norms = getattr(arr, "_norms", None)
+    if norms is not None:
+        _call(lib.spax_decode_layers_normed, "spax_decode_layers_normed", arr, stream, arr,
+              norms, len(arr), int(flags), _ptr(ws), int(ws_bytes))
+        return
     _call(lib.spax_decode_layers, "spax_decode_layers", arr, stream, arr, len(arr),
           int(flags), _ptr(ws), int(ws_bytes))
 

@@ -61,6 +61,7 @@ class Step(C.Structure):
 TYPE_F32, TYPE_F16, TYPE_BF16, TYPE_E4M3 = 0, 1, 2, 3
 NORM_RMS, NORM_LAYER = 0, 1
 ACT_SILU, ACT_GELU_TANH = 0, 1
+GEMM_PLAIN, GEMM_ACT, GEMM_GATED = 0, 1, 2
 
 
 def _struct(pointers=(), strides=(), ints=(), floats=(), pad=False, first=()):
@@ -105,6 +106,26 @@ class ResidualNormArgs(C.Structure):
 class GluArgs(C.Structure):
     _fields_ = _struct(("gate", "up", "x"), ("gate_stride", "up_stride", "x_stride"),
                        ("src_type", "x_type", "act", "n_rows", "d"), pad=True)
+
+
+class HeadNorm(C.Structure):
+    _fields_ = _struct(("q_weight", "q_bias", "k_weight", "k_bias"), ("q_stride", "k_stride"),
+                       ("kind",), ("eps",))
+
+
+class ChunkAttentionArgs(C.Structure):
+    _fields_ = _struct(("q", "out", "lse", "starts", "lens"),
+                       ("q_token_stride", "q_head_stride", "out_token_stride",
+                        "out_head_stride"),
+                       ("type", "n_heads", "n_tokens", "max_len", "window"), ("scale",),
+                       first=[("cache", C.POINTER(KvCache))])
+
+
+class PackedGemmArgs(C.Structure):
+    _fields_ = _struct(("packed", "x", "bias", "residual", "y"),
+                       ("x_stride", "residual_stride", "y_stride"),
+                       ("n_rows", "form", "act", "residual_type", "y_type"), ("scale",),
+                       first=[("layout", C.POINTER(Layout))])
 
 
 class DecoderLayer(C.Structure):
@@ -174,11 +195,19 @@ def _load():
         "spax_kv_append": (C.c_int, [C.POINTER(KvAppendArgs), P]),
         "spax_attention_workspace_bytes": (C.c_size_t, [C.POINTER(AttentionArgs)]),
         "spax_paged_attention": (C.c_int, [C.POINTER(AttentionArgs), P, C.c_size_t, P]),
+        "spax_kv_append_normed": (C.c_int, [C.POINTER(KvAppendArgs), C.POINTER(HeadNorm), P]),
+        "spax_chunk_attention_workspace_bytes": (C.c_size_t, [C.POINTER(ChunkAttentionArgs)]),
+        "spax_chunk_attention": (C.c_int, [C.POINTER(ChunkAttentionArgs), P, C.c_size_t, P]),
+        "spax_packed_gemm_workspace_bytes": (C.c_size_t, [C.POINTER(PackedGemmArgs)]),
+        "spax_packed_gemm": (C.c_int, [C.POINTER(PackedGemmArgs), P, C.c_size_t, P]),
         "spax_residual_norm": (C.c_int, [C.POINTER(ResidualNormArgs), P]),
         "spax_glu": (C.c_int, [C.POINTER(GluArgs), P]),
         "spax_layers_workspace_bytes": (C.c_size_t, [C.POINTER(DecoderLayer), C.c_int32]),
         "spax_decode_layers": (C.c_int, [C.POINTER(DecoderLayer), C.c_int32, C.c_int32, P,
                                          C.c_size_t, P]),
+        "spax_decode_layers_normed": (C.c_int, [C.POINTER(DecoderLayer),
+                                                C.POINTER(C.POINTER(HeadNorm)), C.c_int32,
+                                                C.c_int32, P, C.c_size_t, P]),
         "spax_column_ranges": (C.c_int, [P, C.c_int32, C.c_int32, P, P, C.POINTER(C.c_int32)]),
         "spax_pinned_workspace_bytes": (C.c_size_t, [C.POINTER(Layout)]),
         "spax_storage_ledger": (C.c_int, [C.POINTER(Layout), P, C.c_int32, P, C.c_int32,

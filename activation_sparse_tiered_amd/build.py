@@ -31,7 +31,8 @@ FLAGS = [
 ]
 SOURCES = ["host.cpp", "api.cpp", "pack.hip", "tiers.hip", "gemv.hip", "decode.hip", "batch.hip",
            "pinned.cpp", "probe.hip", "budgets.cpp", "api_layer.cpp", "layers.cpp",
-           "kv_append.hip", "attention.hip", "norm.hip", "glu.hip"]
+           "kv_append.hip", "attention.hip", "chunk_attention.hip", "norm.hip", "glu.hip",
+           "packed_gemm.hip"]
 
 
 def hipcc() -> str:

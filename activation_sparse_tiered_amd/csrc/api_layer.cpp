@@ -153,6 +153,41 @@ bool rows_apart(const spax_kv_cache& c) {
   return strides_ok(n, s, 4, c.head_dim);
 }
 
+int check_head_norm(const spax_head_norm& m, const spax_kv_append_args& a, int64_t d) {
+  if (!m.q_weight && !m.k_weight && !m.q_bias && !m.k_bias)
+    return fail(SPAX_ERR_NULL, "norm: q_weight or k_weight is required");
+  if (m.kind != SPAX_NORM_RMS && m.kind != SPAX_NORM_LAYER)
+    return fail(SPAX_ERR_UNSUPPORTED, "norm: kind %d", m.kind);
+  if (!aligned(m.q_weight, 4) || !aligned(m.q_bias, 4) || !aligned(m.k_weight, 4) ||
+      !aligned(m.k_bias, 4))
+    return fail(SPAX_ERR_ALIGN, "norm: weights and biases must be 4-byte aligned");
+  if (!std::isfinite(m.eps) || m.eps < 0.0f)
+    return fail(SPAX_ERR_PARAM, "norm: eps must be finite and >= 0");
+  if ((m.q_bias && !m.q_weight) || (m.k_bias && !m.k_weight))
+    return fail(SPAX_ERR_PARAM, "norm: a bias needs its weight");
+  if (m.q_weight && a.n_heads == 0)
+    return fail(SPAX_ERR_PARAM, "norm: q_weight needs q");
+  if ((m.q_weight && ((m.q_stride != 0 && m.q_stride < d) || !stride_range(a.n_heads, m.q_stride))) ||
+      (m.k_weight &&
+       ((m.k_stride != 0 && m.k_stride < d) || !stride_range(a.cache->n_kv_heads, m.k_stride))))
+    return fail(SPAX_ERR_PARAM, "norm: a stride is neither 0 nor from %lld up, or out of range",
+                (long long)d);
+  return SPAX_OK;
+}
+
+// A workspace that an operator needs: there, aligned, large enough, apart from its buffers.
+int check_workspace(const Spans& b, const void* ws, size_t ws_bytes, size_t need) {
+  if (!need) return SPAX_OK;
+  if (!ws) return fail(SPAX_ERR_NULL, "workspace is NULL");
+  if (!aligned(ws, 256)) return fail(SPAX_ERR_ALIGN, "ws must be 256-byte aligned");
+  if (ws_bytes < need)
+    return fail(SPAX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
+  for (int i = 0; i < b.n; ++i)
+    if (overlaps(ws, need, b.s[i].p, b.s[i].bytes))
+      return fail(SPAX_ERR_PARAM, "the workspace overlaps %s", b.s[i].name);
+  return SPAX_OK;
+}
+
 }  // namespace
 
 bool shares(const Span& x, const Span& y) {
@@ -165,7 +200,7 @@ bool shares(const Span& x, const Span& y) {
   return at < x.row || at + y.row > step;
 }
 
-int check_kv_append(const spax_kv_append_args* a, Spans* spans) {
+int check_kv_append(const spax_kv_append_args* a, const spax_head_norm* m, Spans* spans) {
   if (!a) return fail(SPAX_ERR_NULL, "args is NULL");
   int st = check_cache(a->cache);
   if (st) return st;
@@ -200,6 +235,7 @@ int check_kv_append(const spax_kv_append_args* a, Spans* spans) {
       !aligned(a->positions, 4) || !aligned(a->seq, 4) || !aligned(a->inv_freq, 4))
     return fail(SPAX_ERR_ALIGN, "a pointer is not aligned to its element");
   const int64_t n = a->n_tokens, d = c.head_dim;
+  if (m && (st = check_head_norm(*m, *a, d))) return st;
   if ((st = check_rows2("q", n, a->q_token_stride, a->n_heads, a->q_head_stride, d, false)) ||
       (st = check_rows2("k", n, a->k_token_stride, c.n_kv_heads, a->k_head_stride, d, false)) ||
       (st = check_rows2("v", n, a->v_token_stride, c.n_kv_heads, a->v_head_stride, d, false)) ||
@@ -220,8 +256,16 @@ int check_kv_append(const spax_kv_append_args* a, Spans* spans) {
     b.add(a->seq, 4 * (size_t)n, false, "seq");
     b.add(a->inv_freq, 2 * (size_t)a->rot_dim, false, "inv_freq");
     add_cache(&c, true, &b);
+    if (m) {
+      const int64_t nq = m->q_stride ? a->n_heads : 1, nk = m->k_stride ? c.n_kv_heads : 1;
+      add_rows(&b, m->q_weight, nq, m->q_stride, 1, 0, d, SPAX_F32, false, "q_weight");
+      add_rows(&b, m->q_bias, nq, m->q_stride, 1, 0, d, SPAX_F32, false, "q_bias");
+      add_rows(&b, m->k_weight, nk, m->k_stride, 1, 0, d, SPAX_F32, false, "k_weight");
+      add_rows(&b, m->k_bias, nk, m->k_stride, 1, 0, d, SPAX_F32, false, "k_bias");
+    }
   }
-  // q may be rotated in place: a thread reads both values of a pair before it writes them
+  // q may be rotated in place: a thread reads its values of a head, and a head's threads have all
+  // read theirs where it is normed, before any is written
   const bool in_place = a->q == a->q_out && a->src_type == a->out_type &&
                         a->q_token_stride == a->out_token_stride &&
                         a->q_head_stride == a->out_head_stride;
@@ -390,14 +434,122 @@ int check_glu(const spax_glu_args* a, Spans* spans) {
   return SPAX_OK;
 }
 
+int check_chunk_attention(const spax_chunk_attention_args* a, Spans* spans) {
+  if (!a) return fail(SPAX_ERR_NULL, "args is NULL");
+  int st = check_cache(a->cache);
+  if (st) return st;
+  const spax_kv_cache& c = *a->cache;
+  if (a->n_tokens != 0 && (!a->q || !a->out || !a->starts || !a->lens))
+    return fail(SPAX_ERR_NULL, "q, out, starts and lens are required");
+  if (a->type != SPAX_F16 && a->type != SPAX_BF16)
+    return fail(SPAX_ERR_UNSUPPORTED, "type %d", a->type);
+  if (c.type != a->type && c.type != SPAX_E4M3)
+    return fail(SPAX_ERR_UNSUPPORTED, "type %d with a cache of type %d", a->type, c.type);
+  if (a->n_heads < 1 || a->n_heads > 65535 || a->n_heads % c.n_kv_heads)
+    return fail(SPAX_ERR_SHAPE, "n_heads %d is not a multiple of n_kv_heads %d in 1..65535",
+                a->n_heads, c.n_kv_heads);
+  if (a->n_tokens < 0 || (int64_t)a->n_tokens * a->n_heads > (1 << 30))
+    return fail(SPAX_ERR_SHAPE, "n_tokens %d of %d heads outside 0..2^30 rows", a->n_tokens,
+                a->n_heads);
+  if (a->max_len < 1 || a->max_len > (int64_t)c.max_pages * c.page_size || a->max_len > (1 << 30))
+    return fail(SPAX_ERR_SHAPE, "max_len %d outside 1..%lld", a->max_len,
+                (long long)c.max_pages * c.page_size);
+  if (a->window < 0) return fail(SPAX_ERR_SHAPE, "window %d < 0", a->window);
+  if (!std::isfinite(a->scale)) return fail(SPAX_ERR_PARAM, "scale is not finite");
+  if (!aligned(a->q, 16) || !aligned(a->out, 16) || a->q_token_stride % 8 ||
+      a->q_head_stride % 8 || a->out_token_stride % 8 || a->out_head_stride % 8)
+    return fail(SPAX_ERR_ALIGN, "q and out must be 16-byte aligned, their strides multiples of 8");
+  if (!aligned(a->lens, 4) || !aligned(a->starts, 4) || !aligned(a->lse, 4))
+    return fail(SPAX_ERR_ALIGN, "starts, lens and lse must be 4-byte aligned");
+  const int64_t n = a->n_tokens, d = c.head_dim;
+  if ((st = check_rows2("q", n, a->q_token_stride, a->n_heads, a->q_head_stride, d, false)) ||
+      (st = check_rows2("out", n, a->out_token_stride, a->n_heads, a->out_head_stride, d, true)))
+    return st;
+  if (chunk_plan(a).blocks >= 1 << 23)  // a grid holds 2^32 threads
+    return fail(SPAX_ERR_SHAPE, "%d tokens of %d sequences are too many", a->n_tokens, c.n_seqs);
+  Spans b;
+  if (n > 0) {
+    add_rows(&b, a->q, n, a->q_token_stride, a->n_heads, a->q_head_stride, d, a->type, false, "q");
+    add_rows(&b, a->out, n, a->out_token_stride, a->n_heads, a->out_head_stride, d, a->type, true,
+             "out");
+    b.add(a->lse, 4 * (size_t)n * (size_t)a->n_heads, true, "lse");
+    b.add(a->starts, 4 * ((size_t)c.n_seqs + 1), false, "starts");
+    b.add(a->lens, 4 * (size_t)c.n_seqs, false, "lens");
+    add_cache(&c, false, &b);
+  }
+  if ((st = check_overlaps(b, [](const Span&, const Span&) { return false; }))) return st;
+  if (spans) *spans = b;
+  return SPAX_OK;
+}
+
+int check_packed_gemm(const spax_packed_gemm_args* a, Spans* spans) {
+  if (!a || !a->layout) return fail(SPAX_ERR_NULL, "args or layout is NULL");
+  const spax_layout& L = *a->layout;
+  if (!layout_ok(&L)) return fail(SPAX_ERR_SHAPE, "layout is not initialised");
+  if (a->n_rows != 0 && (!a->packed || !a->x || !a->y))
+    return fail(SPAX_ERR_NULL, "packed, x and y are required");
+  if (a->form < SPAX_GEMM_PLAIN || a->form > SPAX_GEMM_GATED)
+    return fail(SPAX_ERR_UNSUPPORTED, "form %d", a->form);
+  if (a->form != SPAX_GEMM_PLAIN && a->act != SPAX_ACT_SILU && a->act != SPAX_ACT_GELU_TANH)
+    return fail(SPAX_ERR_UNSUPPORTED, "act %d", a->act);
+  if (!is_float_type(a->y_type) || (a->residual && !is_float_type(a->residual_type)))
+    return fail(SPAX_ERR_UNSUPPORTED, "types %d, %d", a->residual_type, a->y_type);
+  const bool gated = a->form == SPAX_GEMM_GATED;
+  if (gated && (L.n_mats != 2 || L.d_out[0] != L.d_out[1]))
+    return fail(SPAX_ERR_SHAPE, "GATED needs two matrices of equal d_out");
+  if (a->n_rows < 0 || a->n_rows >= 1 << 20)
+    return fail(SPAX_ERR_SHAPE, "n_rows %d outside 0..2^20 - 1", a->n_rows);
+  if (!std::isfinite(a->scale)) return fail(SPAX_ERR_PARAM, "scale is not finite");
+  if (!aligned(a->packed, 256)) return fail(SPAX_ERR_ALIGN, "packed must be 256-byte aligned");
+  if (!aligned(a->x, 16) || (a->n_rows > 1 && a->x_stride % 8))
+    return fail(SPAX_ERR_ALIGN, "x must be 16-byte aligned, its stride a multiple of 8");
+  if (!aligned(a->bias, 4) || !aligned(a->y, (size_t)elem::bytes_of(a->y_type)) ||
+      !aligned(a->residual, a->residual ? (size_t)elem::bytes_of(a->residual_type) : 1))
+    return fail(SPAX_ERR_ALIGN, "a pointer is not aligned to its element");
+  const int64_t n = a->n_rows, d = gated ? L.d_out[0] : L.d_out_total;
+  if (n > 1 && (a->x_stride < L.d_in || a->y_stride < d || (a->residual && a->residual_stride < d) ||
+                !stride_range(n, a->x_stride) || !stride_range(n, a->y_stride) ||
+                !stride_range(n, a->residual_stride)))
+    return fail(SPAX_ERR_PARAM, "a stride is below its row or out of range");
+  if (gemm_plan(a).blocks >= 1 << 22)  // a grid holds 2^32 threads
+    return fail(SPAX_ERR_SHAPE, "%d rows of %lld columns are too many", a->n_rows,
+                (long long)L.d_out_total);
+  Spans b;
+  if (n > 0) {
+    b.add(a->packed, (size_t)L.total_bytes, false, "packed");
+    add_rows(&b, a->x, n, a->x_stride, 1, 0, L.d_in, SPAX_F16, false, "x");
+    b.add(a->bias, 4 * (size_t)L.d_out_total, false, "bias");
+    if (a->residual)
+      add_rows(&b, a->residual, n, a->residual_stride, 1, 0, d, a->residual_type, false,
+               "residual");
+    add_rows(&b, a->y, n, a->y_stride, 1, 0, d, a->y_type, true, "y");
+  }
+  // the stream updated in place: a thread reads its own values before it writes them
+  const bool stream = a->residual == a->y && a->residual_type == a->y_type &&
+                      (n == 1 || a->residual_stride == a->y_stride);
+  const int st =
+      check_overlaps(b, [&](const Span&, const Span& y) { return stream && is(y, "residual"); });
+  if (st) return st;
+  if (spans) *spans = b;
+  return SPAX_OK;
+}
+
 }  // namespace spax
 
 extern "C" {
 
 int spax_kv_append(const spax_kv_append_args* a, hipStream_t stream) {
   clear_error();
-  const int st = check_kv_append(a, nullptr);
-  return st ? st : launch_kv_append(a, stream);
+  const int st = check_kv_append(a, nullptr, nullptr);
+  return st ? st : launch_kv_append(a, nullptr, stream);
+}
+
+int spax_kv_append_normed(const spax_kv_append_args* a, const spax_head_norm* norm,
+                          hipStream_t stream) {
+  clear_error();
+  if (!norm) return fail(SPAX_ERR_NULL, "norm is NULL");
+  const int st = check_kv_append(a, norm, nullptr);
+  return st ? st : launch_kv_append(a, norm, stream);
 }
 
 size_t spax_attention_workspace_bytes(const spax_attention_args* a) {
@@ -414,17 +566,8 @@ int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes
   Spans b;
   const int st = check_attention(a, &b);
   if (st) return st;
-  const size_t need = attention_plan(a).ws_bytes;
-  if (need) {
-    if (!ws) return fail(SPAX_ERR_NULL, "workspace is NULL");
-    if (!aligned(ws, 256)) return fail(SPAX_ERR_ALIGN, "ws must be 256-byte aligned");
-    if (ws_bytes < need)
-      return fail(SPAX_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws_bytes, need);
-    for (int i = 0; i < b.n; ++i)
-      if (overlaps(ws, need, b.s[i].p, b.s[i].bytes))
-        return fail(SPAX_ERR_PARAM, "the workspace overlaps %s", b.s[i].name);
-  }
-  return launch_attention(a, ws, stream);
+  const int bad = check_workspace(b, ws, ws_bytes, attention_plan(a).ws_bytes);
+  return bad ? bad : launch_attention(a, ws, stream);
 }
 
 int spax_residual_norm(const spax_residual_norm_args* a, hipStream_t stream) {
@@ -437,6 +580,42 @@ int spax_glu(const spax_glu_args* a, hipStream_t stream) {
   clear_error();
   const int st = check_glu(a, nullptr);
   return st ? st : launch_glu(a, stream);
+}
+
+size_t spax_chunk_attention_workspace_bytes(const spax_chunk_attention_args* a) {
+  if (check_chunk_attention(a, nullptr)) {
+    clear_error();
+    return 0;
+  }
+  return chunk_plan(a).ws_bytes;
+}
+
+int spax_chunk_attention(const spax_chunk_attention_args* a, void* ws, size_t ws_bytes,
+                         hipStream_t stream) {
+  clear_error();
+  Spans b;
+  int st = check_chunk_attention(a, &b);
+  if (st) return st;
+  st = check_workspace(b, ws, ws_bytes, chunk_plan(a).ws_bytes);
+  return st ? st : launch_chunk_attention(a, ws, stream);
+}
+
+size_t spax_packed_gemm_workspace_bytes(const spax_packed_gemm_args* a) {
+  if (check_packed_gemm(a, nullptr)) {
+    clear_error();
+    return 0;
+  }
+  return gemm_plan(a).ws_bytes;
+}
+
+int spax_packed_gemm(const spax_packed_gemm_args* a, void* ws, size_t ws_bytes,
+                     hipStream_t stream) {
+  clear_error();
+  Spans b;
+  int st = check_packed_gemm(a, &b);
+  if (st) return st;
+  st = check_workspace(b, ws, ws_bytes, gemm_plan(a).ws_bytes);
+  return st ? st : launch_packed_gemm(a, ws, stream);
 }
 
 }  // extern "C"

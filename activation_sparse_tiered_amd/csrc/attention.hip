@@ -35,6 +35,7 @@
 // of a token's heads side by side, 39.5 with each head's rows together.  1 x 509 keys, 32 heads:
 // 8.7 us, latency (time stamps of one workgroup: first loads out at 3.0, first tile done at 5.8,
 // the second at 7.0, waves joined and stored at 8.6).
+#include "attn_core.h"
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -42,12 +43,11 @@ namespace spax {
 namespace {
 
 using namespace elem;
+using namespace attn;
 
 // Keys that a wave takes per step.  64 of the narrower rows were no faster: 32 x 32768 e4m3 325.7 us
 // (32: 323.5), 1 x 2000 of dim 64 11.8 (10.8).
 constexpr int kTile = 32;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kJoinThreads = 256;
 // Waves per workgroup: two per SIMD leave a wave 256 registers, one leaves 512, which the widest
 // 16-bit heads need: 8 x 8192 keys of 256 took 30 us with four waves and 55 with eight, which
@@ -76,46 +76,6 @@ struct AttnArgs {
   int32_t max_len, window, shares, lds_waves, k_lds;
   float scale;
 };
-
-// kLift: the exponentials are taken of s - m + kLift (base 2), so the largest is 2^kLift, the most
-// that fp16 holds with room for its rounding.  It cancels in o / l, and lse takes it off again.
-template <class T>
-struct Mma;
-template <>
-struct Mma<f16> {
-  static constexpr float kLift = 15.0f, kUnlift = 0x1p-15f;
-  typedef f16 v8 __attribute__((ext_vector_type(8)));
-  static __device__ inline f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a),
-                                                  __builtin_bit_cast(v8, b), c, 0, 0, 0);
-  }
-  // two e4m3 values (the low or high half of w) as 16-bit ones, exactly
-  template <bool HI>
-  static __device__ inline uint32_t widen(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
-  }
-  typedef f16x2 v2;
-};
-template <>
-struct Mma<bf16> {
-  static constexpr float kLift = 0.0f, kUnlift = 1.0f;
-  typedef bf16 v8 __attribute__((ext_vector_type(8)));
-  static __device__ inline f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a),
-                                                   __builtin_bit_cast(v8, b), c, 0, 0, 0);
-  }
-  template <bool HI>
-  static __device__ inline uint32_t widen(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
-  }
-  typedef bf16x2 v2;
-};
-
-// ln of the sum of exponentials whose largest exponent is m (base 2) and whose lifted sum is l.
-template <class T>
-__device__ inline float lse_of(float m, float l) {
-  return l == 0.0f ? -INFINITY : (m + log2f(l * Mma<T>::kUnlift)) * kLn2;
-}
 
 // The cache is read once, so its loads are marked as not worth keeping: 1 x 32768 keys 31.0 us
 // without, 27.6 with; 48 ragged 45.7 and 41.5; 32 x 32768 e4m3 330 and 325.

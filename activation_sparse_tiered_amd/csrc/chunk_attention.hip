@@ -1,0 +1,595 @@
+// spax_chunk_attention: a chunk of new query tokens per sequence over a paged cache, causal.
+//
+// A sequence's query rows for one key head, tokens times the group's heads, are laid end to end and
+// cut into tiles of 128, so any group fills them.  Per row with keys k_j, values v_j, in one pass:
+//   s_j = scale q.k_j,  m = running max of s,  p = exp(s - m),
+//   l <- l exp(m_old - m) + sum p,   o <- o exp(m_old - m) + sum p v,   out = o / l.
+// Pieces of a tile's keys (m, l, o) join by the same rule.
+//
+// A workgroup of four waves takes a tile, 32 rows a wave, and walks over its keys, kKeys at a time,
+// which pass through LDS once for all four:
+//   * S^T = K Q^T by 32x32x16 matrix instructions, keys as rows, query rows as columns.
+//   * S^T's layout (lane: one row, keys 8 b + 4 h + i) is that of the second product's P operand if
+//     that product counts keys in the order {4 h + i, 8 + 4 h + i} of every 16, so probabilities
+//     never cross lanes and a row's maximum and sum are in two lanes.
+//   * O^T = V^T P^T: eight keys of one dim come from LDS by transposing reads of four rows.
+//   * p enters the product as one 16-bit value, in fp16 lifted by 2^15 (Mma::kLift): splitting it
+//     in two, as the attention of single tokens does, would add half of the matrix work again where
+//     that is the bound, for an error that is about that of rounding the result.
+//   * Masked keys get p = 0, but 0 * inf is NaN: in tiles that some row does not see whole, values
+//     that are not finite are taken out of the product and counted apart (see take_values).
+#include "attn_core.h"
+#include "layer_ops.h"
+#include "mask_core.h"
+
+namespace spax {
+namespace {
+
+using namespace elem;
+using namespace attn;
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr int kRows = 32 * kWaves;  // query rows of a tile
+
+struct ChunkArgs {
+  const void *q, *k, *v;
+  void* out;
+  float *lse, *part_o, *part_ml;
+  const int32_t *starts, *lens, *table;
+  const float *k_scale, *v_scale;
+  int64_t qt, qh, ot, oh;
+  int64_t k_page, k_head, k_row, v_page, v_head, v_row, table_stride;
+  int32_t n_tokens, n_heads, n_kv, group, n_seqs, n_pages, page_shift;
+  int32_t max_len, window, tiles, pieces;
+  float scale;
+};
+
+// A tile of query rows: rows from..to of sequence seq's n_new * group, for one key head.
+struct Tile {
+  int seq, first, n_new, len;  // first: its first token's row of q
+  int from, to;                // from == to: no such tile
+  __device__ inline int position(int token) const { return len - n_new + token; }
+};
+
+__device__ inline int clamp_to(int x, int most) { return x < 0 ? 0 : x > most ? most : x; }
+
+// Tile `index` of all sequences' tiles laid end to end.  Lane l holds sequence base + l; past 64
+// sequences that is a chain of loads, one for every 64.
+__device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
+  int before = 0;
+  for (int base = 0; base < a.n_seqs; base += 64) {
+    const int s = base + lane;
+    int first = 0, n_new = 0;
+    if (s < a.n_seqs) {
+      first = clamp_to(a.starts[s], a.n_tokens);
+      n_new = clamp_to(a.starts[s + 1], a.n_tokens) - first;
+      n_new = n_new < 0 ? 0 : n_new;
+    }
+    const int tiles = (n_new * a.group + kRows - 1) / kRows;
+    const int upto = before + mask::wave_scan(tiles);
+    const int last = __builtin_amdgcn_readlane(upto, 63);
+    if (index < last) {
+      const int who = __builtin_ctzll(__ballot(upto > index));
+      Tile t;
+      t.seq = base + who;
+      t.first = __builtin_amdgcn_readlane(first, who);
+      t.n_new = __builtin_amdgcn_readlane(n_new, who);
+      t.len = clamp_to(a.lens[t.seq], a.max_len);
+      const int begins =
+          __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(tiles, who);
+      t.from = (index - begins) * kRows;
+      const int rows = t.n_new * a.group;
+      t.to = t.from + kRows < rows ? t.from + kRows : rows;
+      return t;
+    }
+    before = last;
+  }
+  return Tile{0, 0, 0, 0, 0, 0};
+}
+
+// The keys [lo, hi) that the token at position p sees.
+__device__ inline int lo_of(const ChunkArgs& a, int p) {
+  return a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
+}
+__device__ inline int hi_of(int p) { return p < 0 ? 0 : p + 1; }
+
+template <class T, bool NARROW, int D>
+struct Shape {
+  static constexpr int kKeys = D >= 192 ? 32 : 64;     // per step
+  static constexpr int EB = NARROW ? 1 : 2;
+  static constexpr int kChunks = D * EB / 16;          // 16-byte pieces of a cached row
+  static constexpr int kItems = kKeys * kChunks;       // of a step's keys
+  static constexpr int kLoads = (kItems + kThreads - 1) / kThreads;
+  // Rows in LDS, always 16-bit.  K: an odd number of 16-byte pieces, so that the 16 rows of a read
+  // pass lie on different banks.  V: 64 or 192 bytes past a multiple of 256, so that the four
+  // rows of a transposing read (64 bytes each) do.
+  static constexpr int kKPitch = 2 * D + 16;
+  static constexpr int kVPitch = (2 * D) % 128 == 0 ? 2 * D + 64 : 2 * D;
+  static constexpr int kBuffer = kKeys * (kKPitch + kVPitch);
+  static constexpr int kBlocks = kKeys / 32, kSteps = kKeys / 16;
+};
+
+template <class T, bool NARROW, int D>
+struct Loader {
+  using S = Shape<T, NARROW, D>;
+  const uint8_t *k, *v;  // of the key head
+  const int32_t* table;  // of the sequence
+  int64_t k_page, k_row, v_page, v_row;
+  int page_shift, n_pages, lo, hi;  // the tile's keys
+
+  // The table entry of key `key0 + lane` (past the end: of the last key).
+  __device__ inline int look_up(int key0, int lane) const {
+    const int at = key0 + (lane & (S::kKeys - 1));
+    return table[(at < hi ? at : hi - 1) >> page_shift];
+  }
+  // That entry as the key's page, or -1 where it names no page or no row of the tile sees a key of
+  // its group of four (which lie on one page).
+  __device__ inline int page_of(int entry, int key0, int lane) const {
+    const int key = key0 + (lane & (S::kKeys - 1));
+    return (key | 3) >= lo && (key & ~3) < hi && (uint32_t)entry < (uint32_t)n_pages ? entry : -1;
+  }
+  u32x4 kx[S::kLoads], vx[S::kLoads];
+  __device__ inline void load(int page, int key0) {
+    const int mask = (1 << page_shift) - 1;
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x;
+      const int row = e / S::kChunks, chunk = e % S::kChunks;
+      const int pg = __shfl(page, row);
+      if (S::kItems % kThreads && e >= S::kItems) continue;
+      const int64_t p = pg < 0 ? 0 : pg, in = (key0 + row) & mask;  // unseen: any row, masked later
+      kx[i] = *reinterpret_cast<const u32x4*>(k + S::EB * (p * k_page + in * k_row) + 16 * chunk);
+      vx[i] = *reinterpret_cast<const u32x4*>(v + S::EB * (p * v_page + in * v_row) + 16 * chunk);
+    }
+  }
+  // Into LDS; values of keys without a page as zeros.
+  __device__ inline void lay_out(uint8_t* buffer, int page) const {
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int e = i * kThreads + (int)threadIdx.x;
+      const int row = e / S::kChunks, chunk = e % S::kChunks;
+      const uint32_t keep = __shfl(page, row) >= 0 ? ~0u : 0u;
+      if (S::kItems % kThreads && e >= S::kItems) continue;
+      uint8_t* kr = buffer + row * S::kKPitch + 16 * (NARROW ? 2 : 1) * chunk;
+      uint8_t* vr =
+          buffer + S::kKeys * S::kKPitch + row * S::kVPitch + 16 * (NARROW ? 2 : 1) * chunk;
+      const u32x4 vz = vx[i] & keep;
+      if constexpr (NARROW) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          *reinterpret_cast<u32x4*>(kr + 16 * y) = widen4(kx[i][2 * y], kx[i][2 * y + 1]);
+          *reinterpret_cast<u32x4*>(vr + 16 * y) = widen4(vz[2 * y], vz[2 * y + 1]);
+        }
+      } else {
+        *reinterpret_cast<u32x4*>(kr) = kx[i];
+        *reinterpret_cast<u32x4*>(vr) = vz;
+      }
+    }
+  }
+  static __device__ inline u32x4 widen4(uint32_t x, uint32_t y) {
+    return u32x4{Mma<T>::template widen<false>(x), Mma<T>::template widen<true>(x),
+                 Mma<T>::template widen<false>(y), Mma<T>::template widen<true>(y)};
+  }
+};
+
+// Four keys of one dim per lane: rows `row`.. of 16 dims for every 16 lanes.
+__device__ inline u32x2 read_turned(const uint8_t* p) {
+  typedef short v4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4 lds_v4;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)p));
+}
+
+// A value that is not finite as a count in a sum of at most 64 of them: 1 for inf, 2^7 for -inf,
+// 2^14 for NaN (powers of two, exact in both types); finite ones as 0.
+template <class T>
+__device__ inline uint32_t odd_ones(uint32_t w) {
+  typename Mma<T>::v2 x = __builtin_bit_cast(typename Mma<T>::v2, w), y;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float f = (float)x[i];
+    y[i] = (T)(f != f ? 0x1p14f : f == INFINITY ? 1.0f : f == -INFINITY ? 0x1p7f : 0.0f);
+  }
+  return __builtin_bit_cast(uint32_t, y);
+}
+template <class T>
+__device__ inline uint32_t finite_ones(uint32_t w) {
+  const uint32_t bad = ((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u;
+  return w & ~((bad >> 15) * 0xffffu);
+}
+template <class T>
+__device__ inline bool has_odd(uint32_t w) {
+  return (((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u) != 0u;
+}
+
+template <class T, bool NARROW, int D>
+struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
+  using S = Shape<T, NARROW, D>;
+  static constexpr int KC = D / 16, OB = D / 32;
+  u32x4 q[KC];
+  f32x16 o[OB];
+  float m, l;
+  int lo, hi;          // this lane's row: the keys it sees
+  int lo_max, hi_min;  // of the wave's rows: keys in [lo_max, hi_min) are seen by all
+
+  __device__ inline void score(const uint8_t* keys, int lane, float to_log2,
+                               f32x16 (&s)[S::kBlocks]) const {
+    const int h = lane >> 5, r = lane & 31;
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b) {
+      f32x16 x = {};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + (32 * b + r) * S::kKPitch + 32 * c +
+                                                        16 * h);
+        x = Mma<T>::mul32(k, q[c], x);
+      }
+      s[b] = x * to_log2;
+    }
+  }
+  // Bit 16 b + i: the lane's row sees key 32 b + 8 (i / 4) + 4 h + i % 4.
+  __device__ inline uint32_t seen(int key0, int page, int lane) const {
+    const int h = lane >> 5;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int g = 0; g < 4 * S::kBlocks; ++g) {
+      const int at = 32 * (g / 4) + 8 * (g % 4) + 4 * h;
+      const bool paged = __shfl(page, at) >= 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = key0 + at + i;
+        bits |= (paged && key >= lo && key < hi ? 1u : 0u) << (4 * g + i);
+      }
+    }
+    return bits;
+  }
+  __device__ inline void soften(f32x16 (&s)[S::kBlocks]) {
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any(top > m)) {
+      const float higher = fmaxf(m, top);
+      const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
+      m = higher;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < OB; ++t) o[t] *= f;
+    }
+    const float base = (m == -INFINITY ? 0.0f : m) - Mma<T>::kLift;
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - base);
+        sum += s[b][i];
+      }
+    l += sum;
+  }
+  static __device__ inline u32x4 operand(const f32x16 (&s)[S::kBlocks], int step) {
+    u32x4 p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      typename Mma<T>::v2 x;
+      x.x = (T)s[step / 2][8 * (step % 2) + 2 * i];
+      x.y = (T)s[step / 2][8 * (step % 2) + 2 * i + 1];
+      p[i] = __builtin_bit_cast(uint32_t, x);
+    }
+    return p;
+  }
+  static __device__ inline u32x4 read_values(const uint8_t* values, int block, int step, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    const uint8_t* p = values + (16 * step + 4 * (g >> 1) + (i >> 2)) * S::kVPitch +
+                       2 * (32 * block + 16 * (g & 1) + 4 * (i & 3));
+    const u32x2 x = read_turned(p), y = read_turned(p + 8 * S::kVPitch);
+    return u32x4{x.x, x.y, y.x, y.y};
+  }
+  // o += p v.  EDGE: some row does not see some key.  Values that are not finite then stay out of the
+  // product; a second one counts, for each row and dim, those of keys that the row does see.
+  template <bool EDGE>
+  __device__ inline void take_values(const f32x16 (&s)[S::kBlocks], const uint8_t* values,
+                                     uint32_t bits, int lane) {
+    u32x4 p[S::kSteps];
+#pragma unroll
+    for (int t = 0; t < S::kSteps; ++t) p[t] = operand(s, t);
+#pragma unroll
+    for (int b = 0; b < OB; ++b) {
+      u32x4 v[S::kSteps];
+      bool odd = false;
+#pragma unroll
+      for (int t = 0; t < S::kSteps; ++t) {
+        v[t] = read_values(values, b, t, lane);
+        if constexpr (EDGE)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd |= has_odd<T>(v[t][i]);
+      }
+      if (EDGE && __any(odd)) {
+        f32x16 count = {};
+#pragma unroll
+        for (int t = 0; t < S::kSteps; ++t) {
+          u32x4 fine, bad, one;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            fine[i] = finite_ones<T>(v[t][i]);
+            bad[i] = odd_ones<T>(v[t][i]);
+            typename Mma<T>::v2 x;
+            x.x = (T)(float)((bits >> (8 * t + 2 * i)) & 1u);
+            x.y = (T)(float)((bits >> (8 * t + 2 * i + 1)) & 1u);
+            one[i] = __builtin_bit_cast(uint32_t, x);
+          }
+          o[b] = Mma<T>::mul32(fine, p[t], o[b]);
+          count = Mma<T>::mul32(bad, one, count);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int n = (int)count[i];
+          const bool up = n & 127, down = (n >> 7) & 127, nan = n >> 14;
+          if (n) o[b][i] += nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < S::kSteps; ++t) o[b] = Mma<T>::mul32(v[t], p[t], o[b]);
+      }
+    }
+  }
+  __device__ inline void step(const uint8_t* buffer, int key0, int page, bool paged, float to_log2,
+                              int lane) {
+    f32x16 s[S::kBlocks];
+    score(buffer, lane, to_log2, s);
+    const uint8_t* values = buffer + S::kKeys * S::kKPitch;
+    if (paged && key0 >= lo_max && key0 + S::kKeys <= hi_min) {
+      soften(s);
+      take_values<false>(s, values, 0u, lane);
+    } else {
+      const uint32_t bits = seen(key0, page, lane);
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[b][i] = (bits >> (16 * b + i)) & 1u ? s[b][i] : -INFINITY;
+      soften(s);
+      take_values<true>(s, values, bits, lane);
+    }
+  }
+};
+
+// The tile's steps of keys, and those of one piece of it.
+struct Span2 {
+  int first, count;
+};
+template <int KEYS>
+__device__ inline Span2 steps_of(const ChunkArgs& a, const Tile& t, int piece, int* lo, int* hi) {
+  *hi = hi_of(t.position((t.to - 1) / a.group));
+  *lo = lo_of(a, t.position(t.from / a.group));
+  const int first = *lo / KEYS, all = *hi > *lo ? (*hi + KEYS - 1) / KEYS - first : 0;
+  const int per = (all + a.pieces - 1) / a.pieces;
+  const int from = piece * per < all ? piece * per : all;
+  const int to = from + per < all ? from + per : all;
+  return Span2{first + from, to - from};
+}
+
+template <class T, bool NARROW, int D>
+__global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkArgs a) {
+  using S = Shape<T, NARROW, D>;
+  using R = Rows<T, NARROW, D>;
+  extern __shared__ uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int h = lane >> 5, r = lane & 31;
+  // Workgroups go to the 8 XCDs in turn: the tiles of a key head, which read the same rows, meet on
+  // few of them.  Later tiles of a sequence see more keys and are begun first.
+  const int kvh = blockIdx.x % (unsigned)a.n_kv, rest = blockIdx.x / (unsigned)a.n_kv;
+  const int piece = rest % a.pieces;
+  const Tile tile = find_tile(a, a.tiles - 1 - rest / a.pieces, lane);
+  if (tile.from == tile.to) return;
+
+  Loader<T, NARROW, D> in;
+  const Span2 steps = steps_of<S::kKeys>(a, tile, piece, &in.lo, &in.hi);
+  float to_log2 = a.scale * kLog2e, v_mul = 1.0f;
+  if constexpr (NARROW) {
+    if (a.k_scale) to_log2 *= a.k_scale[kvh];
+    if (a.v_scale) v_mul = a.v_scale[kvh];
+  }
+  in.k = (const uint8_t*)a.k + (int64_t)S::EB * kvh * a.k_head;
+  in.v = (const uint8_t*)a.v + (int64_t)S::EB * kvh * a.v_head;
+  in.table = a.table + tile.seq * a.table_stride;
+  in.k_page = a.k_page; in.k_row = a.k_row; in.v_page = a.v_page; in.v_row = a.v_row;
+  in.page_shift = a.page_shift; in.n_pages = a.n_pages;
+
+  const int first = tile.from + 32 * wave;  // the wave's rows
+  const int last = (first + 32 < tile.to ? first + 32 : tile.to) - 1;
+  const int row = first + r <= last ? first + r : last;
+  const bool works = last >= first, mine = works && first + r <= last;
+  const int token = works ? row / a.group : 0, head = kvh * a.group + (works ? row % a.group : 0);
+  R w;
+  if (works) {
+    const uint8_t* q = (const uint8_t*)a.q + 2 * ((tile.first + token) * a.qt + head * a.qh);
+#pragma unroll
+    for (int c = 0; c < R::KC; ++c)
+      w.q[c] = *reinterpret_cast<const u32x4*>(q + 32 * c + 16 * h);
+  }
+#pragma unroll
+  for (int t = 0; t < R::OB; ++t) w.o[t] = f32x16{};
+  w.m = -INFINITY;
+  w.l = 0.0f;
+  w.lo = lo_of(a, tile.position(token));
+  w.hi = hi_of(tile.position(token));
+  int lo_min = 0, hi_max = 0;
+  if (works) {
+    lo_min = lo_of(a, tile.position(first / a.group));
+    w.lo_max = lo_of(a, tile.position(last / a.group));
+    w.hi_min = hi_of(tile.position(first / a.group));
+    hi_max = hi_of(tile.position(last / a.group));
+  }
+
+  if (steps.count > 0) {
+    int key0 = steps.first * S::kKeys;
+    int page = in.page_of(in.look_up(key0, lane), key0, lane);
+    in.load(page, key0);
+    int entry = in.look_up(key0 + S::kKeys, lane);
+    in.lay_out(lds, page);
+    for (int i = 0; i < steps.count; ++i) {
+      const uint8_t* buffer = lds + (i & 1) * S::kBuffer;
+      mask::lds_barrier();  // this buffer is laid out, the other one has been read
+      const int next = key0 + S::kKeys;
+      int next_page = -1;
+      if (i + 1 < steps.count) {
+        next_page = in.page_of(entry, next, lane);
+        in.load(next_page, next);
+        entry = in.look_up(next + S::kKeys, lane);
+      }
+      if (works && key0 + S::kKeys > lo_min && key0 < hi_max)
+        w.step(buffer, key0, page, __all(page >= 0), to_log2, lane);
+      if (i + 1 < steps.count) in.lay_out(lds + (~i & 1) * S::kBuffer, next_page);
+      key0 = next;
+      page = next_page;
+    }
+  }
+
+  if (!works) return;
+  w.l += __shfl_xor(w.l, 32);
+  if (!mine) return;
+  const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
+  if (a.pieces == 1) {
+    const float f = w.l == 0.0f ? 0.0f : v_mul / w.l;
+    T* out = (T*)a.out + (tile.first + token) * a.ot + head * a.oh;
+#pragma unroll
+    for (int b = 0; b < R::OB; ++b)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f == 0.0f ? 0.0f : w.o[b][4 * g + i] * f;
+        store_n<4>(out + 32 * b + 8 * g + 4 * h, x);
+      }
+    if (a.lse && h == 0) a.lse[at] = lse_of<T>(w.m, w.l);
+    return;
+  }
+  const int64_t part = (int64_t)piece * a.n_tokens * a.n_heads + at;
+  if (steps.count > 0) {
+#pragma unroll
+    for (int b = 0; b < R::OB; ++b)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = w.o[b][4 * g + i];
+        *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * g + 4 * h) = x;
+      }
+  }
+  if (h == 0) {
+    a.part_ml[2 * part] = w.m;
+    a.part_ml[2 * part + 1] = w.l;
+  }
+}
+
+// Joins a tile's pieces: four dims of a row a thread.  A piece that a row has no key in has no o.
+template <class T, int D>
+__global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a) {
+  const int kvh = blockIdx.x % (unsigned)a.n_kv;
+  const Tile tile = find_tile(a, blockIdx.x / (unsigned)a.n_kv, threadIdx.x & 63);
+  const float v_mul = a.v_scale ? a.v_scale[kvh] : 1.0f;
+  for (int e = threadIdx.x; e < (tile.to - tile.from) * (D / 4); e += kThreads) {
+    const int row = tile.from + e / (D / 4), d = 4 * (e % (D / 4));
+    const int token = tile.first + row / a.group, head = kvh * a.group + row % a.group;
+    const int64_t at = (int64_t)token * a.n_heads + head;
+    const int64_t step = (int64_t)a.n_tokens * a.n_heads;
+    float m = -INFINITY;
+    for (int c = 0; c < a.pieces; ++c) m = fmaxf(m, a.part_ml[2 * (at + c * step)]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < a.pieces; ++c) {
+      const int64_t part = at + c * step;
+      const float pl = a.part_ml[2 * part + 1];
+      if (pl == 0.0f) continue;
+      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * part] - base);
+      l += f * pl;
+      sum += f * *reinterpret_cast<const f32x4*>(a.part_o + part * D + d);
+    }
+    const float inv = v_mul / l;
+    float out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
+    store_n<4>((T*)a.out + token * a.ot + head * a.oh + d, out);
+    if (a.lse && d == 0) a.lse[at] = lse_of<T>(m, l);
+  }
+}
+
+template <class T, bool NARROW, int D>
+int launch(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
+  constexpr int kLds = 2 * Shape<T, NARROW, D>::kBuffer;
+  hipLaunchKernelGGL((chunk_kernel<T, NARROW, D>), dim3(blocks), dim3(kThreads), kLds, s, a);
+  SPAX_HIP_CHECK(hipGetLastError());
+  if (a.pieces > 1) {
+    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)(a.tiles * a.n_kv)),
+                       dim3(kThreads), 0, s, a);
+    SPAX_HIP_CHECK(hipGetLastError());
+  }
+  return SPAX_OK;
+}
+
+template <class T, bool NARROW>
+int launch_dim(const ChunkArgs& a, int dim, unsigned blocks, hipStream_t s) {
+  switch (dim) {
+    case 64: return launch<T, NARROW, 64>(a, blocks, s);
+    case 96: return launch<T, NARROW, 96>(a, blocks, s);
+    case 128: return launch<T, NARROW, 128>(a, blocks, s);
+    case 192: return launch<T, NARROW, 192>(a, blocks, s);
+    default: return launch<T, NARROW, 256>(a, blocks, s);
+  }
+}
+
+}  // namespace
+
+ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
+  const spax_kv_cache& c = *a->cache;
+  ChunkPlan p{};
+  if (a->n_tokens == 0) return p;
+  const int64_t group = a->n_heads / c.n_kv_heads;
+  // every sequence with tokens has at most one tile that is not full
+  p.tiles = a->n_tokens * group / kRows + (c.n_seqs < a->n_tokens ? c.n_seqs : a->n_tokens);
+  int64_t keys = a->max_len;
+  if (a->window > 0 && (int64_t)a->window + a->n_tokens < keys)
+    keys = (int64_t)a->window + a->n_tokens;
+  const int64_t steps = (keys + 63) / 64, items = p.tiles * c.n_kv_heads;
+  int64_t pieces = 512 / items;
+  if (pieces > steps / 2) pieces = steps / 2;
+  p.pieces = (int32_t)(pieces < 1 ? 1 : pieces > 64 ? 64 : pieces);
+  p.blocks = items * p.pieces;
+  if (p.pieces > 1)
+    p.ws_bytes = aligned_size((size_t)p.pieces * a->n_tokens * a->n_heads *
+                              ((size_t)c.head_dim + 2) * sizeof(float));
+  return p;
+}
+
+int launch_chunk_attention(const spax_chunk_attention_args* p, void* ws, hipStream_t s) {
+  if (p->n_tokens == 0) return SPAX_OK;
+  const spax_kv_cache& c = *p->cache;
+  const ChunkPlan plan = chunk_plan(p);
+  ChunkArgs a{};
+  a.q = p->q; a.k = c.k; a.v = c.v; a.out = p->out; a.lse = p->lse;
+  a.starts = p->starts; a.lens = p->lens; a.table = c.page_table;
+  a.k_scale = c.k_scale; a.v_scale = c.v_scale;
+  a.qt = p->q_token_stride; a.qh = p->q_head_stride;
+  a.ot = p->out_token_stride; a.oh = p->out_head_stride;
+  a.k_page = c.k_page_stride; a.k_head = c.k_head_stride; a.k_row = c.k_row_stride;
+  a.v_page = c.v_page_stride; a.v_head = c.v_head_stride; a.v_row = c.v_row_stride;
+  a.table_stride = c.table_stride;
+  a.n_tokens = p->n_tokens; a.n_heads = p->n_heads; a.n_kv = c.n_kv_heads;
+  a.group = p->n_heads / c.n_kv_heads; a.n_seqs = c.n_seqs; a.n_pages = c.n_pages;
+  a.page_shift = __builtin_ctz((unsigned)c.page_size);
+  a.max_len = p->max_len; a.window = p->window; a.scale = p->scale;
+  a.tiles = (int32_t)plan.tiles; a.pieces = plan.pieces;
+  a.part_o = (float*)ws;
+  a.part_ml = (float*)ws + (size_t)plan.pieces * p->n_tokens * p->n_heads * c.head_dim;
+  const unsigned blocks = (unsigned)plan.blocks;
+  if (c.type == SPAX_E4M3)
+    return p->type == SPAX_F16 ? launch_dim<f16, true>(a, c.head_dim, blocks, s)
+                               : launch_dim<bf16, true>(a, c.head_dim, blocks, s);
+  return p->type == SPAX_F16 ? launch_dim<f16, false>(a, c.head_dim, blocks, s)
+                             : launch_dim<bf16, false>(a, c.head_dim, blocks, s);
+}
+
+}  // namespace spax

@@ -4,6 +4,7 @@
 // act(g) = g / (1 + exp(-2u)), u = sqrt(2/pi) (g + 0.044715 g^3): no cancellation near tanh = -1.
 // Bound: bytes (three rows move, nothing is reused) or, for one row, launch latency.  Measured: 2048
 // x 14336 bf16: 32.6 us, 5.4 TB/s (a large copy reaches 5.1); 1 x 11008: 2.4 us on the device.
+#include "act.h"
 #include "layer_ops.h"
 
 namespace spax {
@@ -19,20 +20,6 @@ struct GluArgs {
   int64_t gs, us, xs;
   int32_t d, gelu, blocks_per_row;
 };
-
-// act(g) * up.  With h = exp(-|u| / 2), 1 / (1 + exp(-u)) is 1 / (1 + h h) above zero and
-// h h / (1 + h h) below, where one h goes to each factor: exp(-u) itself overflows at u = -88, where act(g)
-// is still 2^-121, and h h alone ends there.  1 + h h is in [1, 2], where the hardware's reciprocal
-// is good to 2^-23 of itself.
-__device__ inline float act_mul(float g, float up, bool gelu) {
-  float u = g;
-  if (gelu) {
-    constexpr float kTwoRootTwoOverPi = 1.59576912160573071176f;
-    u = kTwoRootTwoOverPi * (g + 0.044715f * g * g * g);
-  }
-  const float h = expf(-0.5f * fabsf(u)), f = u < 0.0f ? h : 1.0f;
-  return g * f * __builtin_amdgcn_rcpf(1.0f + h * h) * (up * f);
-}
 
 // Eight values per thread; rows need not start on eight (see load_any).
 template <class SRC, class X>

@@ -1,4 +1,5 @@
-// spax_kv_append: keys and values of new tokens into the paged cache, rotated on the way.
+// spax_kv_append, spax_kv_append_normed: keys and values of new tokens into the paged cache, rotated
+// on the way, their heads and the queries' normed before that where asked.
 //
 // For a pair (x, y) of a head at position p with frequency f:
 //   a = p f,   (x, y) -> (x cos a - y sin a, x sin a + y cos a).
@@ -34,6 +35,11 @@ struct AppendArgs {
   int64_t kc_page, kc_head, kc_row, vc_page, vc_head, vc_row, table_stride;
   int32_t n_heads, n_kv, dim, rot, interleaved, n_seqs, n_pages, max_pages, page_shift;
   int32_t heads_at_once, heads_per_block;
+  // the normed form
+  const float *q_w, *q_b, *k_w, *k_b;
+  int64_t q_ws, k_ws;  // from head to head
+  float eps;
+  int32_t layer, lanes;  // lanes: threads set aside for a head, a power of two
 };
 
 // Where token t's rows go: the row of key head 0, or -1.
@@ -114,9 +120,89 @@ __device__ inline void divide_e4m3(float v[N], float scale) {
   }
 }
 
+// The sum of v over the `lanes` threads (a power of two, aligned) that hold a head.  More than a wave's
+// meet in `waves`; every thread of the workgroup calls it as often.
+__device__ inline float sum_of_head(float v, int lanes, float* waves) {
+  for (int z = 1; z < lanes && z < 64; z <<= 1) v += __shfl_xor(v, z);
+  if (lanes > 64) {
+    const int wave = threadIdx.x >> 6, first = wave & ~(lanes / 64 - 1);
+    __syncthreads();  // the last sums have been read
+    if ((threadIdx.x & 63) == 0) waves[wave] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int y = 0; y < lanes / 64; ++y) v += waves[first + y];
+  }
+  return v;
+}
+
+// N 32-bit values from any 4-byte aligned address.
+template <int N>
+__device__ inline void load_f32(const float* p, float v[N]) {
+  typedef float FN __attribute__((ext_vector_type(N), aligned(4)));
+  const FN x = *reinterpret_cast<const FN*>(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = x[i];
+}
+
+// A head's norm and its weights, held from head to head as long as they are the same.
+template <int N>
+struct HeadNorm {
+  float w[2 * N], b[2 * N];
+  int have = -1;  // 0: the queries' shared weights, 1: the keys'
+  // x and y: this thread's values of a head, zeros where it has none (`on` false, or y with `single`).
+  __device__ inline void apply(const AppendArgs& a, float x[N], float y[N], int h, bool on,
+                               bool single, int e0, int e1, float* waves) {
+    const int which = h < a.n_heads ? 0 : 1;
+    const float* weight = which ? a.k_w : a.q_w;
+    const float* bias = which ? a.k_b : a.q_b;
+    const bool normed = on && weight && h < a.n_heads + a.n_kv;
+    if (normed && have != which) {
+      const int64_t stride = which ? a.k_ws : a.q_ws;
+      const int64_t at = (which ? h - a.n_heads : h) * stride;
+      load_f32<N>(weight + at + e0, w);
+      if (!single) load_f32<N>(weight + at + e1, w + N);
+      if (bias) {
+        load_f32<N>(bias + at + e0, b);
+        if (!single) load_f32<N>(bias + at + e1, b + N);
+      }
+      have = stride ? -1 : which;
+    }
+    const float share = 1.0f / (float)a.dim;
+    float mean = 0.0f;
+    if (a.layer) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) s += x[i] + y[i];
+      mean = sum_of_head(s, a.lanes, waves) * share;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float u = x[i] - mean, v = single ? 0.0f : y[i] - mean;
+      s += u * u + v * v;
+    }
+    s = sum_of_head(on ? s : 0.0f, a.lanes, waves);
+    if (!normed) return;
+    const float r = 1.0f / sqrtf(s * share + a.eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = (x[i] - mean) * r * w[i];
+      y[i] = single ? 0.0f : (y[i] - mean) * r * w[N + i];
+      if (bias) {
+        x[i] += b[i];
+        y[i] += single ? 0.0f : b[N + i];
+      }
+    }
+  }
+};
+template <>
+struct HeadNorm<0> {};
+
 // SRC: type of q, k, v; LOW: of q_out (and a 16-bit cache); C: of the cache.  A thread's item is N
-// pairs of a head, or as many values that are copied: 2 N of them, one for N = 1.
-template <class SRC, class LOW, class C, int N>
+// pairs of a head, or as many values that are copied: 2 N of them, one for N = 1.  NORM: a head's
+// threads lie in a.lanes neighbouring ones, some of them without an item, and all go through
+// every round, since the sums of a norm pass through all of them.
+template <class SRC, class LOW, class C, int N, bool NORM>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int kCopied = N > 1 ? 2 * N : 1;
   const int t = blockIdx.x;
@@ -124,8 +210,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   // items of a head: pairs / N rotated ones, then the copied values
   const int turned = pairs / N;
   const int items = turned + (a.dim - a.rot) / kCopied;
-  const int slot = threadIdx.x / items;
-  const int j = threadIdx.x - slot * items;
+  const int slot = threadIdx.x / (NORM ? a.lanes : items);
+  const int j = threadIdx.x - slot * (NORM ? a.lanes : items);
   const int p = a.positions[t];
   const bool turns = j < turned;
   // element offsets of the item's first and second values
@@ -161,7 +247,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     rx = load_any<SN>(src + e0);
     if (!single) ry = load_any<SN>(src + e1);
   };
-  const int mine = slot < a.heads_at_once ? h0 + slot : h1;  // threads past the last slot: none
+  // threads past the last slot, or past a head's last item: none
+  const int mine = slot < a.heads_at_once && (!NORM || j < items) ? h0 + slot : h1;
   load(mine);
   const Place to = place_of(a, t, p);
   find_sines();
@@ -171,15 +258,23 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     sn[i] = turns ? sines[0][N * j + i] : 0.0f;
     cs[i] = turns ? sines[1][N * j + i] : 1.0f;
   }
-  for (int h = mine; h < h1; h += a.heads_at_once) {
+  HeadNorm<NORM ? N : 0> norm;
+  __shared__ float waves[NORM ? kAppendThreads / 64 : 1];
+  int base = h0;
+  for (int h = mine; (NORM ? base : h) < h1; h += a.heads_at_once, base += a.heads_at_once) {
+    const bool on = !NORM || h < h1;
     const bool is_q = h < n_heads, is_v = h >= n_heads + n_kv;
     float x[N], y[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = (float)rx[i];
-      y[i] = single ? 0.0f : (float)ry[i];
+      x[i] = on ? (float)rx[i] : 0.0f;
+      y[i] = single || !on ? 0.0f : (float)ry[i];
     }
     load(h + a.heads_at_once);  // ahead of this head's stores
+    if constexpr (NORM) {
+      norm.apply(a, x, y, h, on, single, e0, e1, waves);
+      if (!on) continue;
+    }
     if (turns && !is_v) turn<N>(x, y, sn, cs, N > 1 && a.interleaved);
     if (is_q) {
       LOW* dst = (LOW*)a.q_out + t * a.ot + h * a.oh;
@@ -212,31 +307,42 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   }
 }
 
-template <class SRC, class LOW, class C>
+template <class SRC, class LOW, class C, bool NORM>
 int launch(const AppendArgs& a, dim3 grid, int pairs, hipStream_t s) {
   const dim3 blk(kAppendThreads);
   if (pairs == 8)
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 8>), grid, blk, 0, s, a);
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 8, NORM>), grid, blk, 0, s, a);
   else if (pairs == 4)
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 4>), grid, blk, 0, s, a);
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 4, NORM>), grid, blk, 0, s, a);
   else
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 1>), grid, blk, 0, s, a);
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 1, NORM>), grid, blk, 0, s, a);
   SPAX_HIP_CHECK(hipGetLastError());
   return SPAX_OK;
 }
 
-template <class SRC>
+template <class SRC, bool NORM>
 int launch_src(const AppendArgs& a, int out_type, bool narrow, dim3 grid, int pairs,
                hipStream_t s) {
   if (out_type == SPAX_F16)
-    return narrow ? launch<SRC, f16, e4m3>(a, grid, pairs, s) : launch<SRC, f16, f16>(a, grid, pairs, s);
-  return narrow ? launch<SRC, bf16, e4m3>(a, grid, pairs, s)
-                : launch<SRC, bf16, bf16>(a, grid, pairs, s);
+    return narrow ? launch<SRC, f16, e4m3, NORM>(a, grid, pairs, s)
+                  : launch<SRC, f16, f16, NORM>(a, grid, pairs, s);
+  return narrow ? launch<SRC, bf16, e4m3, NORM>(a, grid, pairs, s)
+                : launch<SRC, bf16, bf16, NORM>(a, grid, pairs, s);
+}
+
+template <bool NORM>
+int launch_norm(const AppendArgs& a, int src_type, int out_type, bool narrow, dim3 grid, int pairs,
+                hipStream_t s) {
+  switch (src_type) {
+    case SPAX_F32: return launch_src<float, NORM>(a, out_type, narrow, grid, pairs, s);
+    case SPAX_F16: return launch_src<f16, NORM>(a, out_type, narrow, grid, pairs, s);
+    default: return launch_src<bf16, NORM>(a, out_type, narrow, grid, pairs, s);
+  }
 }
 
 }  // namespace
 
-int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
+int launch_kv_append(const spax_kv_append_args* p, const spax_head_norm* n, hipStream_t s) {
   if (p->n_tokens == 0) return SPAX_OK;
   const spax_kv_cache& c = *p->cache;
   AppendArgs a{};
@@ -259,7 +365,14 @@ int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
   // rotated, and 59 of one, where 20 are).
   const int pairs = p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
   const int items = pairs > 1 ? a.dim / (2 * pairs) : p->rot_dim / 2 + a.dim - p->rot_dim;
-  a.heads_at_once = kAppendThreads / items;
+  int lanes = items;
+  if (n) {
+    for (lanes = 1; lanes < items;) lanes <<= 1;
+    a.q_w = n->q_weight; a.q_b = n->q_bias; a.q_ws = n->q_stride;
+    a.k_w = n->k_weight; a.k_b = n->k_bias; a.k_ws = n->k_stride;
+    a.eps = n->eps; a.layer = n->kind == SPAX_NORM_LAYER; a.lanes = lanes;
+  }
+  a.heads_at_once = kAppendThreads / lanes;
   // One round of heads per workgroup while there are few tokens: latency is then one load and one
   // store deep.  With many a workgroup walks over all heads of its token.  128 tokens: 4.65 us by
   // rounds, 4.9 walking; 511: equal; 1000: 8.4 and 7.5; 4099: 22.9 and 20.0.
@@ -268,11 +381,8 @@ int launch_kv_append(const spax_kv_append_args* p, hipStream_t s) {
   const dim3 grid((unsigned)p->n_tokens,
                   (unsigned)((total + a.heads_per_block - 1) / a.heads_per_block));
   const bool narrow = c.type == SPAX_E4M3;
-  switch (p->src_type) {
-    case SPAX_F32: return launch_src<float>(a, p->out_type, narrow, grid, pairs, s);
-    case SPAX_F16: return launch_src<f16>(a, p->out_type, narrow, grid, pairs, s);
-    default: return launch_src<bf16>(a, p->out_type, narrow, grid, pairs, s);
-  }
+  return n ? launch_norm<true>(a, p->src_type, p->out_type, narrow, grid, pairs, s)
+           : launch_norm<false>(a, p->src_type, p->out_type, narrow, grid, pairs, s);
 }
 
 }  // namespace spax

@@ -18,7 +18,7 @@ struct Span {
 // True if x and y have a byte in common.  Columns of the same rows (equal steps) are told apart;
 // anything else strided counts as all bytes from its first to its last.
 bool shares(const Span& x, const Span& y);
-constexpr int kMaxSpans = 12;
+constexpr int kMaxSpans = 16;
 struct Spans {
   Span s[kMaxSpans];
   int n = 0;
@@ -29,10 +29,12 @@ struct Spans {
 };
 
 // Validation (host only); each also lists the operator's buffers.
-int check_kv_append(const spax_kv_append_args* a, Spans* spans);
+int check_kv_append(const spax_kv_append_args* a, const spax_head_norm* n, Spans* spans);
 int check_attention(const spax_attention_args* a, Spans* spans);
 int check_residual_norm(const spax_residual_norm_args* a, Spans* spans);
 int check_glu(const spax_glu_args* a, Spans* spans);
+int check_chunk_attention(const spax_chunk_attention_args* a, Spans* spans);
+int check_packed_gemm(const spax_packed_gemm_args* a, Spans* spans);
 
 // How an attention call shares out its keys: every key head's sequences, laid end to end, are cut
 // into `shares` equal shares (of the lengths at run time), one workgroup each.
@@ -44,10 +46,32 @@ struct AttentionPlan {
 };
 AttentionPlan attention_plan(const spax_attention_args* a);
 
+// How a chunk attention shares out its work: tiles of query rows (an upper bound; the real number
+// follows from starts), each tile's keys in `pieces` equal pieces.
+struct ChunkPlan {
+  int64_t tiles;
+  int32_t pieces;
+  int64_t blocks;
+  size_t ws_bytes;
+};
+ChunkPlan chunk_plan(const spax_chunk_attention_args* a);
+
+// How a product shares out its work.
+struct GemmPlan {
+  bool wide;             // the tiles of many rows, staged through LDS
+  int32_t row_tiles, col_tiles, splits;
+  int64_t blocks;
+  size_t ws_bytes;
+};
+GemmPlan gemm_plan(const spax_packed_gemm_args* a);
+
 // Launches of validated arguments.
-int launch_kv_append(const spax_kv_append_args* a, hipStream_t s);
+// n: the norm of the heads, or NULL
+int launch_kv_append(const spax_kv_append_args* a, const spax_head_norm* n, hipStream_t s);
 int launch_attention(const spax_attention_args* a, void* ws, hipStream_t s);
 int launch_residual_norm(const spax_residual_norm_args* a, hipStream_t s);
 int launch_glu(const spax_glu_args* a, hipStream_t s);
+int launch_chunk_attention(const spax_chunk_attention_args* a, void* ws, hipStream_t s);
+int launch_packed_gemm(const spax_packed_gemm_args* a, void* ws, hipStream_t s);
 
 }  // namespace spax

@@ -47,12 +47,12 @@ struct Parts {
   Spans append, attention, attn_norm, glu, mlp_norm;
 };
 
-int check_parts(const spax_decoder_layer& L, int i, Parts* b) {
+int check_parts(const spax_decoder_layer& L, const spax_head_norm* norm, int i, Parts* b) {
   if (!L.qkv || !L.append || !L.attention || !L.o || !L.attn_norm || !L.gate_up || !L.glu ||
       !L.down || !L.mlp_norm)
     return fail(SPAX_ERR_NULL, "layer %d: a part is NULL", i);
   int st;
-  if ((st = check_kv_append(L.append, &b->append))) return part_fail(st, i, "append");
+  if ((st = check_kv_append(L.append, norm, &b->append))) return part_fail(st, i, "append");
   if ((st = check_attention(L.attention, &b->attention))) return part_fail(st, i, "attention");
   if ((st = check_residual_norm(L.attn_norm, &b->attn_norm))) return part_fail(st, i, "attn_norm");
   if ((st = check_glu(L.glu, &b->glu))) return part_fail(st, i, "glu");
@@ -104,6 +104,8 @@ int check_parts(const spax_decoder_layer& L, int i, Parts* b) {
 
 struct LayerHooks final : StepHooks {
   const spax_decoder_layer* layers = nullptr;
+  const spax_head_norm* const* norms = nullptr;  // may be NULL
+  const spax_head_norm* norm(int layer) const { return norms ? norms[layer] : nullptr; }
   std::vector<Parts> parts;
   void* ws = nullptr;
   int after(int i, hipStream_t s) override {
@@ -111,7 +113,7 @@ struct LayerHooks final : StepHooks {
     int st = SPAX_OK;
     switch (i % kPhases) {
       case 0:
-        st = launch_kv_append(L.append, s);
+        st = launch_kv_append(L.append, norm(i / kPhases), s);
         return st ? st : launch_attention(L.attention, ws, s);
       case 1: return launch_residual_norm(L.attn_norm, s);
       case 2: return launch_glu(L.glu, s);
@@ -142,20 +144,21 @@ std::vector<spax_phase> phases_of(const spax_decoder_layer* layers, int32_t n) {
   return v;
 }
 
-int decode_layers(const spax_decoder_layer* layers, int32_t n, int32_t flags, void* ws,
-                  size_t ws_bytes, hipStream_t stream) {
+int decode_layers(const spax_decoder_layer* layers, const spax_head_norm* const* norms, int32_t n,
+                  int32_t flags, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!layers) return fail(SPAX_ERR_NULL, "layers is NULL");
   if (n < 1 || n > 65536) return fail(SPAX_ERR_SHAPE, "n_layers %d outside 1..65536", n);
   if (flags & SPAX_STEP_BATCHED)
     return fail(SPAX_ERR_UNSUPPORTED, "SPAX_STEP_BATCHED needs independent phases");
   LayerHooks hooks;
   hooks.layers = layers;
+  hooks.norms = norms;
   hooks.ws = ws;
   hooks.parts.resize((size_t)n);
   size_t need = 0;
   int st;
   for (int i = 0; i < n; ++i) {
-    if ((st = check_parts(layers[i], i, &hooks.parts[i]))) return st;
+    if ((st = check_parts(layers[i], hooks.norm(i), i, &hooks.parts[i]))) return st;
     if (i + 1 < n && layers[i + 1].qkv &&
         ((const void*)layers[i + 1].qkv->x != layers[i].mlp_norm->x ||
          (layers[i + 1].qkv->layout &&
@@ -199,7 +202,7 @@ size_t spax_layers_workspace_bytes(const spax_decoder_layer* layers, int32_t n_l
   const int st = no_throw([&] {
     Parts b;
     for (int i = 0; i < n_layers; ++i) {
-      const int e = check_parts(layers[i], i, &b);
+      const int e = check_parts(layers[i], nullptr, i, &b);
       if (e) return e;
       const size_t w = attention_plan(layers[i].attention).ws_bytes;
       need = w > need ? w : need;
@@ -220,7 +223,17 @@ size_t spax_layers_workspace_bytes(const spax_decoder_layer* layers, int32_t n_l
 int spax_decode_layers(const spax_decoder_layer* layers, int32_t n_layers, int32_t flags,
                        void* ws, size_t ws_bytes, hipStream_t stream) {
   clear_error();
-  return no_throw([&] { return decode_layers(layers, n_layers, flags, ws, ws_bytes, stream); });
+  return no_throw(
+      [&] { return decode_layers(layers, nullptr, n_layers, flags, ws, ws_bytes, stream); });
+}
+
+int spax_decode_layers_normed(const spax_decoder_layer* layers, const spax_head_norm* const* norms,
+                              int32_t n_layers, int32_t flags, void* ws, size_t ws_bytes,
+                              hipStream_t stream) {
+  clear_error();
+  if (!norms) return fail(SPAX_ERR_NULL, "norms is NULL");
+  return no_throw(
+      [&] { return decode_layers(layers, norms, n_layers, flags, ws, ws_bytes, stream); });
 }
 
 }  // extern "C"

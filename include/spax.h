@@ -19,7 +19,8 @@
  *
  * and what stands between two such products in a decoder layer: the append to a paged key-value
  * cache with its rotation, the attention of the new token, the residual add with its norms, and
- * the gated activation ("between the projections" below).
+ * the gated activation ("between the projections" below).  A prompt goes through the same layer
+ * many tokens at a time: spax_packed_gemm, spax_kv_append, spax_chunk_attention.
  *
  * Conventions shared by every entry point:
  *   - Return SPAX_OK (0) or a negative spax_status.  All argument validation happens on
@@ -451,9 +452,10 @@ int spax_decode_step_projections_noalloc(const spax_step* step, hipStream_t stre
 
 /*
  * Operators of a decoder layer that stand between two projection groups: the paged cache append
- * with rotation, the attention of one new token per sequence, the residual add with its norms,
- * and the gated activation.  They take rows of any number of tokens; spax_decode_layers runs
- * them with the projections for the one token of a batch-one step.
+ * with rotation, with or without a norm of each head, the attention of one new token per sequence
+ * or of a chunk of them, the residual add with its norms, and the gated activation; and the
+ * projection of many rows at once.  They take rows of any number of tokens; spax_decode_layers
+ * runs those of one token with the projections of a batch-one step.
  *
  * All of them: pointers inside the structs are device pointers, the structs themselves are host
  * memory read during the call; strides are in elements, positive, and every row's own values
@@ -532,6 +534,35 @@ typedef struct spax_kv_append_args {
 
 int spax_kv_append(const spax_kv_append_args* a, hipStream_t stream);
 
+/* spax_head_norm.kind (and spax_residual_norm_args.kind): x * w / sqrt(mean x^2 + eps), or
+ * (x - mean x) * w / sqrt(mean (x - mean x)^2 + eps); plus the bias if there is one. */
+enum { SPAX_NORM_RMS = 0, SPAX_NORM_LAYER = 1 };
+
+/*
+ * spax_kv_append with a norm of every query head and every key head (over its head_dim values)
+ * before the rotation, in the same pass; values v are cached as they are.  All in 32 bits, one
+ * rounding at the end.
+ *   q_weight, k_weight : head_dim fp32 values, for all heads (stride 0) or a row per head (stride
+ *             >= head_dim); NULL: those heads are not normed (not both NULL; q_weight needs q).
+ *   q_bias, k_bias : likewise, with the strides of their weights; may be NULL.
+ * Squares are summed in 32 bits, as by spax_residual_norm.
+ * Errors: of spax_kv_append; SPAX_ERR_NULL (norm NULL, or without a weight); SPAX_ERR_UNSUPPORTED
+ * (kind); SPAX_ERR_ALIGN; SPAX_ERR_PARAM (eps not finite or < 0, a bias without its weight, q_weight
+ * without q, a stride neither 0 nor >= head_dim, an output that overlaps a weight or bias).
+ */
+typedef struct spax_head_norm {
+  const float* q_weight;
+  const float* q_bias;
+  const float* k_weight;
+  const float* k_bias;
+  int64_t q_stride, k_stride;
+  int32_t kind;
+  float eps;
+} spax_head_norm;
+
+int spax_kv_append_normed(const spax_kv_append_args* a, const spax_head_norm* norm,
+                          hipStream_t stream);
+
 /*
  * Attention of one new token per sequence over the paged cache.  Sequence s (row s of the page
  * table) holds n = lens[s] keys, the new token's own among them; query head h reads key head
@@ -571,9 +602,52 @@ size_t spax_attention_workspace_bytes(const spax_attention_args* a);
 int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes,
                          hipStream_t stream);
 
-/* spax_residual_norm_args.kind: x * w / sqrt(mean x^2 + eps), or (x - mean x) * w /
- * sqrt(mean (x - mean x)^2 + eps); plus the bias if there is one. */
-enum { SPAX_NORM_RMS = 0, SPAX_NORM_LAYER = 1 };
+/*
+ * Attention of a chunk of new tokens per sequence over the paged cache: a prompt, a piece of a long
+ * one, drafted tokens that are checked at once, or any mixture in one call.  The rows of all
+ * sequences are packed: sequence s (row s of the page table) has n_new = starts[s + 1] - starts[s]
+ * new tokens, rows starts[s].. of q and out, and lens[s] keys, the new tokens' own among them
+ * (append first).  Its row i is the token at position p = lens[s] - n_new + i, and over the keys
+ * j in [max(0, p + 1 - window), p] (window 0: all up to p), for query head h with key head
+ * h / (n_heads / n_kv_heads):
+ *   score_j = scale * k_scale * q . k_j,   out = v_scale * sum_j softmax(score)_j v_j,
+ *   lse = ln sum_j exp(score_j).
+ * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)], starts to
+ * [0, n_tokens]; a sequence whose starts do not ascend has no tokens, and rows claimed by two
+ * sequences get either's result.  Keys on entries that name no page are left out; bytes of rows
+ * that a token does not see never reach its result, whatever they hold.  A token with no keys (or at a
+ * negative position), or whose scores are all -inf, gives zeros and lse -inf.  Rows of no
+ * sequence (before starts[0], behind starts[n_seqs]) are left as they were.
+ *   q, out : `type` (SPAX_F16 or SPAX_BF16), the cache's type or the cache E4M3; 16-byte aligned
+ *             with strides a multiple of 8 elements.
+ *   lse    : n_tokens * n_heads, may be NULL.
+ * Probabilities enter the product with v as one `type` value (spax_paged_attention's as two): within
+ * 2^-9 of themselves in BF16, and in F16 within 2^-12 of themselves or 2^-40 of the row's largest so far.
+ *   max_len : host bound on lens; with n_tokens it sets how the keys are shared out.
+ *   ws      : spax_chunk_attention_workspace_bytes(a) bytes (0: none needed), 256-byte aligned,
+ *             any contents; calls that may run at the same time need a workspace each.
+ * n_tokens 0 does nothing.
+ * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (as for the cache; n_heads not a multiple of n_kv_heads or
+ * past 65535; n_tokens < 0, or so many that n_tokens * n_heads passes 2^30; max_len < 1, past
+ * max_pages * page_size or past 2^30; window < 0; more work items than a grid holds);
+ * SPAX_ERR_UNSUPPORTED (types); SPAX_ERR_ALIGN; SPAX_ERR_PARAM (scale not finite, overlapping
+ * buffers); SPAX_ERR_WORKSPACE; SPAX_ERR_HIP.
+ */
+typedef struct spax_chunk_attention_args {
+  const spax_kv_cache* cache;
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* starts;       /* n_seqs + 1 */
+  const int32_t* lens;         /* n_seqs     */
+  int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+  int32_t type, n_heads, n_tokens, max_len, window;
+  float scale;
+} spax_chunk_attention_args;
+
+size_t spax_chunk_attention_workspace_bytes(const spax_chunk_attention_args* a);
+int spax_chunk_attention(const spax_chunk_attention_args* a, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
 
 /*
  * A block's output joins the residual stream, and the next block's input leaves it.  Per row:
@@ -630,6 +704,50 @@ typedef struct spax_glu_args {
 
 int spax_glu(const spax_glu_args* a, hipStream_t stream);
 
+/* spax_packed_gemm_args.form */
+enum { SPAX_GEMM_PLAIN = 0, SPAX_GEMM_ACT = 1, SPAX_GEMM_GATED = 2 };
+
+/*
+ * The product of rows of many tokens with the original columns (region F) of one packed blob, the
+ * projection of a prompt (selection applies per generated token during batch-one decoding:
+ * eigenradar commentary on SpAx, second and last paragraphs).  With W the fused matrices and
+ * t = x W^T + bias (bias NULL: 0), row by row:
+ *   PLAIN: u = t;   ACT: u = act(t);   GATED (two matrices of equal d_out): u = act(t_0) * t_1;
+ *   y = residual + scale * u   (residual NULL: scale * u).
+ * y and residual have d_out_total columns, d_out[0] with GATED.  act: SPAX_ACT_SILU or
+ * SPAX_ACT_GELU_TANH (not read with PLAIN).  A placed blob takes x permuted alike, as by
+ * spax_pack_columns_placed.
+ *   x        : n_rows rows of d_in fp16, 16-byte aligned, x_stride a multiple of 8 (what lies
+ *              between a row's end and the next multiple of 8 may be read and never counts).
+ *   residual : residual_type, y : y_type (SPAX_F32, SPAX_F16, SPAX_BF16); residual may be y itself
+ *              (type and stride alike).
+ * Sums are in 32 bits, in an order that depends on the sizes alone; the weights of an INT4 base
+ * enter the product as w_hat rounded to fp16 (the tiered GEMV keeps them in 32 bits).
+ *   ws       : spax_packed_gemm_workspace_bytes(a) bytes (0: none needed), 256-byte aligned, any
+ *              contents; calls that may run at the same time need a workspace each.
+ * n_rows 0 does nothing.
+ * Errors: SPAX_ERR_NULL; SPAX_ERR_SHAPE (layout not initialised; GATED without two equal
+ * matrices; n_rows < 0 or 2^20 and more); SPAX_ERR_UNSUPPORTED (types, form, act); SPAX_ERR_ALIGN
+ * (packed not 256-byte aligned, x as above, another pointer not aligned to its element);
+ * SPAX_ERR_PARAM (scale not finite, a stride below its row, overlapping buffers);
+ * SPAX_ERR_WORKSPACE; SPAX_ERR_HIP.
+ */
+typedef struct spax_packed_gemm_args {
+  const spax_layout* layout;   /* host pointer to an initialised layout */
+  const void* packed;
+  const uint16_t* x;
+  const float* bias;           /* d_out_total, may be NULL */
+  const void* residual;        /* may be NULL              */
+  void* y;
+  int64_t x_stride, residual_stride, y_stride;
+  int32_t n_rows, form, act, residual_type, y_type;
+  float scale;
+} spax_packed_gemm_args;
+
+size_t spax_packed_gemm_workspace_bytes(const spax_packed_gemm_args* a);
+int spax_packed_gemm(const spax_packed_gemm_args* a, void* ws, size_t ws_bytes,
+                     hipStream_t stream);
+
 /*
  * One decoder layer of a batch-one step, in order: qkv, append, attention, o, attn_norm,
  * gate_up, glu, down, mlp_norm.  attn_norm's x is gate_up's input; mlp_norm's x is the next
@@ -668,6 +786,13 @@ size_t spax_layers_workspace_bytes(const spax_decoder_layer* layers, int32_t n_l
  */
 int spax_decode_layers(const spax_decoder_layer* layers, int32_t n_layers, int32_t flags,
                        void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* spax_decode_layers of layers whose append norms the heads (spax_kv_append_normed): norms[i] is
+ * layer i's, NULL for a layer without; host memory, read during the call.  Errors: also those of
+ * spax_kv_append_normed; SPAX_ERR_NULL if norms is NULL. */
+int spax_decode_layers_normed(const spax_decoder_layer* layers, const spax_head_norm* const* norms,
+                              int32_t n_layers, int32_t flags, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
 
 /* ---------------------------------------------------------------- diagnostics */
 
