@@ -74,7 +74,7 @@ __device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
       t.seq = base + who;
       t.first = __builtin_amdgcn_readlane(first, who);
       t.n_new = __builtin_amdgcn_readlane(n_new, who);
-      t.len = clamp_to(a.lens[t.seq], a.max_len);
+      t.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[t.seq], a.max_len));
       const int begins =
           __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(tiles, who);
       t.from = (index - begins) * kRows;
@@ -93,22 +93,54 @@ __device__ inline int lo_of(const ChunkArgs& a, int p) {
 }
 __device__ inline int hi_of(int p) { return p < 0 ? 0 : p + 1; }
 
+// How a step's keys and values lie in LDS: rows of D 16-bit values, in 16-byte pieces whose places
+// within a row are turned by the row, so that the 16 rows of a pass over K (one piece each) lie on
+// different banks, and the four rows of a transposing read of V (four pieces each) do.
 template <class T, bool NARROW, int D>
 struct Shape {
   static constexpr int kKeys = D >= 192 ? 32 : 64;     // per step
   static constexpr int EB = NARROW ? 1 : 2;
-  static constexpr int kChunks = D * EB / 16;          // 16-byte pieces of a cached row
-  static constexpr int kItems = kKeys * kChunks;       // of a step's keys
-  static constexpr int kLoads = (kItems + kThreads - 1) / kThreads;
-  // Rows in LDS, always 16-bit.  K: an odd number of 16-byte pieces, so that the 16 rows of a read
-  // pass lie on different banks.  V: 64 or 192 bytes past a multiple of 256, so that the four
-  // rows of a transposing read (64 bytes each) do.
-  static constexpr int kKPitch = 2 * D + 16;
-  static constexpr int kVPitch = (2 * D) % 128 == 0 ? 2 * D + 64 : 2 * D;
-  static constexpr int kBuffer = kKeys * (kKPitch + kVPitch);
+  static constexpr int kPieces = D / 8;                // of a row in LDS
+  static constexpr int kRow = 2 * D;
+  static constexpr int kBuffer = 2 * kKeys * kRow;     // keys, then values
   static constexpr int kBlocks = kKeys / 32, kSteps = kKeys / 16;
+  // Where piece c of a row is.
+  static __device__ inline int k_place(int row, int c) {
+    if constexpr (D == 64) return c ^ ((row >> 1) & 7);
+    if constexpr (D == 128 || D == 256) return c ^ (row & 15);
+    return turned(c + (D == 96 ? (row >> 2) & 3 : (row >> 1) & 7));
+  }
+  static __device__ inline int v_place(int row, int c) {
+    if constexpr (D == 64) return c ^ ((row & 2) << 1);
+    if constexpr (D == 128 || D == 256) return c ^ ((row & 3) << 2);
+    return D == 96 ? c : turned(c + 4 * ((row >> 1) & 1));
+  }
+  // Which piece is there.
+  static __device__ inline int k_piece(int row, int at) {
+    if constexpr (D == 64 || D == 128 || D == 256) return k_place(row, at);
+    return turned(at + kPieces - (D == 96 ? (row >> 2) & 3 : (row >> 1) & 7));
+  }
+  static __device__ inline int v_piece(int row, int at) {
+    if constexpr (D == 64 || D == 128 || D == 256) return v_place(row, at);
+    return D == 96 ? at : turned(at + kPieces - 4 * ((row >> 1) & 1));
+  }
+  static __device__ inline int turned(int c) { return c >= kPieces ? c - kPieces : c; }
 };
 
+// 16 bytes a lane from memory to LDS, lane after lane from `to` (uniform) on.  By hand, since the
+// compiler lets every later LDS access wait for such a load; wait_loads() does before a barrier.
+__device__ inline void load_lds(const void* from, const void* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(at), "v"(from)
+               : "memory");
+}
+__device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+
+// Brings a step's keys and values into LDS.  16-bit rows go there straight from memory, 8-bit ones
+// through registers, where they are widened once for all four waves.
 template <class T, bool NARROW, int D>
 struct Loader {
   using S = Shape<T, NARROW, D>;
@@ -128,41 +160,48 @@ struct Loader {
     const int key = key0 + (lane & (S::kKeys - 1));
     return (key | 3) >= lo && (key & ~3) < hi && (uint32_t)entry < (uint32_t)n_pages ? entry : -1;
   }
-  u32x4 kx[S::kLoads], vx[S::kLoads];
-  __device__ inline void load(int page, int key0) {
+  // 16-byte pieces of a step's cached keys, and a thread's share of them
+  static constexpr int kCached = D * S::EB / 16;
+  static constexpr int kItems = S::kKeys * kCached;
+  static constexpr int kLoads = (kItems + kThreads - 1) / kThreads;
+  u32x4 kx[NARROW ? kLoads : 1], vx[NARROW ? kLoads : 1];
+  __device__ inline void load(uint8_t* buffer, int page, int key0, int wave, int lane) {
     const int mask = (1 << page_shift) - 1;
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      const int e = i * kThreads + (int)threadIdx.x;
-      const int row = e / S::kChunks, chunk = e % S::kChunks;
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = NARROW ? i * kThreads + 64 * wave + lane : (wave * kLoads + i) * 64 + lane;
+      const int row = e / kCached, at = e % kCached;
       const int pg = __shfl(page, row);
-      if (S::kItems % kThreads && e >= S::kItems) continue;
+      if (kItems % kThreads && e >= kItems) continue;
       const int64_t p = pg < 0 ? 0 : pg, in = (key0 + row) & mask;  // unseen: any row, masked later
-      kx[i] = *reinterpret_cast<const u32x4*>(k + S::EB * (p * k_page + in * k_row) + 16 * chunk);
-      vx[i] = *reinterpret_cast<const u32x4*>(v + S::EB * (p * v_page + in * v_row) + 16 * chunk);
+      const uint8_t* kr = k + S::EB * (p * k_page + in * k_row);
+      const uint8_t* vr = v + S::EB * (p * v_page + in * v_row);
+      if constexpr (NARROW) {
+        kx[i] = *reinterpret_cast<const u32x4*>(kr + 16 * at);
+        vx[i] = *reinterpret_cast<const u32x4*>(vr + 16 * at);
+      } else {
+        const int first = (wave * kLoads + i) * 1024;
+        load_lds(kr + 16 * S::k_piece(row, at), buffer + first);
+        load_lds(vr + 16 * S::v_piece(row, at), buffer + S::kKeys * S::kRow + first);
+      }
     }
   }
-  // Into LDS; values of keys without a page as zeros.
-  __device__ inline void lay_out(uint8_t* buffer, int page) const {
+  __device__ inline void lay_out(uint8_t* buffer, int wave, int lane) const {
+    if constexpr (NARROW) {
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      const int e = i * kThreads + (int)threadIdx.x;
-      const int row = e / S::kChunks, chunk = e % S::kChunks;
-      const uint32_t keep = __shfl(page, row) >= 0 ? ~0u : 0u;
-      if (S::kItems % kThreads && e >= S::kItems) continue;
-      uint8_t* kr = buffer + row * S::kKPitch + 16 * (NARROW ? 2 : 1) * chunk;
-      uint8_t* vr =
-          buffer + S::kKeys * S::kKPitch + row * S::kVPitch + 16 * (NARROW ? 2 : 1) * chunk;
-      const u32x4 vz = vx[i] & keep;
-      if constexpr (NARROW) {
+      for (int i = 0; i < kLoads; ++i) {
+        const int e = i * kThreads + 64 * wave + lane;
+        const int row = e / kCached, at = e % kCached;
+        if (kItems % kThreads && e >= kItems) continue;
+        uint8_t* kr = buffer + row * S::kRow;
+        uint8_t* vr = kr + S::kKeys * S::kRow;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          *reinterpret_cast<u32x4*>(kr + 16 * y) = widen4(kx[i][2 * y], kx[i][2 * y + 1]);
-          *reinterpret_cast<u32x4*>(vr + 16 * y) = widen4(vz[2 * y], vz[2 * y + 1]);
+          *reinterpret_cast<u32x4*>(kr + 16 * S::k_place(row, 2 * at + y)) =
+              widen4(kx[i][2 * y], kx[i][2 * y + 1]);
+          *reinterpret_cast<u32x4*>(vr + 16 * S::v_place(row, 2 * at + y)) =
+              widen4(vx[i][2 * y], vx[i][2 * y + 1]);
         }
-      } else {
-        *reinterpret_cast<u32x4*>(kr) = kx[i];
-        *reinterpret_cast<u32x4*>(vr) = vz;
       }
     }
   }
@@ -179,26 +218,10 @@ __device__ inline u32x2 read_turned(const uint8_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)p));
 }
 
-// A value that is not finite as a count in a sum of at most 64 of them: 1 for inf, 2^7 for -inf,
-// 2^14 for NaN (powers of two, exact in both types); finite ones as 0.
+// The sign bits of those of two values that are not finite.
 template <class T>
 __device__ inline uint32_t odd_ones(uint32_t w) {
-  typename Mma<T>::v2 x = __builtin_bit_cast(typename Mma<T>::v2, w), y;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float f = (float)x[i];
-    y[i] = (T)(f != f ? 0x1p14f : f == INFINITY ? 1.0f : f == -INFINITY ? 0x1p7f : 0.0f);
-  }
-  return __builtin_bit_cast(uint32_t, y);
-}
-template <class T>
-__device__ inline uint32_t finite_ones(uint32_t w) {
-  const uint32_t bad = ((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u;
-  return w & ~((bad >> 15) * 0xffffu);
-}
-template <class T>
-__device__ inline bool has_odd(uint32_t w) {
-  return (((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u) != 0u;
+  return ((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u;
 }
 
 template <class T, bool NARROW, int D>
@@ -208,22 +231,34 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
   u32x4 q[KC];
   f32x16 o[OB];
   float m, l;
+  // of values that are not finite: whether dim 32 b + i (in o's order, bit 16 b + i) met one that is
+  // not -inf, and one that is not inf
+  uint64_t up[(OB + 3) / 4], down[(OB + 3) / 4];
   int lo, hi;          // this lane's row: the keys it sees
   int lo_max, hi_min;  // of the wave's rows: keys in [lo_max, hi_min) are seen by all
 
-  __device__ inline void score(const uint8_t* keys, int lane, float to_log2,
-                               f32x16 (&s)[S::kBlocks]) const {
+  // Raw scores; the scale is part of soften's multiply-add.  Reads are kept kAhead steps ahead of the
+  // products, by hand: left to itself the compiler waits for each.
+  static constexpr int kAhead = 3;
+  __device__ inline void score(const uint8_t* keys, int lane, f32x16 (&s)[S::kBlocks]) const {
     const int h = lane >> 5, r = lane & 31;
+    u32x4 k[kAhead + 1][S::kBlocks];
+    const auto read = [&](int c) {
 #pragma unroll
-    for (int b = 0; b < S::kBlocks; ++b) {
-      f32x16 x = {};
+      for (int b = 0; b < S::kBlocks; ++b)
+        k[c % (kAhead + 1)][b] = *reinterpret_cast<const u32x4*>(
+            keys + (32 * b + r) * S::kRow + 16 * S::k_place(32 * b + r, 2 * c + h));
+    };
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + (32 * b + r) * S::kKPitch + 32 * c +
-                                                        16 * h);
-        x = Mma<T>::mul32(k, q[c], x);
-      }
-      s[b] = x * to_log2;
+    for (int c = 0; c < kAhead; ++c) read(c);
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b) s[b] = f32x16{};
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      if (c + kAhead < KC) read(c + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b) s[b] = Mma<T>::mul32(k[c % (kAhead + 1)][b], q[c], s[b]);
     }
   }
   // Bit 16 b + i: the lane's row sees key 32 b + 8 (i / 4) + 4 h + i % 4.
@@ -242,13 +277,14 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
     }
     return bits;
   }
-  __device__ inline void soften(f32x16 (&s)[S::kBlocks]) {
+  // Scores to p, times 2^kLift; to_log2 > 0.
+  __device__ inline void soften(f32x16 (&s)[S::kBlocks], float to_log2) {
     float top = s[0][0];
 #pragma unroll
     for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = fmaxf(top, __shfl_xor(top, 32)) * to_log2;
     if (__any(top > m)) {
       const float higher = fmaxf(m, top);
       const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
@@ -258,15 +294,15 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
       for (int t = 0; t < OB; ++t) o[t] *= f;
     }
     const float base = (m == -INFINITY ? 0.0f : m) - Mma<T>::kLift;
-    float sum = 0.0f;
+    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - base);
-        sum += s[b][i];
+        s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], to_log2, -base));
+        sum[i & 1] += s[b][i];
       }
-    l += sum;
+    l += sum[0] + sum[1];
   }
   static __device__ inline u32x4 operand(const f32x16 (&s)[S::kBlocks], int step) {
     u32x4 p;
@@ -281,77 +317,84 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
   }
   static __device__ inline u32x4 read_values(const uint8_t* values, int block, int step, int lane) {
     const int i = lane & 15, g = lane >> 4;
-    const uint8_t* p = values + (16 * step + 4 * (g >> 1) + (i >> 2)) * S::kVPitch +
-                       2 * (32 * block + 16 * (g & 1) + 4 * (i & 3));
-    const u32x2 x = read_turned(p), y = read_turned(p + 8 * S::kVPitch);
+    const int row = 16 * step + 4 * (g >> 1) + (i >> 2);
+    const int piece = 4 * block + 2 * (g & 1) + ((i & 3) >> 1);
+    const uint8_t* p = values + row * S::kRow + 16 * S::v_place(row, piece) + 8 * (i & 1);
+    // (eight rows on, a row's pieces are turned alike)
+    const u32x2 x = read_turned(p), y = read_turned(p + 8 * S::kRow);
     return u32x4{x.x, x.y, y.x, y.y};
   }
-  // o += p v.  EDGE: some row does not see some key.  Values that are not finite then stay out of the
-  // product; a second one counts, for each row and dim, those of keys that the row does see.
-  template <bool EDGE>
   __device__ inline void take_values(const f32x16 (&s)[S::kBlocks], const uint8_t* values,
-                                     uint32_t bits, int lane) {
-    u32x4 p[S::kSteps];
+                                     int lane) {
+    u32x4 v[2][OB];
 #pragma unroll
-    for (int t = 0; t < S::kSteps; ++t) p[t] = operand(s, t);
+    for (int b = 0; b < OB; ++b) v[0][b] = read_values(values, b, 0, lane);
 #pragma unroll
-    for (int b = 0; b < OB; ++b) {
-      u32x4 v[S::kSteps];
-      bool odd = false;
+    for (int t = 0; t < S::kSteps; ++t) {
+      const u32x4 p = operand(s, t);
+      if (t + 1 < S::kSteps)
 #pragma unroll
-      for (int t = 0; t < S::kSteps; ++t) {
-        v[t] = read_values(values, b, t, lane);
-        if constexpr (EDGE)
+        for (int b = 0; b < OB; ++b) v[(t + 1) % 2][b] = read_values(values, b, t + 1, lane);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) odd |= has_odd<T>(v[t][i]);
-      }
-      if (EDGE && __any(odd)) {
-        f32x16 count = {};
+      for (int b = 0; b < OB; ++b) o[b] = Mma<T>::mul32(v[t % 2][b], p, o[b]);
+    }
+  }
+  // Notes which dims of the row meet a value that is not finite, which decides them whatever else
+  // they meet.
+  __device__ inline void note_odd(const uint8_t* values, int key0, int page, int lane) {
+    const int h = lane >> 5;
+    const uint32_t bits = seen(key0, page, lane), others = __shfl_xor(bits, 32);
+#pragma unroll 1
+    for (int key = 0; key < S::kKeys; ++key) {
+      // bit 16 b + 4 g + i of half h is key 32 b + 8 g + 4 h + i
+      const int at = 16 * (key >> 5) + 4 * ((key >> 3) & 3) + (key & 3);
+      const uint32_t mine = ((key >> 2) & 1) == h ? bits : others;
+      const uint32_t keep = (mine >> at) & 1u ? ~0u : 0u;
+#pragma unroll 1
+      for (int g = 0; g < 4 * OB; ++g) {  // dims 8 g + 4 h ..
+        const u32x2 w = *reinterpret_cast<const u32x2*>(values + key * S::kRow +
+                                                        16 * S::v_place(key, g) + 8 * h);
+        uint64_t u = 0, d = 0;
 #pragma unroll
-        for (int t = 0; t < S::kSteps; ++t) {
-          u32x4 fine, bad, one;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            fine[i] = finite_ones<T>(v[t][i]);
-            bad[i] = odd_ones<T>(v[t][i]);
-            typename Mma<T>::v2 x;
-            x.x = (T)(float)((bits >> (8 * t + 2 * i)) & 1u);
-            x.y = (T)(float)((bits >> (8 * t + 2 * i + 1)) & 1u);
-            one[i] = __builtin_bit_cast(uint32_t, x);
+        for (int i = 0; i < 4; ++i) {
+          const typename Mma<T>::v2 x = __builtin_bit_cast(typename Mma<T>::v2, w[i / 2] & keep);
+          const float f = (float)(i % 2 ? x.y : x.x);
+          if (!(fabsf(f) < INFINITY)) {
+            u |= f < 0.0f ? 0u : 1u << i;
+            d |= f > 0.0f ? 0u : 1u << i;
           }
-          o[b] = Mma<T>::mul32(fine, p[t], o[b]);
-          count = Mma<T>::mul32(bad, one, count);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int n = (int)count[i];
-          const bool up = n & 127, down = (n >> 7) & 127, nan = n >> 14;
-          if (n) o[b][i] += nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+        const int to = 4 * (g & 15);
+        up[0] |= g < 16 ? u << to : 0;
+        down[0] |= g < 16 ? d << to : 0;
+        if constexpr (OB > 4) {
+          up[1] |= g < 16 ? 0 : u << to;
+          down[1] |= g < 16 ? 0 : d << to;
         }
-      } else {
-#pragma unroll
-        for (int t = 0; t < S::kSteps; ++t) o[b] = Mma<T>::mul32(v[t], p[t], o[b]);
       }
     }
+  }
+  __device__ inline float value(int b, int i) const {
+    const uint64_t bit = (uint64_t)1 << (16 * (b % 4) + i);
+    const bool u = up[b / 4] & bit, d = down[b / 4] & bit;
+    return u || d ? o[b][i] + (u ? d ? NAN : INFINITY : -INFINITY) : o[b][i];
   }
   __device__ inline void step(const uint8_t* buffer, int key0, int page, bool paged, float to_log2,
                               int lane) {
     f32x16 s[S::kBlocks];
-    score(buffer, lane, to_log2, s);
-    const uint8_t* values = buffer + S::kKeys * S::kKPitch;
-    if (paged && key0 >= lo_max && key0 + S::kKeys <= hi_min) {
-      soften(s);
-      take_values<false>(s, values, 0u, lane);
-    } else {
+    score(buffer, lane, s);
+    const bool edge = !paged || key0 < lo_max || key0 + S::kKeys > hi_min;
+    if (edge) {
       const uint32_t bits = seen(key0, page, lane);
 #pragma unroll
       for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           s[b][i] = (bits >> (16 * b + i)) & 1u ? s[b][i] : -INFINITY;
-      soften(s);
-      take_values<true>(s, values, bits, lane);
     }
+    soften(s, to_log2);
+    take_values(s, buffer + S::kKeys * S::kRow, lane);
   }
 };
 
@@ -374,8 +417,9 @@ template <class T, bool NARROW, int D>
 __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkArgs a) {
   using S = Shape<T, NARROW, D>;
   using R = Rows<T, NARROW, D>;
-  extern __shared__ uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  extern __shared__ __attribute__((aligned(256))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, r = lane & 31;
   // Workgroups go to the 8 XCDs in turn: the tiles of a key head, which read the same rows, meet on
   // few of them.  Later tiles of a sequence see more keys and are begun first.
@@ -402,15 +446,21 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
   const int row = first + r <= last ? first + r : last;
   const bool works = last >= first, mine = works && first + r <= last;
   const int token = works ? row / a.group : 0, head = kvh * a.group + (works ? row % a.group : 0);
+  // The scale is kept above zero, as the largest score is found before it is applied: a sign goes to
+  // the queries, and a scale of zero makes them zeros.
+  const uint32_t flip = to_log2 < 0.0f ? 0x80008000u : 0u, keep = to_log2 == 0.0f ? 0u : ~0u;
+  to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
   R w;
   if (works) {
     const uint8_t* q = (const uint8_t*)a.q + 2 * ((tile.first + token) * a.qt + head * a.qh);
 #pragma unroll
     for (int c = 0; c < R::KC; ++c)
-      w.q[c] = *reinterpret_cast<const u32x4*>(q + 32 * c + 16 * h);
+      w.q[c] = (*reinterpret_cast<const u32x4*>(q + 32 * c + 16 * h) ^ flip) & keep;
   }
 #pragma unroll
   for (int t = 0; t < R::OB; ++t) w.o[t] = f32x16{};
+#pragma unroll
+  for (int t = 0; t < (R::OB + 3) / 4; ++t) w.up[t] = w.down[t] = 0u;
   w.m = -INFINITY;
   w.l = 0.0f;
   w.lo = lo_of(a, tile.position(token));
@@ -423,25 +473,66 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
     hi_max = hi_of(tile.position(last / a.group));
   }
 
+  // 0 * inf is NaN, so where some row does not see some key, values that are not finite are taken out
+  // of the step and noted for the rows that do see them.
+  __shared__ int odd_step[2];
+  const int all_lo = lo_of(a, tile.position((tile.to - 1) / a.group));
+  const int all_hi = hi_of(tile.position(tile.from / a.group));
+  if (threadIdx.x < 2) odd_step[threadIdx.x] = 0;
+
   if (steps.count > 0) {
     int key0 = steps.first * S::kKeys;
     int page = in.page_of(in.look_up(key0, lane), key0, lane);
-    in.load(page, key0);
+    in.load(lds, page, key0, wave, lane);
     int entry = in.look_up(key0 + S::kKeys, lane);
-    in.lay_out(lds, page);
+    in.lay_out(lds, wave, lane);
     for (int i = 0; i < steps.count; ++i) {
-      const uint8_t* buffer = lds + (i & 1) * S::kBuffer;
+      uint8_t* buffer = lds + (i & 1) * S::kBuffer;
+      uint8_t* other = lds + (~i & 1) * S::kBuffer;
+      if constexpr (!NARROW) wait_loads();
       mask::lds_barrier();  // this buffer is laid out, the other one has been read
       const int next = key0 + S::kKeys;
       int next_page = -1;
       if (i + 1 < steps.count) {
         next_page = in.page_of(entry, next, lane);
-        in.load(next_page, next);
+        in.load(other, next_page, next, wave, lane);
         entry = in.look_up(next + S::kKeys, lane);
+      }
+      if (!__all(page >= 0) || key0 < all_lo || key0 + S::kKeys > all_hi) {
+        uint8_t* values = buffer + S::kKeys * S::kRow;
+        constexpr int kMine = S::kKeys * S::kRow / 16;
+        uint32_t odd = 0u;
+        for (int e = threadIdx.x; e < kMine; e += kThreads) {
+          u32x4* at = reinterpret_cast<u32x4*>(values + 16 * e);
+          const u32x4 x = *at;
+          const int row = e / S::kPieces, key = key0 + row;
+          const bool seen = key >= in.lo && key < in.hi && __shfl(page, row) >= 0;
+          const uint32_t bad = odd_ones<T>(x.x) | odd_ones<T>(x.y) | odd_ones<T>(x.z) | odd_ones<T>(x.w);
+          if (!seen && bad) *at = u32x4{0u, 0u, 0u, 0u};  // whatever was left in unused rows
+          odd |= seen ? bad : 0u;
+        }
+        if (__any(odd) && lane == 0) odd_step[i & 1] = 1;
+        mask::lds_barrier();
+        if (__builtin_amdgcn_readfirstlane(odd_step[i & 1])) {
+          if (works) w.note_odd(values, key0, page, lane);
+          mask::lds_barrier();
+          for (int e = threadIdx.x; e < kMine; e += kThreads) {
+            u32x4* at = reinterpret_cast<u32x4*>(values + 16 * e);
+            u32x4 x = *at;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t bad = odd_ones<T>(x[y]);
+              x[y] &= ~(bad | (bad - (bad >> 15)));
+            }
+            *at = x;
+          }
+          mask::lds_barrier();
+          if (threadIdx.x == 0) odd_step[i & 1] = 0;
+        }
       }
       if (works && key0 + S::kKeys > lo_min && key0 < hi_max)
         w.step(buffer, key0, page, __all(page >= 0), to_log2, lane);
-      if (i + 1 < steps.count) in.lay_out(lds + (~i & 1) * S::kBuffer, next_page);
+      if (i + 1 < steps.count) in.lay_out(other, wave, lane);
       key0 = next;
       page = next_page;
     }
@@ -460,7 +551,7 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
       for (int g = 0; g < 4; ++g) {
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = f == 0.0f ? 0.0f : w.o[b][4 * g + i] * f;
+        for (int i = 0; i < 4; ++i) x[i] = f == 0.0f ? 0.0f : w.value(b, 4 * g + i) * f;
         store_n<4>(out + 32 * b + 8 * g + 4 * h, x);
       }
     if (a.lse && h == 0) a.lse[at] = lse_of<T>(w.m, w.l);
@@ -474,7 +565,7 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
       for (int g = 0; g < 4; ++g) {
         f32x4 x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = w.o[b][4 * g + i];
+        for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * g + i);
         *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * g + 4 * h) = x;
       }
   }
@@ -484,37 +575,56 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
   }
 }
 
-// Joins a tile's pieces: four dims of a row a thread.  A piece that a row has no key in has no o.
+// Joins the pieces of a row, a wave each: lane c has the maximum and the sum of piece c (at most 64),
+// four dims a lane, D / 4 lanes a piece.  A piece in which the row sees no key has no o.
 template <class T, int D>
 __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a) {
-  const int kvh = blockIdx.x % (unsigned)a.n_kv;
-  const Tile tile = find_tile(a, blockIdx.x / (unsigned)a.n_kv, threadIdx.x & 63);
-  const float v_mul = a.v_scale ? a.v_scale[kvh] : 1.0f;
-  for (int e = threadIdx.x; e < (tile.to - tile.from) * (D / 4); e += kThreads) {
-    const int row = tile.from + e / (D / 4), d = 4 * (e % (D / 4));
-    const int token = tile.first + row / a.group, head = kvh * a.group + row % a.group;
-    const int64_t at = (int64_t)token * a.n_heads + head;
-    const int64_t step = (int64_t)a.n_tokens * a.n_heads;
-    float m = -INFINITY;
-    for (int c = 0; c < a.pieces; ++c) m = fmaxf(m, a.part_ml[2 * (at + c * step)]);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = 0; c < a.pieces; ++c) {
-      const int64_t part = at + c * step;
-      const float pl = a.part_ml[2 * part + 1];
-      if (pl == 0.0f) continue;
-      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * part] - base);
-      l += f * pl;
-      sum += f * *reinterpret_cast<const f32x4*>(a.part_o + part * D + d);
-    }
-    const float inv = v_mul / l;
-    float out[4];
+  constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes;
+  const int lane = threadIdx.x & 63;
+  const int64_t at =
+      (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int token = (int)(at / a.n_heads), head = (int)(at % a.n_heads);
+  if (token >= a.n_tokens) return;
+  bool claimed = false;
+  for (int s = lane; s < a.n_seqs; s += 64)
+    claimed |= a.starts[s] <= token && token < a.starts[s + 1];
+  if (!__any(claimed)) return;
+  const int64_t step = (int64_t)a.n_tokens * a.n_heads;
+  const bool has = lane < a.pieces;
+  const float pm = has ? a.part_ml[2 * (at + lane * step)] : -INFINITY;
+  const float pl = has ? a.part_ml[2 * (at + lane * step) + 1] : 0.0f;
+  float m = pm;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
-    store_n<4>((T*)a.out + token * a.ot + head * a.oh + d, out);
-    if (a.lse && d == 0) a.lse[at] = lse_of<T>(m, l);
+  for (int z = 32; z > 0; z >>= 1) m = fmaxf(m, __shfl_xor(m, z));
+  const float f = pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - (m == -INFINITY ? 0.0f : m));
+  float l = f * pl;
+#pragma unroll
+  for (int z = 32; z > 0; z >>= 1) l += __shfl_xor(l, z);
+  const int slot = lane / kLanes, d = 4 * (lane % kLanes);
+  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int c0 = 0; c0 < a.pieces; c0 += kAtOnce) {
+    const int c = c0 + slot;
+    const float w = __shfl(f, c & 63), some = __shfl(pl, c & 63);
+    if (slot < kAtOnce && c < a.pieces && some != 0.0f)
+      sum += w * *reinterpret_cast<const f32x4*>(a.part_o + (at + c * step) * D + d);
   }
+  if constexpr (kAtOnce > 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x = sum[i];
+#pragma unroll
+      for (int y = 1; y < kAtOnce; ++y) x += __shfl(sum[i], (lane + y * kLanes) & 63);
+      sum[i] = x;
+    }
+  }
+  if (slot > 0) return;
+  const float inv = (a.v_scale ? a.v_scale[head / a.group] : 1.0f) / l;
+  float out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
+  store_n<4>((T*)a.out + token * a.ot + head * a.oh + d, out);
+  if (a.lse && d == 0) a.lse[at] = lse_of<T>(m, l);
 }
 
 template <class T, bool NARROW, int D>
@@ -523,7 +633,7 @@ int launch(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
   hipLaunchKernelGGL((chunk_kernel<T, NARROW, D>), dim3(blocks), dim3(kThreads), kLds, s, a);
   SPAX_HIP_CHECK(hipGetLastError());
   if (a.pieces > 1) {
-    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)(a.tiles * a.n_kv)),
+    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)(((int64_t)a.n_tokens * a.n_heads + kWaves - 1) / kWaves)),
                        dim3(kThreads), 0, s, a);
     SPAX_HIP_CHECK(hipGetLastError());
   }

@@ -120,7 +120,8 @@ template <bool INT4, int TM>
 __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(GemmArgs a) {
   using F = Few<INT4, TM>;
   extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, r = lane & 31;
   // Workgroups go to the 8 XCDs in turn; those that read the same columns get the same one.
   const int per_xcd = gridDim.x >> 3;
@@ -131,37 +132,52 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
 
   const int half = r >> 4, at = 8 * (r & 15);
   const int col = has_col(a, c_tile, half, at) ? first_col(a, c_tile, half) + at : 0;
-  const f16* x_row[TM];
+  // Addresses are a uniform part and 32 bits of the lane's own (8 records are below 2^28 bytes).
+  const uint32_t w_at = 8u * h * (uint32_t)a.w_stride + (INT4 ? (uint32_t)col / 2 : 2u * col);
+  const uint32_t sz_at = 8u * h * (uint32_t)a.w_stride + (uint32_t)a.n / 2 + (uint32_t)col / 128 * 4;
+  const int m0 = 32 * TM * m_tile;
+  int64_t x_at[TM];
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
-    const int m = 32 * (m_tile * TM + t) + r;
-    x_row[t] = a.x + (int64_t)(m < a.rows ? m : a.rows - 1) * a.xs;
+    const int m = m0 + 32 * t + r;
+    x_at[t] = (int64_t)(m < a.rows ? m : a.rows - 1) * a.xs + 8 * h;
   }
   const auto load = [&](typename F::Step& z, int step) {
     const int k0 = kStep * step;
-    const bool whole = k0 + kStep <= a.k;
-    const int valid = a.k - k0 - 8 * h;  // of the lane's eight
+    if (k0 + kStep <= a.k) {
+      const f16* x = a.x + k0;
+      const uint8_t* rec = a.w + (int64_t)k0 * a.w_stride;
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (valid > 0) v = *reinterpret_cast<const u32x4*>(x_row[t] + k0 + 8 * h);
-      if (!whole) {
+      for (int t = 0; t < TM; ++t) z.x[t] = *reinterpret_cast<const u32x4*>(x + x_at[t]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e, rec += a.w_stride) {
+        if constexpr (INT4) {
+          z.q[e] = *reinterpret_cast<const uint32_t*>(rec + w_at);
+          z.sz[e] = *reinterpret_cast<const uint32_t*>(rec + sz_at);
+        } else {
+          z.w[e] = *reinterpret_cast<const u32x4*>(rec + w_at);
+        }
+      }
+    } else {  // the last k: past them x counts as zeros, and the last record stands in
+      const int valid = a.k - k0 - 8 * h;  // of the lane's eight
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (valid > 0) v = *reinterpret_cast<const u32x4*>(a.x + k0 + x_at[t]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           v[i] &= 2 * i + 1 < valid ? ~0u : 2 * i < valid ? 0xffffu : 0u;
+        z.x[t] = v;
       }
-      z.x[t] = v;
-    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // past the last record: the last one again, times zero
-      const int64_t row = whole || e < valid ? k0 + 8 * h + e : a.k - 1;
-      const uint8_t* rec = a.w + row * a.w_stride;
-      if constexpr (INT4) {
-        z.q[e] = *reinterpret_cast<const uint32_t*>(rec + col / 2);
-        z.sz[e] = *reinterpret_cast<const uint32_t*>(rec + a.n / 2 + col / 128 * 4);
-      } else {
-        z.w[e] = *reinterpret_cast<const u32x4*>(rec + 2 * (int64_t)col);
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* rec = a.w + (int64_t)(e < valid ? k0 + 8 * h + e : a.k - 1) * a.w_stride;
+        if constexpr (INT4) {
+          z.q[e] = *reinterpret_cast<const uint32_t*>(rec + col / 2);
+          z.sz[e] = *reinterpret_cast<const uint32_t*>(rec + a.n / 2 + col / 128 * 4);
+        } else {
+          z.w[e] = *reinterpret_cast<const u32x4*>(rec + 2 * (int64_t)col);
+        }
       }
     }
   };
@@ -206,16 +222,13 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
   const int steps = (a.k + kStep - 1) / kStep;
   const int stop = (split + 1) * a.steps < steps ? (split + 1) * a.steps : steps;
   int s = split * a.steps + wave;
-  typename F::Step z0, z1;
-  if (s < stop) load(z0, s);
-  while (s < stop) {
-    if (s + F::kWaves < stop) load(z1, s + F::kWaves);
-    use(z0);
-    s += F::kWaves;
-    if (s >= stop) break;
-    if (s + F::kWaves < stop) load(z0, s + F::kWaves);
-    use(z1);
-    s += F::kWaves;
+  typename F::Step z;
+  if (s < stop) load(z, s);
+  for (; s < stop; s += F::kWaves) {
+    typename F::Step next = z;
+    if (s + F::kWaves < stop) load(next, s + F::kWaves);
+    use(z);
+    z = next;
   }
 
   // Join the waves, some rows at a time.  A lane has row r of each tile, and of register i of every
@@ -244,7 +257,7 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
       const bool gated = a.form == SPAX_GEMM_GATED && a.splits == 1;
       for (int e = threadIdx.x; e < F::kRound * (gated ? 32 : 64); e += F::kThreads) {
         const int row = gated ? e / 32 : e / 64, c = 4 * (gated ? e % 32 : e % 64);
-        const int m = 32 * (m_tile * TM + t) + from + row;
+        const int m = m0 + 32 * t + from + row;
         if (m >= a.rows || !has_col(a, c_tile, c >> 7, c & 127)) continue;
         f32x4 sum0 = {0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;
         for (int w = 0; w < F::kWaves; ++w) {
