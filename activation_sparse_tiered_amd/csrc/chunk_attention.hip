@@ -40,7 +40,7 @@ struct ChunkArgs {
   int64_t qt, qh, ot, oh;
   int64_t k_page, k_head, k_row, v_page, v_head, v_row, table_stride;
   int32_t n_tokens, n_heads, n_kv, group, n_seqs, n_pages, page_shift;
-  int32_t max_len, window, tiles, pieces;
+  int32_t max_len, window, tiles, pieces, least_steps;
   float scale;
 };
 
@@ -53,30 +53,49 @@ struct Tile {
 
 __device__ inline int clamp_to(int x, int most) { return x < 0 ? 0 : x > most ? most : x; }
 
+// The keys [lo, hi) that the token at position p sees.
+__device__ inline int lo_of(const ChunkArgs& a, int p) {
+  return a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
+}
+__device__ inline int hi_of(int p) { return p < 0 ? 0 : p + 1; }
+
+// Steps of `keys` keys that hold [lo, hi).
+__device__ inline int steps_in(int lo, int hi, int keys) {
+  return hi > lo ? (hi + keys - 1) / keys - lo / keys : 0;
+}
+
+// Sequence s = base + lane: its first row, new tokens and tiles.
+struct Seq {
+  int first, n_new, tiles;
+};
+__device__ inline Seq seq_at(const ChunkArgs& a, int s) {
+  Seq q{0, 0, 0};
+  if (s < a.n_seqs) {
+    q.first = clamp_to(a.starts[s], a.n_tokens);
+    const int n = clamp_to(a.starts[s + 1], a.n_tokens) - q.first;
+    q.n_new = n < 0 ? 0 : n;
+    q.tiles = (q.n_new * a.group + kRows - 1) / kRows;
+  }
+  return q;
+}
+
 // Tile `index` of all sequences' tiles laid end to end.  Lane l holds sequence base + l; past 64
 // sequences that is a chain of loads, one for every 64.
 __device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
   int before = 0;
   for (int base = 0; base < a.n_seqs; base += 64) {
-    const int s = base + lane;
-    int first = 0, n_new = 0;
-    if (s < a.n_seqs) {
-      first = clamp_to(a.starts[s], a.n_tokens);
-      n_new = clamp_to(a.starts[s + 1], a.n_tokens) - first;
-      n_new = n_new < 0 ? 0 : n_new;
-    }
-    const int tiles = (n_new * a.group + kRows - 1) / kRows;
-    const int upto = before + mask::wave_scan(tiles);
+    const Seq q = seq_at(a, base + lane);
+    const int upto = before + mask::wave_scan(q.tiles);
     const int last = __builtin_amdgcn_readlane(upto, 63);
     if (index < last) {
       const int who = __builtin_ctzll(__ballot(upto > index));
       Tile t;
       t.seq = base + who;
-      t.first = __builtin_amdgcn_readlane(first, who);
-      t.n_new = __builtin_amdgcn_readlane(n_new, who);
+      t.first = __builtin_amdgcn_readlane(q.first, who);
+      t.n_new = __builtin_amdgcn_readlane(q.n_new, who);
       t.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[t.seq], a.max_len));
       const int begins =
-          __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(tiles, who);
+          __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(q.tiles, who);
       t.from = (index - begins) * kRows;
       const int rows = t.n_new * a.group;
       t.to = t.from + kRows < rows ? t.from + kRows : rows;
@@ -87,11 +106,47 @@ __device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
   return Tile{0, 0, 0, 0, 0, 0};
 }
 
-// The keys [lo, hi) that the token at position p sees.
-__device__ inline int lo_of(const ChunkArgs& a, int p) {
-  return a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0;
+// How many steps of a tile's keys make a piece: an equal share of all tiles' steps for each of kShares
+// workgroups, but no fewer than the plan has room for.  Every wave of both launches finds the same
+// number, in integers, from at most kCounted sequences; with more the plan's own stands.
+constexpr int kShares = 512, kCounted = 256;
+__device__ inline int piece_steps(const ChunkArgs& a, int keys, int lane) {
+  if (a.pieces == 1 || a.n_seqs > kCounted) return a.least_steps;
+  int mine = 0;
+  for (int base = 0; base < a.n_seqs; base += 64) {
+    const int s = base + lane;
+    const Seq q = seq_at(a, s);
+    if (q.n_new == 0) continue;
+    const int len = clamp_to(a.lens[s], a.max_len), p = len - q.n_new;
+    // of the first token and of the last
+    const int some = steps_in(lo_of(a, p), hi_of(p), keys);
+    const int more = steps_in(lo_of(a, len - 1), hi_of(len - 1), keys);
+    const int64_t units = (int64_t)q.tiles * ((some + more + 1) / 2);
+    constexpr int kMost = 1 << 22;  // kCounted of them stay below 2^31
+    mine += units < kMost ? (int)units : kMost;
+  }
+#pragma unroll
+  for (int z = 32; z > 0; z >>= 1) mine += __shfl_xor(mine, z);
+  mine = __builtin_amdgcn_readfirstlane(mine);
+  const int64_t share = ((int64_t)mine * a.n_kv + kShares - 1) / kShares;
+  return share > a.least_steps ? (int)share : a.least_steps;
 }
-__device__ inline int hi_of(int p) { return p < 0 ? 0 : p + 1; }
+
+// The tile's keys [lo, hi), the steps of one piece of them, and how many pieces there are.
+struct Piece {
+  int lo, hi, first, count, pieces;
+};
+__device__ inline Piece piece_of(const ChunkArgs& a, const Tile& t, int piece, int per, int keys) {
+  Piece p;
+  p.hi = hi_of(t.position((t.to - 1) / a.group));
+  p.lo = lo_of(a, t.position(t.from / a.group));
+  const int all = steps_in(p.lo, p.hi, keys);
+  p.pieces = (all + per - 1) / per;
+  const int from = piece * per < all ? piece * per : all;
+  p.first = p.lo / keys + from;
+  p.count = from + per < all ? per : all - from;
+  return p;
+}
 
 // How a step's keys and values lie in LDS: rows of D 16-bit values, in 16-byte pieces whose places
 // within a row are turned by the row, so that the 16 rows of a pass over K (one piece each) lie on
@@ -398,21 +453,6 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
   }
 };
 
-// The tile's steps of keys, and those of one piece of it.
-struct Span2 {
-  int first, count;
-};
-template <int KEYS>
-__device__ inline Span2 steps_of(const ChunkArgs& a, const Tile& t, int piece, int* lo, int* hi) {
-  *hi = hi_of(t.position((t.to - 1) / a.group));
-  *lo = lo_of(a, t.position(t.from / a.group));
-  const int first = *lo / KEYS, all = *hi > *lo ? (*hi + KEYS - 1) / KEYS - first : 0;
-  const int per = (all + a.pieces - 1) / a.pieces;
-  const int from = piece * per < all ? piece * per : all;
-  const int to = from + per < all ? from + per : all;
-  return Span2{first + from, to - from};
-}
-
 template <class T, bool NARROW, int D>
 __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkArgs a) {
   using S = Shape<T, NARROW, D>;
@@ -429,7 +469,10 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
   if (tile.from == tile.to) return;
 
   Loader<T, NARROW, D> in;
-  const Span2 steps = steps_of<S::kKeys>(a, tile, piece, &in.lo, &in.hi);
+  const Piece steps = piece_of(a, tile, piece, piece_steps(a, S::kKeys, lane), S::kKeys);
+  if (piece > 0 && piece >= steps.pieces) return;
+  in.lo = steps.lo;
+  in.hi = steps.hi;
   float to_log2 = a.scale * kLog2e, v_mul = 1.0f;
   if constexpr (NARROW) {
     if (a.k_scale) to_log2 *= a.k_scale[kvh];
@@ -542,7 +585,7 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
   w.l += __shfl_xor(w.l, 32);
   if (!mine) return;
   const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
-  if (a.pieces == 1) {
+  if (steps.pieces <= 1) {
     const float f = w.l == 0.0f ? 0.0f : v_mul / w.l;
     T* out = (T*)a.out + (tile.first + token) * a.ot + head * a.oh;
 #pragma unroll
@@ -558,17 +601,15 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
     return;
   }
   const int64_t part = (int64_t)piece * a.n_tokens * a.n_heads + at;
-  if (steps.count > 0) {
 #pragma unroll
-    for (int b = 0; b < R::OB; ++b)
+  for (int b = 0; b < R::OB; ++b)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        f32x4 x;
+    for (int g = 0; g < 4; ++g) {
+      f32x4 x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * g + i);
-        *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * g + 4 * h) = x;
-      }
-  }
+      for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * g + i);
+      *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * g + 4 * h) = x;
+    }
   if (h == 0) {
     a.part_ml[2 * part] = w.m;
     a.part_ml[2 * part + 1] = w.l;
@@ -576,38 +617,69 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
 }
 
 // Joins the pieces of a row, a wave each: lane c has the maximum and the sum of piece c (at most 64),
-// four dims a lane, D / 4 lanes a piece.  A piece in which the row sees no key has no o.
+// four dims a lane, D / 4 lanes a piece.  Rows whose tile is one piece have their result already.
 template <class T, int D>
 __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a) {
-  constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes;
+  constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kLoads = 8;
+  constexpr int kKeys = D >= 192 ? 32 : 64;
   const int lane = threadIdx.x & 63;
   const int64_t at =
       (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int token = (int)(at / a.n_heads), head = (int)(at % a.n_heads);
   if (token >= a.n_tokens) return;
-  bool claimed = false;
-  for (int s = lane; s < a.n_seqs; s += 64)
-    claimed |= a.starts[s] <= token && token < a.starts[s + 1];
-  if (!__any(claimed)) return;
+  Tile tile{0, 0, 0, 0, 0, 0};
+  for (int base = 0; base < a.n_seqs; base += 64) {
+    const Seq q = seq_at(a, base + lane);
+    const uint64_t has = __ballot(token >= q.first && token - q.first < q.n_new);
+    if (!has) continue;
+    const int who = __builtin_ctzll(has);
+    tile.seq = base + who;
+    tile.first = __builtin_amdgcn_readlane(q.first, who);
+    tile.n_new = __builtin_amdgcn_readlane(q.n_new, who);
+    tile.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[tile.seq], a.max_len));
+    const int row = (token - tile.first) * a.group + head % a.group, rows = tile.n_new * a.group;
+    tile.from = row / kRows * kRows;
+    tile.to = tile.from + kRows < rows ? tile.from + kRows : rows;
+    break;
+  }
+  if (tile.from == tile.to) return;
+  const int pieces = piece_of(a, tile, 0, piece_steps(a, kKeys, lane), kKeys).pieces;
+  if (pieces <= 1) return;
   const int64_t step = (int64_t)a.n_tokens * a.n_heads;
-  const bool has = lane < a.pieces;
+  const int slot = lane / kLanes, d = 4 * (lane % kLanes);
+  const float* from = a.part_o + at * D + d;
+  f32x4 x[kLoads];
+#pragma unroll
+  for (int y = 0; y < kLoads; ++y) {
+    const int c = y * kAtOnce + slot;
+    x[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (slot < kAtOnce && c < pieces) x[y] = *reinterpret_cast<const f32x4*>(from + c * step * D);
+  }
+  const bool has = lane < pieces;
   const float pm = has ? a.part_ml[2 * (at + lane * step)] : -INFINITY;
   const float pl = has ? a.part_ml[2 * (at + lane * step) + 1] : 0.0f;
   float m = pm;
 #pragma unroll
   for (int z = 32; z > 0; z >>= 1) m = fmaxf(m, __shfl_xor(m, z));
-  const float f = pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - (m == -INFINITY ? 0.0f : m));
+  const float f = has ? __builtin_amdgcn_exp2f(pm - (m == -INFINITY ? 0.0f : m)) : 0.0f;
   float l = f * pl;
 #pragma unroll
   for (int z = 32; z > 0; z >>= 1) l += __shfl_xor(l, z);
-  const int slot = lane / kLanes, d = 4 * (lane % kLanes);
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-  for (int c0 = 0; c0 < a.pieces; c0 += kAtOnce) {
-    const int c = c0 + slot;
-    const float w = __shfl(f, c & 63), some = __shfl(pl, c & 63);
-    if (slot < kAtOnce && c < a.pieces && some != 0.0f)
-      sum += w * *reinterpret_cast<const f32x4*>(a.part_o + (at + c * step) * D + d);
+  for (int c0 = 0;;) {
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const int c = c0 + y * kAtOnce + slot;
+      sum += __shfl(f, c & 63) * x[y];
+    }
+    c0 += kLoads * kAtOnce;
+    if (c0 >= pieces) break;
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const int c = c0 + y * kAtOnce + slot;
+      x[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (slot < kAtOnce && c < pieces) x[y] = *reinterpret_cast<const f32x4*>(from + c * step * D);
+    }
   }
   if constexpr (kAtOnce > 1) {
 #pragma unroll
@@ -651,6 +723,8 @@ int launch_dim(const ChunkArgs& a, int dim, unsigned blocks, hipStream_t s) {
   }
 }
 
+constexpr int kLeastSteps = 6;
+
 }  // namespace
 
 ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
@@ -663,10 +737,14 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   int64_t keys = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->n_tokens < keys)
     keys = (int64_t)a->window + a->n_tokens;
-  const int64_t steps = (keys + 63) / 64, items = p.tiles * c.n_kv_heads;
-  int64_t pieces = 512 / items;
-  if (pieces > steps / 2) pieces = steps / 2;
-  p.pieces = (int32_t)(pieces < 1 ? 1 : pieces > 64 ? 64 : pieces);
+  const int64_t width = c.head_dim >= 192 ? 32 : 64;
+  const int64_t steps = (keys + width - 1) / width + 1;  // a window starts anywhere
+  const int64_t items = p.tiles * c.n_kv_heads;
+  int64_t pieces = 2048 / items;
+  if (pieces > steps / kLeastSteps) pieces = steps / kLeastSteps;
+  pieces = pieces < 1 ? 1 : pieces > 64 ? 64 : pieces;
+  p.least_steps = (int32_t)((steps + pieces - 1) / pieces);
+  p.pieces = (int32_t)((steps + p.least_steps - 1) / p.least_steps);
   p.blocks = items * p.pieces;
   if (p.pieces > 1)
     p.ws_bytes = aligned_size((size_t)p.pieces * a->n_tokens * a->n_heads *
@@ -692,6 +770,7 @@ int launch_chunk_attention(const spax_chunk_attention_args* p, void* ws, hipStre
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   a.max_len = p->max_len; a.window = p->window; a.scale = p->scale;
   a.tiles = (int32_t)plan.tiles; a.pieces = plan.pieces;
+  a.least_steps = plan.least_steps;
   a.part_o = (float*)ws;
   a.part_ml = (float*)ws + (size_t)plan.pieces * p->n_tokens * p->n_heads * c.head_dim;
   const unsigned blocks = (unsigned)plan.blocks;

@@ -47,10 +47,10 @@ struct AttentionPlan {
 AttentionPlan attention_plan(const spax_attention_args* a);
 
 // How a chunk attention shares out its work: tiles of query rows (an upper bound; the real number
-// follows from starts), each tile's keys in `pieces` equal pieces.
+// follows from starts), each tile's keys in at most `pieces` pieces of at least least_steps steps.
 struct ChunkPlan {
   int64_t tiles;
-  int32_t pieces;
+  int32_t pieces, least_steps;
   int64_t blocks;
   size_t ws_bytes;
 };
@@ -58,8 +58,9 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a);
 
 // How a product shares out its work.
 struct GemmPlan {
-  bool wide;             // the tiles of many rows, staged through LDS
-  int32_t row_tiles, col_tiles, splits;
+  int32_t tile;                 // rows of a tile
+  int32_t row_tiles, col_tiles;
+  int32_t splits, steps;        // of the k; steps of one of them
   int64_t blocks;
   size_t ws_bytes;
 };

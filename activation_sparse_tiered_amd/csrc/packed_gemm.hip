@@ -8,6 +8,7 @@
 // operand j stands for column 8 i + j.
 #include "act.h"
 #include "layer_ops.h"
+#include "mask_core.h"
 
 namespace spax {
 namespace {
@@ -101,24 +102,25 @@ __device__ inline uint32_t widen2(uint32_t u, int i, f16x2 s, f16x2 z) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, s, z));
 }
 
-// TM tiles of 32 rows, 256 columns; the workgroup's waves take every kWaves-th step of its k.
-template <bool INT4, int TM>
+// 32 rows, 256 columns; the workgroup's waves take every kWaves-th step of its k.
+template <bool INT4>
 struct Few {
-  static constexpr int kWaves = TM == 1 ? 8 : 4;
+  static constexpr int kWaves = 8;
+  static constexpr int kAhead = INT4 ? 3 : 2;  // steps in flight
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kRound = 128 / kWaves;  // rows joined at once
   static constexpr int kPitch = kCols + 4;     // floats between rows in LDS
   static constexpr int kLds = kWaves * kRound * kPitch * 4;
   struct Step {
-    u32x4 x[TM];
+    u32x4 x;
     u32x4 w[INT4 ? 1 : 8];
     uint32_t q[INT4 ? 8 : 1], sz[INT4 ? 8 : 1];
   };
 };
 
-template <bool INT4, int TM>
-__global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(GemmArgs a) {
-  using F = Few<INT4, TM>;
+template <bool INT4>
+__global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs a) {
+  using F = Few<INT4>;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -135,20 +137,14 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
   // Addresses are a uniform part and 32 bits of the lane's own (8 records are below 2^28 bytes).
   const uint32_t w_at = 8u * h * (uint32_t)a.w_stride + (INT4 ? (uint32_t)col / 2 : 2u * col);
   const uint32_t sz_at = 8u * h * (uint32_t)a.w_stride + (uint32_t)a.n / 2 + (uint32_t)col / 128 * 4;
-  const int m0 = 32 * TM * m_tile;
-  int64_t x_at[TM];
-#pragma unroll
-  for (int t = 0; t < TM; ++t) {
-    const int m = m0 + 32 * t + r;
-    x_at[t] = (int64_t)(m < a.rows ? m : a.rows - 1) * a.xs + 8 * h;
-  }
+  const int m0 = 32 * m_tile;
+  const int64_t x_at = (int64_t)(m0 + r < a.rows ? m0 + r : a.rows - 1) * a.xs + 8 * h;
   const auto load = [&](typename F::Step& z, int step) {
     const int k0 = kStep * step;
     if (k0 + kStep <= a.k) {
       const f16* x = a.x + k0;
       const uint8_t* rec = a.w + (int64_t)k0 * a.w_stride;
-#pragma unroll
-      for (int t = 0; t < TM; ++t) z.x[t] = *reinterpret_cast<const u32x4*>(x + x_at[t]);
+      z.x = *reinterpret_cast<const u32x4*>(x + x_at);
 #pragma unroll
       for (int e = 0; e < 8; ++e, rec += a.w_stride) {
         if constexpr (INT4) {
@@ -160,15 +156,12 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
       }
     } else {  // the last k: past them x counts as zeros, and the last record stands in
       const int valid = a.k - k0 - 8 * h;  // of the lane's eight
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (valid > 0) v = *reinterpret_cast<const u32x4*>(a.x + k0 + x_at);
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (valid > 0) v = *reinterpret_cast<const u32x4*>(a.x + k0 + x_at[t]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] &= 2 * i + 1 < valid ? ~0u : 2 * i < valid ? 0xffffu : 0u;
-        z.x[t] = v;
-      }
+      for (int i = 0; i < 4; ++i)
+        v[i] &= 2 * i + 1 < valid ? ~0u : 2 * i < valid ? 0xffffu : 0u;
+      z.x = v;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint8_t* rec = a.w + (int64_t)(e < valid ? k0 + 8 * h + e : a.k - 1) * a.w_stride;
@@ -181,13 +174,9 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
       }
     }
   };
-  f32x16 acc[8][TM];
+  f32x16 acc[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int t = 0; t < TM; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[j][t][i] = 0.0f;
+  for (int j = 0; j < 8; ++j) acc[j] = f32x16{};
   const auto use = [&](const typename F::Step& z) {
     uint32_t lo[4], hi[4];  // int4: columns 0..3 and 4..7 of k and k + 1
     f16x2 s[4], zero[4];
@@ -213,64 +202,287 @@ __global__ __launch_bounds__((Few<INT4, TM>::kThreads)) void gemm_few_kernel(Gem
           f[p] = __builtin_amdgcn_perm(z.w[2 * p + 1][j / 2], z.w[2 * p][j / 2],
                                        j & 1 ? 0x07060302u : 0x05040100u);
       }
-#pragma unroll
-      for (int t = 0; t < TM; ++t)
-        acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            __builtin_bit_cast(f16x8, f), __builtin_bit_cast(f16x8, z.x[t]), acc[j][t], 0, 0, 0);
+      acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          __builtin_bit_cast(f16x8, f), __builtin_bit_cast(f16x8, z.x), acc[j], 0, 0, 0);
     }
   };
   const int steps = (a.k + kStep - 1) / kStep;
   const int stop = (split + 1) * a.steps < steps ? (split + 1) * a.steps : steps;
   int s = split * a.steps + wave;
-  typename F::Step z;
-  if (s < stop) load(z, s);
+  typename F::Step z[F::kAhead];
+#pragma unroll
+  for (int y = 0; y < F::kAhead; ++y)
+    if (s + y * F::kWaves < stop) load(z[y], s + y * F::kWaves);
   for (; s < stop; s += F::kWaves) {
-    typename F::Step next = z;
-    if (s + F::kWaves < stop) load(next, s + F::kWaves);
-    use(z);
-    z = next;
+    typename F::Step next = z[F::kAhead - 1];
+    if (s + F::kAhead * F::kWaves < stop) load(next, s + F::kAhead * F::kWaves);
+    use(z[0]);
+#pragma unroll
+    for (int y = 0; y + 1 < F::kAhead; ++y) z[y] = z[y + 1];
+    z[F::kAhead - 1] = next;
   }
 
-  // Join the waves, some rows at a time.  A lane has row r of each tile, and of register i of every
-  // operand columns 8 (8 (i / 4) + 4 h + i % 4) ..
+  // Join the waves, half of the rows at a time.  A lane has row r, and of register i of every operand
+  // columns 8 (8 (i / 4) + 4 h + i % 4) ..
 #pragma unroll
-  for (int t = 0; t < TM; ++t) {
+  for (int from = 0; from < 32; from += F::kRound) {
+    if (from) __syncthreads();
+    if (r >= from && r < from + F::kRound) {
+      float* to = lds + (wave * F::kRound + r - from) * F::kPitch;
 #pragma unroll
-    for (int from = 0; from < 32; from += F::kRound) {
-      if (t || from) __syncthreads();
-      if (r >= from && r < from + F::kRound) {
-        float* to = lds + (wave * F::kRound + r - from) * F::kPitch;
+      for (int i = 0; i < 16; ++i) {
+        f32x4 v0, v1;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f32x4 v0, v1;
+        for (int j = 0; j < 4; ++j) {
+          v0[j] = acc[j][i];
+          v1[j] = acc[j + 4][i];
+        }
+        float* p = to + 8 * (8 * (i / 4) + 4 * h + i % 4);
+        *reinterpret_cast<f32x4*>(p) = v0;
+        *reinterpret_cast<f32x4*>(p + 4) = v1;
+      }
+    }
+    __syncthreads();
+    const bool gated = a.form == SPAX_GEMM_GATED && a.splits == 1;
+    for (int e = threadIdx.x; e < F::kRound * (gated ? 32 : 64); e += F::kThreads) {
+      const int row = gated ? e / 32 : e / 64, c = 4 * (gated ? e % 32 : e % 64);
+      const int m = m0 + from + row;
+      if (m >= a.rows || !has_col(a, c_tile, c >> 7, c & 127)) continue;
+      f32x4 sum0 = {0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v0[j] = acc[j][t][i];
-            v1[j] = acc[j + 4][t][i];
+      for (int w = 0; w < F::kWaves; ++w) {
+        const float* p = lds + (w * F::kRound + row) * F::kPitch + c;
+        sum0 += *reinterpret_cast<const f32x4*>(p);
+        if (gated) sum1 += *reinterpret_cast<const f32x4*>(p + 128);
+      }
+      const int col = first_col(a, c_tile, c >> 7) + (c & 127);
+      if (a.splits == 1)
+        finish(a, m, col, sum0, sum1);
+      else
+        *reinterpret_cast<f32x4*>(a.parts + ((int64_t)split * a.rows + m) * a.n + col) = sum0;
+    }
+  }
+}
+
+// 16 bytes a lane from memory to LDS, lane after lane from `to` (uniform) on.  By hand, since the
+// compiler lets every later LDS access wait for such a load; wait_loads() does before a barrier.
+__device__ inline void load_lds(const void* from, const void* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(at), "v"(from)
+               : "memory");
+}
+__device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+
+// Four rows of k of one column per lane: 16 columns for every 16 lanes.
+__device__ inline u32x2 read_turned(const uint8_t* p) {
+  typedef short v4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4 lds_v4;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)p));
+}
+
+// Eight int4 values of one k, packed as stored, as fp16 in order.
+__device__ inline u32x4 widen8(uint32_t w, f16x2 s, f16x2 z) {
+  uint32_t r[4];  // columns i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = widen2(w, i, s, z);
+  return u32x4{__builtin_amdgcn_perm(r[1], r[0], 0x05040100u),
+               __builtin_amdgcn_perm(r[3], r[2], 0x05040100u),
+               __builtin_amdgcn_perm(r[1], r[0], 0x07060302u),
+               __builtin_amdgcn_perm(r[3], r[2], 0x07060302u)};
+}
+
+// Many rows: 64 TT of them by 256 columns, 64 k a step, staged in LDS for eight waves: two of 32 TT rows
+// by four of 32 columns in each block of 128.
+template <bool INT4, int TT>
+struct Many {
+  static constexpr int kThreads = 512, kRows = 64 * TT, kDepth = 64;
+  static constexpr int kX = kRows * kDepth * 2, kW = kDepth * kCols * 2;
+  static constexpr int kStage = kX + kW;
+  static constexpr int kPitch = kCols + 4;            // floats between rows in the last exchange
+  static constexpr int kExchange = 32 * TT * kPitch * 4;  // half of the rows at a time
+  static constexpr int kLds = 2 * kStage > kExchange ? 2 * kStage : kExchange;
+  // Where 16-byte piece c of a row of x (eight pieces) and of W (32) lies: 16 rows of a piece of x,
+  // and four rows of four neighbouring pieces of W, are on different banks.
+  static __device__ inline int x_place(int row, int c) { return c ^ ((row >> 1) & 7); }
+  static __device__ inline int w_place(int row, int c) { return c ^ ((row & 3) << 2); }
+};
+
+template <bool INT4, int TT>
+__global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kernel(GemmArgs a) {
+  using M = Many<INT4, TT>;
+  extern __shared__ __attribute__((aligned(256))) uint8_t stages[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, r = lane & 31;
+  const int per_xcd = gridDim.x >> 3;
+  const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  const int m_tile = item % a.row_tiles, rest = item / a.row_tiles;
+  const int split = rest % a.splits, c_tile = rest / a.splits;
+  if (c_tile >= a.col_tiles) return;
+  const int m0 = M::kRows * m_tile;
+
+  const int steps = (a.k + M::kDepth - 1) / M::kDepth;
+  const int first = split * a.steps;
+  const int stop = first + a.steps < steps ? first + a.steps : steps;
+
+  // A thread's pieces of a step: of x by rows, of W by k.
+  constexpr int kXLoads = M::kX / 16 / M::kThreads, kWLoads = INT4 ? 1 : M::kW / 16 / M::kThreads;
+  const f16* x_from[kXLoads];
+#pragma unroll
+  for (int i = 0; i < kXLoads; ++i) {
+    const int e = (wave * kXLoads + i) * 64 + lane, row = e / 8, at = e % 8;
+    const int m = m0 + row < a.rows ? m0 + row : a.rows - 1;
+    x_from[i] = a.x + m * a.xs + 8 * M::x_place(row, at);
+  }
+  int w_row[kWLoads];
+  const uint8_t* w_from[kWLoads];
+  const uint8_t* sz_from = nullptr;
+#pragma unroll
+  for (int i = 0; i < kWLoads; ++i) {
+    const int e = (wave * kWLoads + i) * 64 + lane;
+    w_row[i] = INT4 ? e / 8 : e / 32;
+    const int c = INT4 ? 32 * (e % 8) : 8 * M::w_place(w_row[i], e % 32);
+    const int col = has_col(a, c_tile, c >> 7, c & 127) ? first_col(a, c_tile, c >> 7) + (c & 127) : 0;
+    w_from[i] = a.w + (INT4 ? col / 2 : 2 * (int64_t)col);
+    if constexpr (INT4) sz_from = a.w + a.n / 2 + col / 128 * 4;
+  }
+  u32x4 codes = {};
+  uint32_t sz = 0;
+  const auto load = [&](int step) {
+    uint8_t* stage = stages + (step & 1) * M::kStage;
+    const int k0 = step * M::kDepth;
+    if (k0 + M::kDepth <= a.k) {
+#pragma unroll
+      for (int i = 0; i < kXLoads; ++i)
+        load_lds(x_from[i] + k0, stage + (wave * kXLoads + i) * 1024);
+    } else {  // past the last k, zeros
+#pragma unroll
+      for (int i = 0; i < kXLoads; ++i) {
+        const int e = (wave * kXLoads + i) * 64 + lane;
+        const int valid = a.k - k0 - 8 * M::x_place(e / 8, e % 8);
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (valid > 0) v = *reinterpret_cast<const u32x4*>(x_from[i] + k0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          v[y] &= 2 * y + 1 < valid ? ~0u : 2 * y < valid ? 0xffffu : 0u;
+        *reinterpret_cast<u32x4*>(stage + 16 * e) = v;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i) {
+      // past the last record: that one again, times zero
+      const int k = k0 + w_row[i] < a.k ? k0 + w_row[i] : a.k - 1;
+      const int64_t at = (int64_t)k * a.w_stride;
+      if constexpr (INT4) {
+        codes = *reinterpret_cast<const u32x4*>(w_from[i] + at);
+        sz = *reinterpret_cast<const uint32_t*>(sz_from + at);
+      } else {
+        load_lds(w_from[i] + at, stage + M::kX + (wave * kWLoads + i) * 1024);
+      }
+    }
+  };
+  const auto lay_out = [&](int step) {
+    if constexpr (INT4) {
+      const int e = wave * 64 + lane, row = e / 8;
+      uint8_t* to = stages + (step & 1) * M::kStage + M::kX + row * (2 * kCols);
+      const uint32_t s = __builtin_amdgcn_perm(sz, sz, 0x05040504u);
+      const uint32_t z = __builtin_amdgcn_perm(sz, sz, 0x07060706u);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        *reinterpret_cast<u32x4*>(to + 16 * M::w_place(row, 4 * (e % 8) + y)) =
+            widen8(codes[y], __builtin_bit_cast(f16x2, s), __builtin_bit_cast(f16x2, z));
+    }
+  };
+
+  const int wm = wave >> 2, wn = wave & 3;
+  f32x16 acc[2][TT];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[f][t] = f32x16{};
+  const auto multiply = [&](int step) {
+    const uint8_t* xs = stages + (step & 1) * M::kStage;
+    const uint8_t* ws = xs + M::kX;
+    u32x4 x[2][TT], w[2][2];
+    const auto read = [&](int c) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int i = lane & 15, g = lane >> 4;
+        const int row = 16 * c + 8 * (g >> 1) + (i >> 2);
+        const int piece = 16 * f + 4 * wn + 2 * (g & 1) + ((i & 3) >> 1);
+        const uint8_t* p = ws + row * (2 * kCols) + 16 * M::w_place(row, piece) + 8 * (i & 1);
+        const u32x2 lo = read_turned(p), hi = read_turned(p + 4 * 2 * kCols);
+        w[c & 1][f] = u32x4{lo.x, lo.y, hi.x, hi.y};
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int row = 32 * (wm * TT + t) + r;
+        x[c & 1][t] = *reinterpret_cast<const u32x4*>(xs + row * (2 * M::kDepth) +
+                                                      16 * M::x_place(row, 2 * c + h));
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int c = 0; c < M::kDepth / 16; ++c) {
+      if (c + 1 < M::kDepth / 16) read(c + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              __builtin_bit_cast(f16x8, w[c & 1][f]), __builtin_bit_cast(f16x8, x[c & 1][t]),
+              acc[f][t], 0, 0, 0);
+    }
+  };
+  if (first < stop) {
+    load(first);
+    lay_out(first);
+  }
+  for (int step = first; step < stop; ++step) {
+    wait_loads();
+    mask::lds_barrier();  // this stage is laid out, the other one has been read
+    if (step + 1 < stop) load(step + 1);
+    multiply(step);
+    if (step + 1 < stop) lay_out(step + 1);
+  }
+
+  // The sums go to their rows through LDS, half of the rows at a time.
+  float* out = reinterpret_cast<float*>(stages);
+#pragma unroll
+  for (int round = 0; round < 2; ++round) {
+    mask::lds_barrier();
+    if (wm == round) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = acc[f][t][4 * g + i];
+            *reinterpret_cast<f32x4*>(out + (32 * t + r) * M::kPitch + 128 * f + 32 * wn + 8 * g +
+                                      4 * h) = v;
           }
-          float* p = to + 8 * (8 * (i / 4) + 4 * h + i % 4);
-          *reinterpret_cast<f32x4*>(p) = v0;
-          *reinterpret_cast<f32x4*>(p + 4) = v1;
-        }
-      }
-      __syncthreads();
-      const bool gated = a.form == SPAX_GEMM_GATED && a.splits == 1;
-      for (int e = threadIdx.x; e < F::kRound * (gated ? 32 : 64); e += F::kThreads) {
-        const int row = gated ? e / 32 : e / 64, c = 4 * (gated ? e % 32 : e % 64);
-        const int m = m0 + 32 * t + from + row;
-        if (m >= a.rows || !has_col(a, c_tile, c >> 7, c & 127)) continue;
-        f32x4 sum0 = {0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;
-        for (int w = 0; w < F::kWaves; ++w) {
-          const float* p = lds + (w * F::kRound + row) * F::kPitch + c;
-          sum0 += *reinterpret_cast<const f32x4*>(p);
-          if (gated) sum1 += *reinterpret_cast<const f32x4*>(p + 128);
-        }
-        const int col = first_col(a, c_tile, c >> 7) + (c & 127);
-        if (a.splits == 1)
-          finish(a, m, col, sum0, sum1);
-        else
-          *reinterpret_cast<f32x4*>(a.parts + ((int64_t)split * a.rows + m) * a.n + col) = sum0;
-      }
+    }
+    mask::lds_barrier();
+    const bool gated = a.form == SPAX_GEMM_GATED && a.splits == 1;
+    for (int e = threadIdx.x; e < 32 * TT * (gated ? 32 : 64); e += M::kThreads) {
+      const int row = gated ? e / 32 : e / 64, c = 4 * (gated ? e % 32 : e % 64);
+      const int m = m0 + 32 * TT * round + row;
+      if (m >= a.rows || !has_col(a, c_tile, c >> 7, c & 127)) continue;
+      const float* p = out + row * M::kPitch + c;
+      const f32x4 t0 = *reinterpret_cast<const f32x4*>(p);
+      const f32x4 t1 = gated ? *reinterpret_cast<const f32x4*>(p + 128) : t0;
+      const int col = first_col(a, c_tile, c >> 7) + (c & 127);
+      if (a.splits == 1)
+        finish(a, m, col, t0, t1);
+      else
+        *reinterpret_cast<f32x4*>(a.parts + ((int64_t)split * a.rows + m) * a.n + col) = t0;
     }
   }
 }
@@ -292,33 +504,64 @@ __global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs a) {
   finish(a, m, col, t0, t1);
 }
 
-template <bool INT4, int TM>
+template <bool INT4>
 int launch_few(const GemmArgs& a, unsigned blocks, hipStream_t s) {
-  using F = Few<INT4, TM>;
-  hipLaunchKernelGGL((gemm_few_kernel<INT4, TM>), dim3(blocks), dim3(F::kThreads), F::kLds, s, a);
+  using F = Few<INT4>;
+  hipLaunchKernelGGL(gemm_few_kernel<INT4>, dim3(blocks), dim3(F::kThreads), F::kLds, s, a);
+  SPAX_HIP_CHECK(hipGetLastError());
+  return SPAX_OK;
+}
+
+template <bool INT4, int TT>
+int launch_many(const GemmArgs& a, unsigned blocks, hipStream_t s) {
+  using M = Many<INT4, TT>;
+  hipLaunchKernelGGL((gemm_many_kernel<INT4, TT>), dim3(blocks), dim3(M::kThreads), M::kLds, s, a);
   SPAX_HIP_CHECK(hipGetLastError());
   return SPAX_OK;
 }
 
 }  // namespace
 
+// The tile and the splits of k by what they are expected to take, in us, with one workgroup on each of 256
+// compute units: rounds of workgroups, their steps, and where k is split the sums' way through
+// memory and a second launch.
 GemmPlan gemm_plan(const spax_packed_gemm_args* a) {
   const spax_layout& L = *a->layout;
-  GemmPlan p{};
+  // a tile's rows, k of a step of the workgroup, its time, fewest steps of a split
+  struct Kind {
+    int32_t rows, depth;
+    float step;
+    int32_t least;
+  };
+  static const Kind kinds[] = {{32, 128, 1.15f, 2}, {128, 64, 1.21f, 4}, {256, 64, 2.08f, 4}};
   const bool gated = a->form == SPAX_GEMM_GATED;
-  const int tile = a->n_rows <= 32 ? 32 : 64;
-  p.row_tiles = (a->n_rows + tile - 1) / tile;
-  p.col_tiles = (int32_t)(gated ? (L.d_out[0] + 127) / 128 : (L.d_out_total + kCols - 1) / kCols);
-  const int64_t items = (int64_t)p.row_tiles * p.col_tiles;
-  const int steps = (L.d_in + kStep - 1) / kStep, waves = tile == 32 ? 8 : 4;
-  int64_t splits = items ? 256 / items : 1;
-  const int64_t most = steps / (2 * waves);
-  splits = splits > most ? most : splits;
-  p.splits = (int32_t)(splits < 1 ? 1 : splits);
-  p.blocks = (items * p.splits + 7) / 8 * 8;
-  if (p.splits > 1)
-    p.ws_bytes = aligned_size((size_t)p.splits * a->n_rows * L.d_out_total * sizeof(float));
-  return p;
+  GemmPlan best{};
+  if (a->n_rows < 1) return best;
+  float least = 0.0f;
+  for (const Kind& kind : kinds) {
+    GemmPlan p{};
+    p.tile = kind.rows;
+    p.row_tiles = (a->n_rows + p.tile - 1) / p.tile;
+    p.col_tiles = (int32_t)(gated ? (L.d_out[0] + 127) / 128 : (L.d_out_total + kCols - 1) / kCols);
+    const int64_t items = (int64_t)p.row_tiles * p.col_tiles;
+    const int32_t steps = (L.d_in + kind.depth - 1) / kind.depth;
+    const float join = 8.0f * a->n_rows * (float)L.d_out_total / 4e6f;  // a split's sums there and back
+    for (int32_t splits = 1; splits <= 32 && (splits == 1 || items * (splits - 1) < 256); ++splits) {
+      const int32_t each = (steps + splits - 1) / splits;
+      if (splits > 1 && each < kind.least) break;
+      const float rounds = (float)((items * splits + 255) / 256);
+      const float us = rounds * (3.0f + each * kind.step) + (splits > 1 ? 4.0f + splits * join : 0.0f);
+      if (best.tile && us >= least) continue;
+      least = us;
+      p.splits = (steps + each - 1) / each;
+      p.steps = each * (kind.depth / (p.tile == 32 ? kStep : kind.depth));
+      p.blocks = (items * p.splits + 7) / 8 * 8;
+      best = p;
+    }
+  }
+  if (best.splits > 1)
+    best.ws_bytes = aligned_size((size_t)best.splits * a->n_rows * L.d_out_total * sizeof(float));
+  return best;
 }
 
 int launch_packed_gemm(const spax_packed_gemm_args* p, void* ws, hipStream_t s) {
@@ -334,12 +577,15 @@ int launch_packed_gemm(const spax_packed_gemm_args* p, void* ws, hipStream_t s) 
   a.form = p->form; a.gelu = p->act == SPAX_ACT_GELU_TANH;
   a.residual_type = p->residual_type; a.y_type = p->y_type; a.scale = p->scale;
   a.row_tiles = plan.row_tiles; a.col_tiles = plan.col_tiles; a.splits = plan.splits;
-  const int steps = (a.k + kStep - 1) / kStep;
-  a.steps = (steps + a.splits - 1) / a.splits;
-  const bool int4 = L.base_fmt == SPAX_FMT_INT4, one = p->n_rows <= 32;
+  a.steps = plan.steps;
+  const bool int4 = L.base_fmt == SPAX_FMT_INT4;
   const unsigned blocks = (unsigned)plan.blocks;
-  const int st = int4 ? (one ? launch_few<true, 1>(a, blocks, s) : launch_few<true, 2>(a, blocks, s))
-                      : (one ? launch_few<false, 1>(a, blocks, s) : launch_few<false, 2>(a, blocks, s));
+  int st = SPAX_OK;
+  switch (plan.tile) {
+    case 32: st = int4 ? launch_few<true>(a, blocks, s) : launch_few<false>(a, blocks, s); break;
+    case 128: st = int4 ? launch_many<true, 2>(a, blocks, s) : launch_many<false, 2>(a, blocks, s); break;
+    default: st = int4 ? launch_many<true, 4>(a, blocks, s) : launch_many<false, 4>(a, blocks, s); break;
+  }
   if (st || a.splits == 1) return st;
   const int64_t items = (int64_t)a.rows * (a.width / 4);
   hipLaunchKernelGGL(gemm_join_kernel, dim3((unsigned)((items + kJoinThreads - 1) / kJoinThreads)),

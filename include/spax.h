@@ -614,7 +614,7 @@ int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes
  *   lse = ln sum_j exp(score_j).
  * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)], starts to
  * [0, n_tokens]; a sequence whose starts do not ascend has no tokens, and rows claimed by two
- * sequences get either's result.  Keys on entries that name no page are left out; bytes of rows
+ * sequences hold unspecified values.  Keys on entries that name no page are left out; bytes of rows
  * that a token does not see never reach its result, whatever they hold.  A token with no keys (or at a
  * negative position), or whose scores are all -inf, gives zeros and lse -inf.  Rows of no
  * sequence (before starts[0], behind starts[n_seqs]) are left as they were.
