@@ -28,8 +28,8 @@ namespace {
 using namespace elem;
 using namespace attn;
 
-constexpr int kThreads = 256, kWaves = 4;
-constexpr int kRows = 32 * kWaves;  // query rows of a tile
+// Query rows of a tile of so many waves.
+constexpr int rows_of(int waves) { return 32 * waves; }
 
 struct ChunkArgs {
   const void *q, *k, *v;
@@ -40,7 +40,7 @@ struct ChunkArgs {
   int64_t qt, qh, ot, oh;
   int64_t k_page, k_head, k_row, v_page, v_head, v_row, table_stride;
   int32_t n_tokens, n_heads, n_kv, group, n_seqs, n_pages, page_shift;
-  int32_t max_len, window, tiles, pieces, least_steps;
+  int32_t max_len, window, rows, tiles, pieces, least_steps;  // rows: of a tile
   float scale;
 };
 
@@ -74,7 +74,7 @@ __device__ inline Seq seq_at(const ChunkArgs& a, int s) {
     q.first = clamp_to(a.starts[s], a.n_tokens);
     const int n = clamp_to(a.starts[s + 1], a.n_tokens) - q.first;
     q.n_new = n < 0 ? 0 : n;
-    q.tiles = (q.n_new * a.group + kRows - 1) / kRows;
+    q.tiles = (q.n_new * a.group + a.rows - 1) / a.rows;
   }
   return q;
 }
@@ -96,9 +96,9 @@ __device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
       t.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[t.seq], a.max_len));
       const int begins =
           __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(q.tiles, who);
-      t.from = (index - begins) * kRows;
+      t.from = (index - begins) * a.rows;
       const int rows = t.n_new * a.group;
-      t.to = t.from + kRows < rows ? t.from + kRows : rows;
+      t.to = t.from + a.rows < rows ? t.from + a.rows : rows;
       return t;
     }
     before = last;
@@ -157,7 +157,7 @@ struct Shape {
   static constexpr int EB = NARROW ? 1 : 2;
   static constexpr int kPieces = D / 8;                // of a row in LDS
   static constexpr int kRow = 2 * D;
-  static constexpr int kBuffer = 2 * kKeys * kRow;     // keys, then values
+  static constexpr int kBuffer = kKeys * kRow;         // of keys, or of values
   static constexpr int kBlocks = kKeys / 32, kSteps = kKeys / 16;
   // Where piece c of a row is.
   static __device__ inline int k_place(int row, int c) {
@@ -196,12 +196,11 @@ __device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "m
 
 // Brings a step's keys and values into LDS.  16-bit rows go there straight from memory, 8-bit ones
 // through registers, where they are widened once for all four waves.
-template <class T, bool NARROW, int D>
+template <class T, bool NARROW, int D, int W>
 struct Loader {
   using S = Shape<T, NARROW, D>;
-  const uint8_t *k, *v;  // of the key head
+  static constexpr int kThreads = 64 * W;
   const int32_t* table;  // of the sequence
-  int64_t k_page, k_row, v_page, v_row;
   int page_shift, n_pages, lo, hi;  // the tile's keys
 
   // The table entry of key `key0 + lane` (past the end: of the last key).
@@ -219,43 +218,74 @@ struct Loader {
   static constexpr int kCached = D * S::EB / 16;
   static constexpr int kItems = S::kKeys * kCached;
   static constexpr int kLoads = (kItems + kThreads - 1) / kThreads;
-  u32x4 kx[NARROW ? kLoads : 1], vx[NARROW ? kLoads : 1];
+  // Where 64 pieces of an access are whole rows, these lie in kGroups groups of four keys (or in part of
+  // one), each on one page, whose addresses are found once for the wave; a lane adds its row's place in
+  // the group.  Otherwise (dims 96 and 192) each lane works out its own.
+  static constexpr bool kWhole = 64 % kCached == 0;
+  static constexpr int kRowsAtOnce = kWhole ? 64 / kCached : 1;
+  static constexpr int kGroups = kRowsAtOnce > 4 ? kRowsAtOnce / 4 : 1;
+  struct Side {  // keys or values
+    const uint8_t* base;  // of the key head
+    int64_t page, row, lane;
+    u32x4 x[NARROW ? kLoads : 1];
+  };
+  Side k, v;
+  __device__ inline void start(int lane) {
+    const int at = kWhole ? lane / kCached % 4 : 0;
+    k.lane = S::EB * at * k.row;
+    v.lane = S::EB * at * v.row;
+  }
+  // (an unseen key: any row, masked later)
+  __device__ inline const uint8_t* row_at(const Side& y, int page, int key) const {
+    const int64_t p = page < 0 ? 0 : page, in = key & ((1 << page_shift) - 1);
+    return y.base + S::EB * (p * y.page + in * y.row);
+  }
+  template <bool VALUES>
   __device__ inline void load(uint8_t* buffer, int page, int key0, int wave, int lane) {
-    const int mask = (1 << page_shift) - 1;
+    Side& y = VALUES ? v : k;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int e = NARROW ? i * kThreads + 64 * wave + lane : (wave * kLoads + i) * 64 + lane;
-      const int row = e / kCached, at = e % kCached;
-      const int pg = __shfl(page, row);
-      if (kItems % kThreads && e >= kItems) continue;
-      const int64_t p = pg < 0 ? 0 : pg, in = (key0 + row) & mask;  // unseen: any row, masked later
-      const uint8_t* kr = k + S::EB * (p * k_page + in * k_row);
-      const uint8_t* vr = v + S::EB * (p * v_page + in * v_row);
-      if constexpr (NARROW) {
-        kx[i] = *reinterpret_cast<const u32x4*>(kr + 16 * at);
-        vx[i] = *reinterpret_cast<const u32x4*>(vr + 16 * at);
+      const int access = NARROW ? i * W + wave : wave * kLoads + i;
+      const int e = access * 64 + lane, row = e / kCached, at = e % kCached;
+      const uint8_t* from;
+      if constexpr (kWhole) {
+        if (kItems % kThreads && access * 64 >= kItems) continue;
+        const int first = access * kRowsAtOnce;
+        from = row_at(y, __builtin_amdgcn_readlane(page, first), key0 + first);
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) {
+          const int next = first + 4 * g;
+          const uint8_t* there = row_at(y, __builtin_amdgcn_readlane(page, next), key0 + next);
+          from = lane >= 64 / kGroups * g ? there : from;
+        }
+        from += y.lane;
       } else {
-        const int first = (wave * kLoads + i) * 1024;
-        load_lds(kr + 16 * S::k_piece(row, at), buffer + first);
-        load_lds(vr + 16 * S::v_piece(row, at), buffer + S::kKeys * S::kRow + first);
+        const int pg = __shfl(page, row);
+        if (kItems % kThreads && e >= kItems) continue;
+        from = row_at(y, pg, key0 + row);
       }
+      if constexpr (NARROW)
+        y.x[i] = *reinterpret_cast<const u32x4*>(from + 16 * at);
+      else
+        load_lds(from + 16 * (VALUES ? S::v_piece(row, at) : S::k_piece(row, at)),
+                 buffer + 1024 * access);
     }
   }
+  template <bool VALUES>
   __device__ inline void lay_out(uint8_t* buffer, int wave, int lane) const {
     if constexpr (NARROW) {
+      const Side& y = VALUES ? v : k;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int e = i * kThreads + 64 * wave + lane;
+        const int e = (i * W + wave) * 64 + lane;
         const int row = e / kCached, at = e % kCached;
         if (kItems % kThreads && e >= kItems) continue;
-        uint8_t* kr = buffer + row * S::kRow;
-        uint8_t* vr = kr + S::kKeys * S::kRow;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          *reinterpret_cast<u32x4*>(kr + 16 * S::k_place(row, 2 * at + y)) =
-              widen4(kx[i][2 * y], kx[i][2 * y + 1]);
-          *reinterpret_cast<u32x4*>(vr + 16 * S::v_place(row, 2 * at + y)) =
-              widen4(vx[i][2 * y], vx[i][2 * y + 1]);
+        for (int z = 0; z < 2; ++z) {
+          const int c = 2 * at + z;
+          *reinterpret_cast<u32x4*>(buffer + row * S::kRow +
+                                    16 * (VALUES ? S::v_place(row, c) : S::k_place(row, c))) =
+              widen4(y.x[i][2 * z], y.x[i][2 * z + 1]);
         }
       }
     }
@@ -279,96 +309,115 @@ __device__ inline uint32_t odd_ones(uint32_t w) {
   return ((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u;
 }
 
+// The exponentials are taken of s - m + kLift (base 2), and the running maximum m is raised only once a
+// score is kSlack above it, so the largest is 2^(kLift + kSlack): all that fp16 holds.  In fp16 the lift
+// keeps a long tail under one large key; both cancel in o / l.
+template <class T>
+struct Soft;
+template <>
+struct Soft<f16> {
+  static constexpr float kLift = 14.0f, kSlack = 1.9f, kUnlift = 0x1p-14f;
+};
+template <>
+struct Soft<bf16> {
+  static constexpr float kLift = 0.0f, kSlack = 8.0f, kUnlift = 1.0f;
+};
+
+template <class T>
+__device__ inline float log_sum(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l * Soft<T>::kUnlift)) * kLn2;
+}
+
+// A wave's 32 query rows; a lane has row lane % 32.
 template <class T, bool NARROW, int D>
-struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
+struct Rows {
   using S = Shape<T, NARROW, D>;
   static constexpr int KC = D / 16, OB = D / 32;
+  using Scores = f32x16[S::kBlocks];
+  using Keys = u32x4[KC][S::kBlocks];
+  using Values = u32x4[S::kSteps][OB];
   u32x4 q[KC];
   f32x16 o[OB];
   float m, l;
   // of values that are not finite: whether dim 32 b + i (in o's order, bit 16 b + i) met one that is
   // not -inf, and one that is not inf
   uint64_t up[(OB + 3) / 4], down[(OB + 3) / 4];
-  int lo, hi;          // this lane's row: the keys it sees
-  int lo_max, hi_min;  // of the wave's rows: keys in [lo_max, hi_min) are seen by all
+  int lo, hi;  // the keys that the row sees
 
-  // Raw scores; the scale is part of soften's multiply-add.  Reads are kept kAhead steps ahead of the
-  // products, by hand: left to itself the compiler waits for each.
-  static constexpr int kAhead = 3;
-  __device__ inline void score(const uint8_t* keys, int lane, f32x16 (&s)[S::kBlocks]) const {
-    const int h = lane >> 5, r = lane & 31;
-    u32x4 k[kAhead + 1][S::kBlocks];
-    const auto read = [&](int c) {
+  static __device__ inline u32x4 read_keys(const uint8_t* keys, int block, int c, int lane) {
+    const int row = 32 * block + (lane & 31);
+    return *reinterpret_cast<const u32x4*>(keys + row * S::kRow +
+                                           16 * S::k_place(row, 2 * c + (lane >> 5)));
+  }
+  // Raw scores; the scale is part of soften's multiply-add.
+  __device__ inline void score(const Keys& k, Scores& s) const {
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
 #pragma unroll
       for (int b = 0; b < S::kBlocks; ++b)
-        k[c % (kAhead + 1)][b] = *reinterpret_cast<const u32x4*>(
-            keys + (32 * b + r) * S::kRow + 16 * S::k_place(32 * b + r, 2 * c + h));
-    };
-#pragma unroll
-    for (int c = 0; c < kAhead; ++c) read(c);
-#pragma unroll
-    for (int b = 0; b < S::kBlocks; ++b) s[b] = f32x16{};
-#pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      if (c + kAhead < KC) read(c + kAhead);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int b = 0; b < S::kBlocks; ++b) s[b] = Mma<T>::mul32(k[c % (kAhead + 1)][b], q[c], s[b]);
-    }
+        s[b] = Mma<T>::mul32(k[c][b], q[c], c == 0 ? f32x16{} : s[b]);
   }
   // Bit 16 b + i: the lane's row sees key 32 b + 8 (i / 4) + 4 h + i % 4.
   __device__ inline uint32_t seen(int key0, int page, int lane) const {
     const int h = lane >> 5;
     uint32_t bits = 0;
 #pragma unroll
-    for (int g = 0; g < 4 * S::kBlocks; ++g) {
-      const int at = 32 * (g / 4) + 8 * (g % 4) + 4 * h;
+    for (int y = 0; y < 4 * S::kBlocks; ++y) {
+      const int at = 32 * (y / 4) + 8 * (y % 4) + 4 * h;
       const bool paged = __shfl(page, at) >= 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = key0 + at + i;
-        bits |= (paged && key >= lo && key < hi ? 1u : 0u) << (4 * g + i);
+        bits |= (paged && key >= lo && key < hi ? 1u : 0u) << (4 * y + i);
       }
     }
     return bits;
   }
-  // Scores to p, times 2^kLift; to_log2 > 0.
-  __device__ inline void soften(f32x16 (&s)[S::kBlocks], float to_log2) {
+  __device__ inline void mask_out(Scores& s, int key0, int page, int lane) const {
+    const uint32_t bits = seen(key0, page, lane);
+#pragma unroll
+    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = (bits >> (16 * b + i)) & 1u ? s[b][i] : -INFINITY;
+  }
+  // The running maximum; to_log2 > 0.
+  __device__ inline void raise(const Scores& s, float to_log2) {
     float top = s[0][0];
 #pragma unroll
     for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-    top = fmaxf(top, __shfl_xor(top, 32)) * to_log2;
-    if (__any(top > m)) {
-      const float higher = fmaxf(m, top);
-      const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
-      m = higher;
-      l *= f;
+    // the row's other lane
+    const auto both =
+        __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * to_log2;
+    if (!__any(top > m + Soft<T>::kSlack)) return;
+    const float higher = fmaxf(m, top);
+    const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
+    m = higher;
+    l *= f;
 #pragma unroll
-      for (int t = 0; t < OB; ++t) o[t] *= f;
-    }
-    const float base = (m == -INFINITY ? 0.0f : m) - Mma<T>::kLift;
+    for (int b = 0; b < OB; ++b) o[b] *= f;
+  }
+  // Scores to p, in the second product's operand order, and their sums.
+  __device__ inline void soften(const Scores& s, float to_log2, u32x4 (&p)[S::kSteps]) {
+    const float base = (m == -INFINITY ? 0.0f : m) - Soft<T>::kLift;
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int b = 0; b < S::kBlocks; ++b)
+    for (int t = 0; t < S::kSteps; ++t)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], to_log2, -base));
-        sum[i & 1] += s[b][i];
+      for (int i = 0; i < 4; ++i) {
+        typename Mma<T>::v2 x;
+        const int at = 8 * (t % 2) + 2 * i;
+        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t / 2][at], to_log2, -base));
+        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t / 2][at + 1], to_log2, -base));
+        sum[0] += p0;
+        sum[1] += p1;
+        x.x = (T)p0;
+        x.y = (T)p1;
+        p[t][i] = __builtin_bit_cast(uint32_t, x);
       }
     l += sum[0] + sum[1];
-  }
-  static __device__ inline u32x4 operand(const f32x16 (&s)[S::kBlocks], int step) {
-    u32x4 p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      typename Mma<T>::v2 x;
-      x.x = (T)s[step / 2][8 * (step % 2) + 2 * i];
-      x.y = (T)s[step / 2][8 * (step % 2) + 2 * i + 1];
-      p[i] = __builtin_bit_cast(uint32_t, x);
-    }
-    return p;
   }
   static __device__ inline u32x4 read_values(const uint8_t* values, int block, int step, int lane) {
     const int i = lane & 15, g = lane >> 4;
@@ -379,21 +428,11 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
     const u32x2 x = read_turned(p), y = read_turned(p + 8 * S::kRow);
     return u32x4{x.x, x.y, y.x, y.y};
   }
-  __device__ inline void take_values(const f32x16 (&s)[S::kBlocks], const uint8_t* values,
-                                     int lane) {
-    u32x4 v[2][OB];
+  __device__ inline void take_values(const Values& v, const u32x4 (&p)[S::kSteps]) {
 #pragma unroll
-    for (int b = 0; b < OB; ++b) v[0][b] = read_values(values, b, 0, lane);
+    for (int t = 0; t < S::kSteps; ++t)
 #pragma unroll
-    for (int t = 0; t < S::kSteps; ++t) {
-      const u32x4 p = operand(s, t);
-      if (t + 1 < S::kSteps)
-#pragma unroll
-        for (int b = 0; b < OB; ++b) v[(t + 1) % 2][b] = read_values(values, b, t + 1, lane);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int b = 0; b < OB; ++b) o[b] = Mma<T>::mul32(v[t % 2][b], p, o[b]);
-    }
+      for (int b = 0; b < OB; ++b) o[b] = Mma<T>::mul32(v[t][b], p[t], o[b]);
   }
   // Notes which dims of the row meet a value that is not finite, which decides them whatever else
   // they meet.
@@ -435,29 +474,14 @@ struct Rows {  // a wave's 32 query rows; a lane has row lane % 32
     const bool u = up[b / 4] & bit, d = down[b / 4] & bit;
     return u || d ? o[b][i] + (u ? d ? NAN : INFINITY : -INFINITY) : o[b][i];
   }
-  __device__ inline void step(const uint8_t* buffer, int key0, int page, bool paged, float to_log2,
-                              int lane) {
-    f32x16 s[S::kBlocks];
-    score(buffer, lane, s);
-    const bool edge = !paged || key0 < lo_max || key0 + S::kKeys > hi_min;
-    if (edge) {
-      const uint32_t bits = seen(key0, page, lane);
-#pragma unroll
-      for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[b][i] = (bits >> (16 * b + i)) & 1u ? s[b][i] : -INFINITY;
-    }
-    soften(s, to_log2);
-    take_values(s, buffer + S::kKeys * S::kRow, lane);
-  }
 };
 
-template <class T, bool NARROW, int D>
-__global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkArgs a) {
+template <class T, bool NARROW, int D, int W>
+__global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkArgs a) {
   using S = Shape<T, NARROW, D>;
   using R = Rows<T, NARROW, D>;
-  extern __shared__ __attribute__((aligned(256))) uint8_t lds[];
+  constexpr int kThreads = 64 * W;
+  extern __shared__ __attribute__((aligned(256))) uint8_t lds[];  // two steps' keys and values
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, r = lane & 31;
@@ -468,7 +492,7 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
   const Tile tile = find_tile(a, a.tiles - 1 - rest / a.pieces, lane);
   if (tile.from == tile.to) return;
 
-  Loader<T, NARROW, D> in;
+  Loader<T, NARROW, D, W> in;
   const Piece steps = piece_of(a, tile, piece, piece_steps(a, S::kKeys, lane), S::kKeys);
   if (piece > 0 && piece >= steps.pieces) return;
   in.lo = steps.lo;
@@ -478,44 +502,37 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
     if (a.k_scale) to_log2 *= a.k_scale[kvh];
     if (a.v_scale) v_mul = a.v_scale[kvh];
   }
-  in.k = (const uint8_t*)a.k + (int64_t)S::EB * kvh * a.k_head;
-  in.v = (const uint8_t*)a.v + (int64_t)S::EB * kvh * a.v_head;
+  in.k.base = (const uint8_t*)a.k + (int64_t)S::EB * kvh * a.k_head;
+  in.v.base = (const uint8_t*)a.v + (int64_t)S::EB * kvh * a.v_head;
   in.table = a.table + tile.seq * a.table_stride;
-  in.k_page = a.k_page; in.k_row = a.k_row; in.v_page = a.v_page; in.v_row = a.v_row;
+  in.k.page = a.k_page; in.k.row = a.k_row; in.v.page = a.v_page; in.v.row = a.v_row;
   in.page_shift = a.page_shift; in.n_pages = a.n_pages;
+  in.start(lane);
 
-  const int first = tile.from + 32 * wave;  // the wave's rows
-  const int last = (first + 32 < tile.to ? first + 32 : tile.to) - 1;
-  const int row = first + r <= last ? first + r : last;
-  const bool works = last >= first, mine = works && first + r <= last;
-  const int token = works ? row / a.group : 0, head = kvh * a.group + (works ? row % a.group : 0);
   // The scale is kept above zero, as the largest score is found before it is applied: a sign goes to
   // the queries, and a scale of zero makes them zeros.
   const uint32_t flip = to_log2 < 0.0f ? 0x80008000u : 0u, keep = to_log2 == 0.0f ? 0u : ~0u;
   to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
+  const int first = tile.from + 32 * wave;  // the wave's rows; past the last row, that one again
+  const bool works = first < tile.to;
+  const int last = first + 32 < tile.to ? first + 31 : tile.to - 1;
+  const int lo_min = works ? lo_of(a, tile.position(first / a.group)) : 0;
+  const int hi_max = works ? hi_of(tile.position(last / a.group)) : 0;
+  const int row = first + r < tile.to ? first + r : tile.to - 1;
+  const int token = row / a.group, head = kvh * a.group + row % a.group;
   R w;
-  if (works) {
-    const uint8_t* q = (const uint8_t*)a.q + 2 * ((tile.first + token) * a.qt + head * a.qh);
+  const uint8_t* q = (const uint8_t*)a.q + 2 * ((tile.first + token) * a.qt + head * a.qh);
 #pragma unroll
-    for (int c = 0; c < R::KC; ++c)
-      w.q[c] = (*reinterpret_cast<const u32x4*>(q + 32 * c + 16 * h) ^ flip) & keep;
-  }
+  for (int c = 0; c < R::KC; ++c)
+    w.q[c] = (*reinterpret_cast<const u32x4*>(q + 32 * c + 16 * h) ^ flip) & keep;
 #pragma unroll
-  for (int t = 0; t < R::OB; ++t) w.o[t] = f32x16{};
+  for (int b = 0; b < R::OB; ++b) w.o[b] = f32x16{};
 #pragma unroll
-  for (int t = 0; t < (R::OB + 3) / 4; ++t) w.up[t] = w.down[t] = 0u;
+  for (int b = 0; b < (R::OB + 3) / 4; ++b) w.up[b] = w.down[b] = 0u;
   w.m = -INFINITY;
   w.l = 0.0f;
   w.lo = lo_of(a, tile.position(token));
   w.hi = hi_of(tile.position(token));
-  int lo_min = 0, hi_max = 0;
-  if (works) {
-    lo_min = lo_of(a, tile.position(first / a.group));
-    w.lo_max = lo_of(a, tile.position(last / a.group));
-    w.hi_min = hi_of(tile.position(first / a.group));
-    hi_max = hi_of(tile.position(last / a.group));
-  }
-
   // 0 * inf is NaN, so where some row does not see some key, values that are not finite are taken out
   // of the step and noted for the rows that do see them.
   __shared__ int odd_step[2];
@@ -524,29 +541,33 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
   if (threadIdx.x < 2) odd_step[threadIdx.x] = 0;
 
   if (steps.count > 0) {
+    const auto keys = [&](int i) { return lds + 2 * (i & 1) * S::kBuffer; };
+    const auto values = [&](int i) { return lds + (2 * (i & 1) + 1) * S::kBuffer; };
     int key0 = steps.first * S::kKeys;
     int page = in.page_of(in.look_up(key0, lane), key0, lane);
-    in.load(lds, page, key0, wave, lane);
+    in.template load<false>(keys(0), page, key0, wave, lane);
+    in.template load<true>(values(0), page, key0, wave, lane);
     int entry = in.look_up(key0 + S::kKeys, lane);
-    in.lay_out(lds, wave, lane);
+    in.template lay_out<false>(keys(0), wave, lane);
+    in.template lay_out<true>(values(0), wave, lane);
     for (int i = 0; i < steps.count; ++i) {
-      uint8_t* buffer = lds + (i & 1) * S::kBuffer;
-      uint8_t* other = lds + (~i & 1) * S::kBuffer;
       if constexpr (!NARROW) wait_loads();
-      mask::lds_barrier();  // this buffer is laid out, the other one has been read
+      mask::lds_barrier();  // this step is laid out, the last one has been read
       const int next = key0 + S::kKeys;
       int next_page = -1;
       if (i + 1 < steps.count) {
         next_page = in.page_of(entry, next, lane);
-        in.load(other, next_page, next, wave, lane);
+        in.template load<false>(keys(i + 1), next_page, next, wave, lane);
+        in.template load<true>(values(i + 1), next_page, next, wave, lane);
         entry = in.look_up(next + S::kKeys, lane);
       }
-      if (!__all(page >= 0) || key0 < all_lo || key0 + S::kKeys > all_hi) {
-        uint8_t* values = buffer + S::kKeys * S::kRow;
-        constexpr int kMine = S::kKeys * S::kRow / 16;
+      const bool edge = !__all(page >= 0) || key0 < all_lo || key0 + S::kKeys > all_hi;
+      if (edge) {
+        uint8_t* v = values(i);
+        constexpr int kMine = S::kBuffer / 16;
         uint32_t odd = 0u;
         for (int e = threadIdx.x; e < kMine; e += kThreads) {
-          u32x4* at = reinterpret_cast<u32x4*>(values + 16 * e);
+          u32x4* at = reinterpret_cast<u32x4*>(v + 16 * e);
           const u32x4 x = *at;
           const int row = e / S::kPieces, key = key0 + row;
           const bool seen = key >= in.lo && key < in.hi && __shfl(page, row) >= 0;
@@ -557,10 +578,10 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
         if (__any(odd) && lane == 0) odd_step[i & 1] = 1;
         mask::lds_barrier();
         if (__builtin_amdgcn_readfirstlane(odd_step[i & 1])) {
-          if (works) w.note_odd(values, key0, page, lane);
+          if (works) w.note_odd(v, key0, page, lane);
           mask::lds_barrier();
           for (int e = threadIdx.x; e < kMine; e += kThreads) {
-            u32x4* at = reinterpret_cast<u32x4*>(values + 16 * e);
+            u32x4* at = reinterpret_cast<u32x4*>(v + 16 * e);
             u32x4 x = *at;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -573,9 +594,33 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
           if (threadIdx.x == 0) odd_step[i & 1] = 0;
         }
       }
-      if (works && key0 + S::kKeys > lo_min && key0 < hi_max)
-        w.step(buffer, key0, page, __all(page >= 0), to_log2, lane);
-      if (i + 1 < steps.count) in.lay_out(other, wave, lane);
+      if (works && key0 + S::kKeys > lo_min && key0 < hi_max) {
+        typename R::Scores s;
+        {
+          typename R::Keys k;
+#pragma unroll
+          for (int c = 0; c < R::KC; ++c)
+#pragma unroll
+            for (int b = 0; b < S::kBlocks; ++b) k[c][b] = R::read_keys(keys(i), b, c, lane);
+          w.score(k, s);
+        }
+        if (edge) w.mask_out(s, key0, page, lane);
+        w.raise(s, to_log2);
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 p[S::kSteps];
+        w.soften(s, to_log2, p);
+        __builtin_amdgcn_sched_barrier(0);
+        typename R::Values v;
+#pragma unroll
+        for (int t = 0; t < S::kSteps; ++t)
+#pragma unroll
+          for (int b = 0; b < R::OB; ++b) v[t][b] = R::read_values(values(i), b, t, lane);
+        w.take_values(v, p);
+      }
+      if (i + 1 < steps.count) {
+        in.template lay_out<false>(keys(i + 1), wave, lane);
+        in.template lay_out<true>(values(i + 1), wave, lane);
+      }
       key0 = next;
       page = next_page;
     }
@@ -583,7 +628,7 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
 
   if (!works) return;
   w.l += __shfl_xor(w.l, 32);
-  if (!mine) return;
+  if (first + r >= tile.to) return;
   const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
   if (steps.pieces <= 1) {
     const float f = w.l == 0.0f ? 0.0f : v_mul / w.l;
@@ -591,24 +636,24 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
 #pragma unroll
     for (int b = 0; b < R::OB; ++b)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int y = 0; y < 4; ++y) {
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = f == 0.0f ? 0.0f : w.value(b, 4 * g + i) * f;
-        store_n<4>(out + 32 * b + 8 * g + 4 * h, x);
+        for (int i = 0; i < 4; ++i) x[i] = f == 0.0f ? 0.0f : w.value(b, 4 * y + i) * f;
+        store_n<4>(out + 32 * b + 8 * y + 4 * h, x);
       }
-    if (a.lse && h == 0) a.lse[at] = lse_of<T>(w.m, w.l);
+    if (a.lse && h == 0) a.lse[at] = log_sum<T>(w.m, w.l);
     return;
   }
   const int64_t part = (int64_t)piece * a.n_tokens * a.n_heads + at;
 #pragma unroll
   for (int b = 0; b < R::OB; ++b)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int y = 0; y < 4; ++y) {
       f32x4 x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * g + i);
-      *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * g + 4 * h) = x;
+      for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * y + i);
+      *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * y + 4 * h) = x;
     }
   if (h == 0) {
     a.part_ml[2 * part] = w.m;
@@ -618,13 +663,14 @@ __global__ __launch_bounds__(kThreads, D > 192 ? 1 : 2) void chunk_kernel(ChunkA
 
 // Joins the pieces of a row, a wave each: lane c has the maximum and the sum of piece c (at most 64),
 // four dims a lane, D / 4 lanes a piece.  Rows whose tile is one piece have their result already.
+constexpr int kJoinWaves = 4;
 template <class T, int D>
-__global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a) {
   constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kLoads = 8;
   constexpr int kKeys = D >= 192 ? 32 : 64;
   const int lane = threadIdx.x & 63;
   const int64_t at =
-      (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      (int64_t)blockIdx.x * kJoinWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int token = (int)(at / a.n_heads), head = (int)(at % a.n_heads);
   if (token >= a.n_tokens) return;
   Tile tile{0, 0, 0, 0, 0, 0};
@@ -638,8 +684,8 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a) {
     tile.n_new = __builtin_amdgcn_readlane(q.n_new, who);
     tile.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[tile.seq], a.max_len));
     const int row = (token - tile.first) * a.group + head % a.group, rows = tile.n_new * a.group;
-    tile.from = row / kRows * kRows;
-    tile.to = tile.from + kRows < rows ? tile.from + kRows : rows;
+    tile.from = row / a.rows * a.rows;
+    tile.to = tile.from + a.rows < rows ? tile.from + a.rows : rows;
     break;
   }
   if (tile.from == tile.to) return;
@@ -696,17 +742,30 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(ChunkArgs a) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
   store_n<4>((T*)a.out + token * a.ot + head * a.oh + d, out);
-  if (a.lse && d == 0) a.lse[at] = lse_of<T>(m, l);
+  if (a.lse && d == 0) a.lse[at] = log_sum<T>(m, l);
+}
+
+template <class T, bool NARROW, int D, int W>
+void start(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
+  constexpr int kLds = 4 * Shape<T, NARROW, D>::kBuffer;
+  hipLaunchKernelGGL((chunk_kernel<T, NARROW, D, W>), dim3(blocks), dim3(64 * W), kLds, s, a);
 }
 
 template <class T, bool NARROW, int D>
 int launch(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
-  constexpr int kLds = 2 * Shape<T, NARROW, D>::kBuffer;
-  hipLaunchKernelGGL((chunk_kernel<T, NARROW, D>), dim3(blocks), dim3(kThreads), kLds, s, a);
+  if constexpr (D < 192) {
+    if (a.rows == rows_of(8))
+      start<T, NARROW, D, 8>(a, blocks, s);
+    else
+      start<T, NARROW, D, 4>(a, blocks, s);
+  } else {
+    start<T, NARROW, D, 4>(a, blocks, s);
+  }
   SPAX_HIP_CHECK(hipGetLastError());
   if (a.pieces > 1) {
-    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)(((int64_t)a.n_tokens * a.n_heads + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, s, a);
+    const int64_t rows = (int64_t)a.n_tokens * a.n_heads;
+    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
+                       dim3(64 * kJoinWaves), 0, s, a);
     SPAX_HIP_CHECK(hipGetLastError());
   }
   return SPAX_OK;
@@ -733,7 +792,18 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   if (a->n_tokens == 0) return p;
   const int64_t group = a->n_heads / c.n_kv_heads;
   // every sequence with tokens has at most one tile that is not full
-  p.tiles = a->n_tokens * group / kRows + (c.n_seqs < a->n_tokens ? c.n_seqs : a->n_tokens);
+  const auto tiles = [&](int rows) {
+    // every sequence with tokens has at most one tile that is not full
+    return a->n_tokens * group / rows + (c.n_seqs < a->n_tokens ? c.n_seqs : a->n_tokens);
+  };
+  // Eight waves that share a step's keys bring half as many in for a row as two workgroups of four, and
+  // have a unit to themselves (1 x 8192 of 16 bits: 657 us, 691 with four; 24 mixed 88 and 106), but
+  // widen 8-bit keys all at the same time (8 x 512 over 15872: 1755 and 1350), and want one
+  // workgroup for each unit (1 x 509 of 32 heads: 31 and 25).
+  const bool wide = c.type != SPAX_E4M3 && c.head_dim < 192 &&
+                    tiles(rows_of(8)) * c.n_kv_heads >= 256;
+  p.rows = rows_of(wide ? 8 : 4);
+  p.tiles = tiles(p.rows);
   int64_t keys = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->n_tokens < keys)
     keys = (int64_t)a->window + a->n_tokens;
@@ -769,7 +839,7 @@ int launch_chunk_attention(const spax_chunk_attention_args* p, void* ws, hipStre
   a.group = p->n_heads / c.n_kv_heads; a.n_seqs = c.n_seqs; a.n_pages = c.n_pages;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   a.max_len = p->max_len; a.window = p->window; a.scale = p->scale;
-  a.tiles = (int32_t)plan.tiles; a.pieces = plan.pieces;
+  a.rows = plan.rows; a.tiles = (int32_t)plan.tiles; a.pieces = plan.pieces;
   a.least_steps = plan.least_steps;
   a.part_o = (float*)ws;
   a.part_ml = (float*)ws + (size_t)plan.pieces * p->n_tokens * p->n_heads * c.head_dim;

@@ -49,6 +49,7 @@ AttentionPlan attention_plan(const spax_attention_args* a);
 // How a chunk attention shares out its work: tiles of query rows (an upper bound; the real number
 // follows from starts), each tile's keys in at most `pieces` pieces of at least least_steps steps.
 struct ChunkPlan {
+  int32_t rows;  // of a tile
   int64_t tiles;
   int32_t pieces, least_steps;
   int64_t blocks;
