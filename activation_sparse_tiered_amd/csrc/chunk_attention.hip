@@ -132,6 +132,12 @@ __device__ inline int piece_steps(const ChunkArgs& a, int keys, int lane) {
   return share > a.least_steps ? (int)share : a.least_steps;
 }
 
+// A tile of up to kWholeSteps steps stays whole: its pieces' way through memory and the second launch take
+// longer than the steps they save (1 x 509 tokens of 32 heads, nine steps: 25 us whole, 36 in
+// two).  Longer ones are cut down to kLeastSteps (1 x 5 over 8192: 24.2 us with six, 21.7 with four,
+// 21.0 with three, of which more join).
+constexpr int kWholeSteps = 12, kLeastSteps = 4;
+
 // The tile's keys [lo, hi), the steps of one piece of them, and how many pieces there are.
 struct Piece {
   int lo, hi, first, count, pieces;
@@ -141,6 +147,7 @@ __device__ inline Piece piece_of(const ChunkArgs& a, const Tile& t, int piece, i
   p.hi = hi_of(t.position((t.to - 1) / a.group));
   p.lo = lo_of(a, t.position(t.from / a.group));
   const int all = steps_in(p.lo, p.hi, keys);
+  if (all <= kWholeSteps) per = kWholeSteps;
   p.pieces = (all + per - 1) / per;
   const int from = piece * per < all ? piece * per : all;
   p.first = p.lo / keys + from;
@@ -753,7 +760,7 @@ void start(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
 
 template <class T, bool NARROW, int D>
 int launch(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
-  if constexpr (D < 192) {
+  if constexpr (!NARROW && D < 192) {
     if (a.rows == rows_of(8))
       start<T, NARROW, D, 8>(a, blocks, s);
     else
@@ -781,8 +788,6 @@ int launch_dim(const ChunkArgs& a, int dim, unsigned blocks, hipStream_t s) {
     default: return launch<T, NARROW, 256>(a, blocks, s);
   }
 }
-
-constexpr int kLeastSteps = 6;
 
 }  // namespace
 
@@ -812,6 +817,7 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   const int64_t items = p.tiles * c.n_kv_heads;
   int64_t pieces = 2048 / items;
   if (pieces > steps / kLeastSteps) pieces = steps / kLeastSteps;
+  if (steps <= kWholeSteps) pieces = 1;
   pieces = pieces < 1 ? 1 : pieces > 64 ? 64 : pieces;
   p.least_steps = (int32_t)((steps + pieces - 1) / pieces);
   p.pieces = (int32_t)((steps + p.least_steps - 1) / p.least_steps);
