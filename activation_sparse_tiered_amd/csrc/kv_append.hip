@@ -120,10 +120,21 @@ __device__ inline void divide_e4m3(float v[N], float scale) {
   }
 }
 
-// The sum of v over the `lanes` threads (a power of two, aligned) that hold a head.  More than a wave's
-// meet in `waves`; every thread of the workgroup calls it as often.
+template <int CTRL>
+__device__ inline float add_moved(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+
+// The sum of v over the `lanes` threads (a power of two, aligned) that hold a head: within 16 lanes by
+// moves between registers.  More than a wave's meet in `waves`; every thread of the workgroup calls
+// it as often.
 __device__ inline float sum_of_head(float v, int lanes, float* waves) {
-  for (int z = 1; z < lanes && z < 64; z <<= 1) v += __shfl_xor(v, z);
+  if (lanes > 1) v = add_moved<0xB1>(v);   // lane ^ 1
+  if (lanes > 2) v = add_moved<0x4E>(v);   // lane ^ 2
+  if (lanes > 4) v = add_moved<0x141>(v);  // the other four of eight
+  if (lanes > 8) v = add_moved<0x140>(v);  // the other eight of sixteen
+  if (lanes > 16) v += __shfl_xor(v, 16);
+  if (lanes > 32) v += __shfl_xor(v, 32);
   if (lanes > 64) {
     const int wave = threadIdx.x >> 6, first = wave & ~(lanes / 64 - 1);
     __syncthreads();  // the last sums have been read
@@ -147,7 +158,7 @@ __device__ inline void load_f32(const float* p, float v[N]) {
 // A head's norm and its weights, held from head to head as long as they are the same.
 template <int N>
 struct HeadNorm {
-  float w[2 * N], b[2 * N];
+  float w[2 * N];
   int have = -1;  // 0: the queries' shared weights, 1: the keys'
   // x and y: this thread's values of a head, zeros where it has none (`on` false, or y with `single`).
   __device__ inline void apply(const AppendArgs& a, float x[N], float y[N], int h, bool on,
@@ -155,16 +166,12 @@ struct HeadNorm {
     const int which = h < a.n_heads ? 0 : 1;
     const float* weight = which ? a.k_w : a.q_w;
     const float* bias = which ? a.k_b : a.q_b;
+    const int64_t stride = which ? a.k_ws : a.q_ws;
+    const int64_t at = (which ? h - a.n_heads : h) * stride;
     const bool normed = on && weight && h < a.n_heads + a.n_kv;
     if (normed && have != which) {
-      const int64_t stride = which ? a.k_ws : a.q_ws;
-      const int64_t at = (which ? h - a.n_heads : h) * stride;
       load_f32<N>(weight + at + e0, w);
       if (!single) load_f32<N>(weight + at + e1, w + N);
-      if (bias) {
-        load_f32<N>(bias + at + e0, b);
-        if (!single) load_f32<N>(bias + at + e1, b + N);
-      }
       have = stride ? -1 : which;
     }
     const float share = 1.0f / (float)a.dim;
@@ -183,16 +190,21 @@ struct HeadNorm {
     }
     s = sum_of_head(on ? s : 0.0f, a.lanes, waves);
     if (!normed) return;
-    const float r = 1.0f / sqrtf(s * share + a.eps);
+    const float r = rsqrtf(s * share + a.eps);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       x[i] = (x[i] - mean) * r * w[i];
       y[i] = single ? 0.0f : (y[i] - mean) * r * w[N + i];
-      if (bias) {
-        x[i] += b[i];
-        y[i] += single ? 0.0f : b[N + i];
-      }
     }
+    if (!bias) return;
+    float b[N];
+    load_f32<N>(bias + at + e0, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += b[i];
+    if (single) return;
+    load_f32<N>(bias + at + e1, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] += b[i];
   }
 };
 template <>
@@ -250,6 +262,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   // threads past the last slot, or past a head's last item: none
   const int mine = slot < a.heads_at_once && (!NORM || j < items) ? h0 + slot : h1;
   load(mine);
+  HeadNorm<NORM ? N : 0> norm;
   const Place to = place_of(a, t, p);
   find_sines();
   float sn[N], cs[N];
@@ -258,7 +271,6 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     sn[i] = turns ? sines[0][N * j + i] : 0.0f;
     cs[i] = turns ? sines[1][N * j + i] : 1.0f;
   }
-  HeadNorm<NORM ? N : 0> norm;
   __shared__ float waves[NORM ? kAppendThreads / 64 : 1];
   int base = h0;
   for (int h = mine; (NORM ? base : h) < h1; h += a.heads_at_once, base += a.heads_at_once) {
