@@ -14,6 +14,10 @@
 // Measured: 4099 tokens of 32 + 8 + 8 heads of 128, fp16 to e4m3, 92 MB: 19.6 us, 4.7 TB/s (a large
 // copy reaches 5.1); one token: 2.8 us on the device, a load of the position and one of the page
 // before the stores can go.
+//
+// A normed head (x w / sqrt(mean x^2 + eps), or of x less its mean) is summed over its threads by moves
+// between registers, in 32 bits, before it turns: the same bytes, 24.0 us for the same prompts,
+// 3.8 TB/s; what it adds is the chain from a head's values through their sum to its stores.
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -322,12 +326,18 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
 template <class SRC, class LOW, class C, bool NORM>
 int launch(const AppendArgs& a, dim3 grid, int pairs, hipStream_t s) {
   const dim3 blk(kAppendThreads);
-  if (pairs == 8)
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 8, NORM>), grid, blk, 0, s, a);
-  else if (pairs == 4)
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 4, NORM>), grid, blk, 0, s, a);
-  else
-    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 1, NORM>), grid, blk, 0, s, a);
+  if constexpr (NORM) {
+    if (pairs == 4)
+      hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 4, true>), grid, blk, 0, s, a);
+    else
+      hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 1, true>), grid, blk, 0, s, a);
+  } else if (pairs == 8) {
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 8, false>), grid, blk, 0, s, a);
+  } else if (pairs == 4) {
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 4, false>), grid, blk, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((kv_append_kernel<SRC, LOW, C, 1, false>), grid, blk, 0, s, a);
+  }
   SPAX_HIP_CHECK(hipGetLastError());
   return SPAX_OK;
 }
@@ -374,8 +384,9 @@ int launch_kv_append(const spax_kv_append_args* p, const spax_head_norm* n, hipS
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   // 16 bytes of a 16-bit head at a time where the rotated part divides into such pieces (the
   // prompts of 4099 tokens: 20.0 us with pieces of eight pairs, 20.6 of four, where 40 values are
-  // rotated, and 59 of one, where 20 are).
-  const int pairs = p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
+  // rotated, and 59 of one, where 20 are).  Normed, pieces of four: their weights take half the registers
+  // (24.0 us, 26.1 of eight).
+  const int pairs = !n && p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
   const int items = pairs > 1 ? a.dim / (2 * pairs) : p->rot_dim / 2 + a.dim - p->rot_dim;
   int lanes = items;
   if (n) {
