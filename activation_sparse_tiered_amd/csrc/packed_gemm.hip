@@ -95,12 +95,20 @@ __device__ inline void finish(const GemmArgs& a, int m, int col, f32x4 t0, f32x4
 }
 
 // Two int4 values of one column (k and k + 1) as fp16, from words whose low and high halves hold them
-// at bit 4 i: 0x6400 | q is 1024 + q, and the multiply-add rounds s q + z once.
-__device__ inline uint32_t widen2(uint32_t u, int i, f16x2 s, f16x2 z) {
-  const uint32_t q = ((u >> (4 * i)) & 0x000f000fu) | 0x64006400u;
-  const f16x2 v = __builtin_bit_cast(f16x2, q) - f16x2{(f16)1024.0f, (f16)1024.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, s, z));
-}
+// at bit 4 i: 0x6400 | q is 1024 + q, and the multiply-add rounds s q + z once.  The constants are
+// hidden in registers, where an and and an or become one instruction.
+struct Widen {
+  uint32_t mask, magic;
+  __device__ inline Widen() : mask(0x000f000fu), magic(0x64006400u) {
+    asm("" : "+v"(mask));
+    asm("" : "+s"(magic));
+  }
+  __device__ inline uint32_t two(uint32_t u, int i, f16x2 s, f16x2 z) const {
+    const uint32_t q = ((u >> (4 * i)) & mask) | magic;
+    const f16x2 v = __builtin_bit_cast(f16x2, q) - f16x2{(f16)1024.0f, (f16)1024.0f};
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, s, z));
+  }
+};
 
 // 32 rows, 256 columns; the workgroup's waves take every kWaves-th step of its k.
 template <bool INT4>
@@ -174,6 +182,7 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
       }
     }
   };
+  const Widen widen;
   f32x16 acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = f32x16{};
@@ -197,7 +206,7 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         if constexpr (INT4)
-          f[p] = widen2(j < 4 ? lo[p] : hi[p], j & 3, s[p], zero[p]);
+          f[p] = widen.two(j < 4 ? lo[p] : hi[p], j & 3, s[p], zero[p]);
         else
           f[p] = __builtin_amdgcn_perm(z.w[2 * p + 1][j / 2], z.w[2 * p][j / 2],
                                        j & 1 ? 0x07060302u : 0x05040100u);
@@ -284,10 +293,10 @@ __device__ inline u32x2 read_turned(const uint8_t* p) {
 }
 
 // Eight int4 values of one k, packed as stored, as fp16 in order.
-__device__ inline u32x4 widen8(uint32_t w, f16x2 s, f16x2 z) {
+__device__ inline u32x4 widen8(const Widen& widen, uint32_t w, f16x2 s, f16x2 z) {
   uint32_t r[4];  // columns i and i + 4
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = widen2(w, i, s, z);
+  for (int i = 0; i < 4; ++i) r[i] = widen.two(w, i, s, z);
   return u32x4{__builtin_amdgcn_perm(r[1], r[0], 0x05040100u),
                __builtin_amdgcn_perm(r[3], r[2], 0x05040100u),
                __builtin_amdgcn_perm(r[1], r[0], 0x07060302u),
@@ -349,6 +358,7 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
     w_from[i] = a.w + (INT4 ? col / 2 : 2 * (int64_t)col);
     if constexpr (INT4) sz_from = a.w + a.n / 2 + col / 128 * 4;
   }
+  const Widen widen;
   u32x4 codes = {};
   uint32_t sz = 0;
   const auto load = [&](int step) {
@@ -393,7 +403,7 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
 #pragma unroll
       for (int y = 0; y < 4; ++y)
         *reinterpret_cast<u32x4*>(to + 16 * M::w_place(row, 4 * (e % 8) + y)) =
-            widen8(codes[y], __builtin_bit_cast(f16x2, s), __builtin_bit_cast(f16x2, z));
+            widen8(widen, codes[y], __builtin_bit_cast(f16x2, s), __builtin_bit_cast(f16x2, z));
     }
   };
 
@@ -495,11 +505,25 @@ __global__ __launch_bounds__(kJoinThreads) void gemm_join_kernel(GemmArgs a) {
   const int64_t e = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   const int m = (int)(e / per_row), col = 4 * (int)(e % per_row);
   if (m >= a.rows) return;
+  const bool gated = a.form == SPAX_GEMM_GATED;
+  const float* p = a.parts + (int64_t)m * a.n + col;
+  const int64_t step = (int64_t)a.rows * a.n;
   f32x4 t0 = {0.0f, 0.0f, 0.0f, 0.0f}, t1 = t0;
-  for (int s = 0; s < a.splits; ++s) {
-    const float* p = a.parts + ((int64_t)s * a.rows + m) * a.n + col;
-    t0 += *reinterpret_cast<const f32x4*>(p);
-    if (a.form == SPAX_GEMM_GATED) t1 += *reinterpret_cast<const f32x4*>(p + a.width);
+  constexpr int kLoads = 8;  // in flight
+  for (int s = 0; s < a.splits; s += kLoads) {
+    f32x4 x[kLoads], y[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      x[i] = y[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (s + i >= a.splits) continue;
+      x[i] = *reinterpret_cast<const f32x4*>(p + (s + i) * step);
+      if (gated) y[i] = *reinterpret_cast<const f32x4*>(p + (s + i) * step + a.width);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      t0 += x[i];
+      t1 += y[i];
+    }
   }
   finish(a, m, col, t0, t1);
 }
