@@ -11,7 +11,7 @@ arithmetic before it:
 * chunk attention: the error of a score is at most (dim + 4) 2^-24 reach (reach = scale sum
   |q_i k_i|), and it moves a weight and the total by that much each; sums of weights and of
   weighted values run over at most 2048 fp32 additions here; a weight enters rounded to its type:
-  half a step of itself (2^-11, 2^-8), and in fp16 2^-40 of the row's largest.  Together mass (2
+  half a step of itself (2^-11, 2^-8), and in fp16 2^-39 of the row's largest.  Together mass (2
   (dim + 4) 2^-24 reach + 2048 2^-24 + 2^-16 + half a step), mass = sum softmax |v|.
 * product: a column's sum of d_in products passes through at most 16 roundings within a matrix
   instruction, one per 16 k and one per wave and split: mass (16 + d_in / 16 + 32) 2^-23, mass = sum
@@ -354,6 +354,113 @@ def test_chunk_of_one_token_is_the_attention_of_one(env):  # noqa: F811
     assert float((one.float() - many.float()).abs().max()) <= 5 * 3 * 2.0 ** -11
 
 
+def _chunk_call(env, q, cache, starts, ln, **kw):
+    torch, spax, dev = env
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full(q.shape[:2], float("nan"), device=dev)
+    a = spax.make_chunk_attention(cache, q, starts, ln, out, lse=lse, **kw)
+    need = spax.spax_chunk_attention_workspace_bytes(a)
+    spax.spax_chunk_attention(a, torch.empty(need, dtype=torch.uint8, device=dev) if need else None)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("far", [False, True], ids=["whole", "pieces"])
+@pytest.mark.parametrize("page", [4, 16, 64])
+def test_chunk_pages_that_are_not_there(env, page, far):  # noqa: F811
+    """Entries that name no page, in the middle, at the beginning and for all of a token's keys: those
+    keys are left out, and a token without any gives zeros and -inf."""
+    torch, spax, dev = env
+    sizes = [(70, 300), (5, 0), (3, 200)]
+    q, kc, vc, table, starts, ln, scales = _chunk_inputs(env, sizes, 4, 2, 64, page, "fp16", "fp16",
+                                                         "heads", 13)
+    kc.masked_fill_(torch.isnan(kc), 7.0)
+    for s, at in ((0, 100), (0, 260), (0, 345), (2, 0)):
+        table[s, at // page] = -1 if at != 260 else kc.shape[0]
+    table[1] = -1
+    if far:
+        wide = torch.full((3, 16384 // page), -1, dtype=torch.int32, device=dev)
+        wide[:, :table.shape[1]] = table
+        table = wide
+    out, lse = _chunk_call(env, q, spax.make_kv_cache(kc, vc, table), starts, ln)
+    _chunk_check(q, kc, vc, table, starts, ln, scales, out, lse, 64, "fp16", 0, None)
+    first = int(starts[1])
+    assert not bool(out[first:first + 5].any()) and bool((lse[first:first + 5] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("seqs", [250, 300])
+def test_chunk_many_sequences_in_pieces(env, seqs):  # noqa: F811
+    """More and fewer sequences than those whose steps are counted, some long, one key head."""
+    torch, spax, dev = env
+    sizes = [((i % 3), 2000 if i % 50 == 0 else 20 + i) for i in range(seqs)]
+    q, kc, vc, table, starts, ln, scales = _chunk_inputs(env, sizes, 2, 1, 64, 16, "bf16", "bf16",
+                                                         "heads", 17)
+    wide = torch.full((seqs, 512), -1, dtype=torch.int32, device=dev)
+    wide[:, :table.shape[1]] = table
+    out, lse = _chunk_call(env, q, spax.make_kv_cache(kc, vc, wide), starts, ln)
+    _chunk_check(q, kc, vc, wide, starts, ln, scales, out, lse, 64, "bf16", 0, None)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
+def test_chunk_scales(env, scale):  # noqa: F811
+    """A scale below zero turns the order of the scores, and one of zero makes them equal."""
+    torch, spax, dev = env
+    q, kc, vc, table, starts, ln, _ = _chunk_inputs(env, [(40, 90)], 4, 2, 64, 16, "fp16", "fp16",
+                                                    "heads", 19)
+    out, lse = _chunk_call(env, q, spax.make_kv_cache(kc, vc, table), starts, ln, scale=scale)
+    k, v = (np.nan_to_num(_f64(t)) for t in (kc, vc))
+    rows, ref, ref_lse, mass, reach = oprompt.chunk_attention(
+        _f64(q), k, v, table.cpu().numpy(), starts.cpu().numpy(), ln.cpu().numpy(), scale)
+    score = 68 * 2.0 ** -24 * reach
+    tol = STEP["fp16"] * np.abs(ref) + TINY["fp16"] + mass * (
+        2 * score[..., None] + 2048 * 2.0 ** -24 + 2.0 ** -16 + STEP["fp16"])
+    _check(_f64(out)[rows], ref, tol, "out")
+    _check(_f64(lse)[rows], ref_lse, score + 2048 * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(ref_lse)), "lse")
+
+
+def test_chunk_scores_of_minus_infinity(env):  # noqa: F811
+    """Rows whose scores are all -inf give zeros; a single one is left out."""
+    torch, spax, dev = env
+    kc, vc = (torch.ones(4, 1, 16, 64, dtype=torch.float16, device=dev) for _ in range(2))
+    kc[0, 0, 5, 0] = -float("inf")
+    vc[0, 0, 5] = 9.0
+    q = torch.zeros(40, 2, 64, dtype=torch.float16, device=dev)
+    q[:, 0, 0] = 1.0                   # sees -inf at key 5, else 1
+    q[:, 1] = 1.0
+    q[:, 1, 0] = -float("inf")         # -inf everywhere but at key 5, where it is inf
+    table = torch.arange(4, dtype=torch.int32, device=dev)[None].contiguous()
+    out, lse = _chunk_call(env, q, spax.make_kv_cache(kc, vc, table),
+                           torch.tensor([0, 40], dtype=torch.int32, device=dev),
+                           torch.tensor([40], dtype=torch.int32, device=dev), scale=1.0)
+    assert bool((out[:, 0] == 1.0).all())
+    assert not bool(out[:5, 1].any()) and bool((lse[:5, 1] == -float("inf")).all())
+    assert bool(torch.isnan(out[5:, 1]).all())
+    seen = torch.tensor([i + 1 - (i >= 5) for i in range(40)], device=dev)
+    assert torch.allclose(lse[:, 0], 1.0 + seen.float().log(), atol=1e-5)
+
+
+def test_chunk_far_in_memory(env):  # noqa: F811
+    """Pages more than 2^32 elements into the cache."""
+    torch, spax, dev = env
+    pages, page, dim = (1 << 22) + 64, 16, 64
+    whole = torch.empty(pages, 1, page, dim, dtype=torch.float16, device=dev)
+    g = _gen(torch, 23)
+    ids = torch.tensor([3, pages - 1, pages - 17, 1 << 21, pages - 2, 9], device=dev)
+    near = torch.full((6, 1, page, dim), float("nan"), dtype=torch.float16, device=dev)
+    for i in range(6):
+        near[i] = _randn(torch, g, (1, page, dim), torch.float16)
+        whole[ids[i]] = near[i]
+    q = _randn(torch, g, (30, 4, dim), torch.float16)
+    starts = torch.tensor([0, 30], dtype=torch.int32, device=dev)
+    ln = torch.tensor([91], dtype=torch.int32, device=dev)
+    got = []
+    for cached, table in ((whole, ids), (near, torch.arange(6, device=dev))):
+        cache = spax.make_kv_cache(cached, cached, table.int()[None].contiguous())
+        got.append(_chunk_call(env, q, cache, starts, ln))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert bool(torch.isfinite(got[0][0]).all())
+
+
 # ------------------------------------------------------------------ product with a packed blob
 
 GEMM = [
@@ -479,3 +586,65 @@ def test_packed_gemm_rows_are_apart(env):  # noqa: F811
     keep = [i for i in range(66) if i not in (7, 64)]
     assert torch.equal(z[keep], y[keep]) and bool(torch.isnan(z[7]).all())
     assert not bool(torch.isfinite(z[64]).any())
+
+
+@pytest.mark.parametrize("rows,d_in,d_out", [(3, 32768, [65536, 8192]), (70, 32768, [65536, 8192]),
+                                             (250, 11000, [10944])])
+def test_packed_gemm_far_in_memory(env, rows, d_in, d_out):  # noqa: F811
+    """Blobs of more than 2^32 bytes: the last records, and columns at the ends of one.  The last case: k
+    cut into pieces between tiles of 256 rows."""
+    torch, spax, dev = env
+    L = spax.spax_layout_init(d_in, d_out, spax.FMT_FP16, 128, 128 if d_out[0] % 128 == 0 else 64)
+    assert L.off_A > 1 << 32 or rows == 250
+    packed = torch.zeros(int(L.total_bytes), dtype=torch.uint8, device=dev)
+    w = packed[:int(L.off_A)].view(torch.float16).view(d_in, -1)
+    used = torch.tensor([0, 5, d_in * 5 // 8, d_in - 17, d_in - 2, d_in - 1], device=dev)
+    g = _gen(torch, 29)
+    for k in used.tolist():
+        w[k] = _randn(torch, g, (w.shape[1],), torch.float16)
+    x = torch.zeros(rows, d_in, dtype=torch.float16, device=dev)
+    x[:, used] = _randn(torch, g, (rows, 6), torch.float16)
+    y = torch.empty(rows, sum(d_out), device=dev)
+    a = spax.make_packed_gemm(L, packed, x, y)
+    need = spax.spax_packed_gemm_workspace_bytes(a)
+    spax.spax_packed_gemm(a, torch.empty(need, dtype=torch.uint8, device=dev) if need else None)
+    torch.cuda.synchronize()
+    ref = _f64(x[:, used]) @ _f64(w[used, :sum(d_out)])
+    mass = np.abs(_f64(x[:, used])) @ np.abs(_f64(w[used, :sum(d_out)]))
+    _check(_f64(y), ref, mass * 2.0 ** -20, "y")   # six products, a handful of roundings each
+
+
+# Sizes at which the rows go by tiles of 128 and of 256, with and without splits of k, with ends of
+# every kind inside the last tile.
+LARGE = [
+    (2000, 130, [2112, 1984], "fp16", "plain", "silu", True, "fp16", "fp16", 1.0),
+    (1900, 77, [2112, 2112], "fp16", "gated", "gelu", True, None, "bf16", 1.0),
+    (200, 4099, [12224], "fp16", "plain", "silu", False, None, "fp32", 1.0),
+    (2000, 200, [2176, 1920], "int4", "act", "silu", False, "fp32", "fp16", 0.5),
+    (200, 4099, [12160], "int4", "plain", "silu", True, None, "fp16", 1.0),
+    (3001, 130, [4352], "fp16", "plain", "silu", False, "fp32", "fp32", 1.0),
+    (3001, 64, [2240, 2240], "fp16", "gated", "silu", False, None, "fp16", 1.0),
+    (1000, 4100, [4032], "fp16", "act", "gelu", True, "bf16", "bf16", 1.0),
+    (3001, 190, [4352], "int4", "plain", "silu", True, None, "fp16", 1.0),
+    (1000, 3000, [2048, 2048], "int4", "gated", "silu", False, None, "fp16", 1.0),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=[f"{c[0]}x{c[1]}x{sum(c[2])}-{c[3]}-{c[4]}" for c in LARGE])
+def test_packed_gemm_of_many_rows(env, case):  # noqa: F811
+    """Rows at both ends of every tile, all columns."""
+    torch, spax, dev = env
+    rows, d_in, d_out, fmt, form, act, bias, res, y, scale = case
+    L, packed, w, x, b, r, out = _gemm_case(env, case, rows + d_in)
+    out = out[:, :out.shape[1] - 3].contiguous()
+    a = spax.make_packed_gemm(L, packed, x, out, bias=b, act=None if form == "plain" else act,
+                              gated=form == "gated", residual=r, scale=scale)
+    need = spax.spax_packed_gemm_workspace_bytes(a)
+    print(f"[gemm] {case} workspace {need}", flush=True)
+    spax.spax_packed_gemm(a, torch.full((need,), 0xFF, dtype=torch.uint8, device=dev) if need else None)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out).all())
+    pick = sorted({i for t in range(0, rows, 128) for i in (t, t + 1, t + 31, t + 32, t + 127)
+                   if i < rows} | {rows - 1})[:96] + [rows - 2, rows - 1]
+    rest = [t[pick] if t is not None else None for t in (x, r, out)]
+    _gemm_check(_f64(rest[2]), rest[0], w, case, b, rest[1])
