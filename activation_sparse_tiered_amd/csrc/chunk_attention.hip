@@ -577,7 +577,8 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
           u32x4* at = reinterpret_cast<u32x4*>(v + 16 * e);
           const u32x4 x = *at;
           const int row = e / S::kPieces, key = key0 + row;
-          const bool seen = key >= in.lo && key < in.hi && __shfl(page, row) >= 0;
+          const bool paged = __shfl(page, row) >= 0;  // (whole waves)
+          const bool seen = paged && key >= in.lo && key < in.hi;
           const uint32_t bad = odd_ones<T>(x.x) | odd_ones<T>(x.y) | odd_ones<T>(x.z) | odd_ones<T>(x.w);
           if (!seen && bad) *at = u32x4{0u, 0u, 0u, 0u};  // whatever was left in unused rows
           odd |= seen ? bad : 0u;
@@ -638,7 +639,8 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
   if (first + r >= tile.to) return;
   const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
   if (steps.pieces <= 1) {
-    const float f = w.l == 0.0f ? 0.0f : v_mul / w.l;
+    const bool none = w.l == 0.0f;  // no key, or all scores -inf: zeros
+    const float f = v_mul / w.l;
     T* out = (T*)a.out + (tile.first + token) * a.ot + head * a.oh;
 #pragma unroll
     for (int b = 0; b < R::OB; ++b)
@@ -646,7 +648,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
       for (int y = 0; y < 4; ++y) {
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = f == 0.0f ? 0.0f : w.value(b, 4 * y + i) * f;
+        for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : w.value(b, 4 * y + i) * f;
         store_n<4>(out + 32 * b + 8 * y + 4 * h, x);
       }
     if (a.lse && h == 0) a.lse[at] = log_sum<T>(w.m, w.l);
@@ -796,7 +798,6 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   ChunkPlan p{};
   if (a->n_tokens == 0) return p;
   const int64_t group = a->n_heads / c.n_kv_heads;
-  // every sequence with tokens has at most one tile that is not full
   const auto tiles = [&](int rows) {
     // every sequence with tokens has at most one tile that is not full
     return a->n_tokens * group / rows + (c.n_seqs < a->n_tokens ? c.n_seqs : a->n_tokens);
