@@ -40,7 +40,8 @@ struct ChunkArgs {
   int64_t qt, qh, ot, oh;
   int64_t k_page, k_head, k_row, v_page, v_head, v_row, table_stride;
   int32_t n_tokens, n_heads, n_kv, group, n_seqs, n_pages, page_shift;
-  int32_t max_len, window, rows, tiles, pieces, least_steps;  // rows: of a tile
+  int32_t max_len, window, rows, tiles, pieces;  // rows: of a tile
+  int32_t key_shift, least_steps, whole_steps, shares, join_groups, join_waves;   // a step is 2^key_shift keys
   float scale;
 };
 
@@ -59,18 +60,19 @@ __device__ inline int lo_of(const ChunkArgs& a, int p) {
 }
 __device__ inline int hi_of(int p) { return p < 0 ? 0 : p + 1; }
 
-// Steps of `keys` keys that hold [lo, hi).
-__device__ inline int steps_in(int lo, int hi, int keys) {
-  return hi > lo ? (hi + keys - 1) / keys - lo / keys : 0;
+// Steps that hold [lo, hi).
+__device__ inline int steps_in(const ChunkArgs& a, int lo, int hi) {
+  return hi > lo ? ((hi - 1) >> a.key_shift) + 1 - (lo >> a.key_shift) : 0;
 }
 
-// Sequence s = base + lane: its first row, new tokens and tiles.
+// Sequence s: its first row, new tokens, tiles and length.
 struct Seq {
-  int first, n_new, tiles;
+  int first, n_new, tiles, len;
 };
 __device__ inline Seq seq_at(const ChunkArgs& a, int s) {
-  Seq q{0, 0, 0};
+  Seq q{0, 0, 0, 0};
   if (s < a.n_seqs) {
+    q.len = clamp_to(a.lens[s], a.max_len);
     q.first = clamp_to(a.starts[s], a.n_tokens);
     const int n = clamp_to(a.starts[s + 1], a.n_tokens) - q.first;
     q.n_new = n < 0 ? 0 : n;
@@ -79,12 +81,17 @@ __device__ inline Seq seq_at(const ChunkArgs& a, int s) {
   return q;
 }
 
-// Tile `index` of all sequences' tiles laid end to end.  Lane l holds sequence base + l; past 64
-// sequences that is a chain of loads, one for every 64.
-__device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
+// Lane l holds sequence base + l; `seqs` are the first 64, which are loaded once.  Past them every 64
+// are a step of a chain of loads.
+__device__ inline Seq seqs_from(const ChunkArgs& a, const Seq& seqs, int base, int lane) {
+  return base == 0 ? seqs : seq_at(a, base + lane);
+}
+
+// Tile `index` of all sequences' tiles laid end to end.
+__device__ inline Tile find_tile(const ChunkArgs& a, const Seq& seqs, int index, int lane) {
   int before = 0;
   for (int base = 0; base < a.n_seqs; base += 64) {
-    const Seq q = seq_at(a, base + lane);
+    const Seq q = seqs_from(a, seqs, base, lane);
     const int upto = before + mask::wave_scan(q.tiles);
     const int last = __builtin_amdgcn_readlane(upto, 63);
     if (index < last) {
@@ -93,7 +100,7 @@ __device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
       t.seq = base + who;
       t.first = __builtin_amdgcn_readlane(q.first, who);
       t.n_new = __builtin_amdgcn_readlane(q.n_new, who);
-      t.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[t.seq], a.max_len));
+      t.len = __builtin_amdgcn_readlane(q.len, who);
       const int begins =
           __builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(q.tiles, who);
       t.from = (index - begins) * a.rows;
@@ -106,21 +113,20 @@ __device__ inline Tile find_tile(const ChunkArgs& a, int index, int lane) {
   return Tile{0, 0, 0, 0, 0, 0};
 }
 
-// How many steps of a tile's keys make a piece: an equal share of all tiles' steps for each of kShares
-// workgroups, but no fewer than the plan has room for.  Every wave of both launches finds the same
+// How many steps of a tile's keys make a piece, about: an equal share of all tiles' steps for each of the
+// plan's shares, but no fewer than it has room for.  Every wave of both launches finds the same
 // number, in integers, from at most kCounted sequences; with more the plan's own stands.
-constexpr int kShares = 512, kCounted = 256;
-__device__ inline int piece_steps(const ChunkArgs& a, int keys, int lane) {
+constexpr int kCounted = 256;
+__device__ inline int piece_steps(const ChunkArgs& a, const Seq& seqs, int lane) {
   if (a.pieces == 1 || a.n_seqs > kCounted) return a.least_steps;
   int mine = 0;
   for (int base = 0; base < a.n_seqs; base += 64) {
-    const int s = base + lane;
-    const Seq q = seq_at(a, s);
+    const Seq q = seqs_from(a, seqs, base, lane);
     if (q.n_new == 0) continue;
-    const int len = clamp_to(a.lens[s], a.max_len), p = len - q.n_new;
+    const int len = q.len, p = len - q.n_new;
     // of the first token and of the last
-    const int some = steps_in(lo_of(a, p), hi_of(p), keys);
-    const int more = steps_in(lo_of(a, len - 1), hi_of(len - 1), keys);
+    const int some = steps_in(a, lo_of(a, p), hi_of(p));
+    const int more = steps_in(a, lo_of(a, len - 1), hi_of(len - 1));
     const int64_t units = (int64_t)q.tiles * ((some + more + 1) / 2);
     constexpr int kMost = 1 << 22;  // kCounted of them stay below 2^31
     mine += units < kMost ? (int)units : kMost;
@@ -128,29 +134,24 @@ __device__ inline int piece_steps(const ChunkArgs& a, int keys, int lane) {
 #pragma unroll
   for (int z = 32; z > 0; z >>= 1) mine += __shfl_xor(mine, z);
   mine = __builtin_amdgcn_readfirstlane(mine);
-  const int64_t share = ((int64_t)mine * a.n_kv + kShares - 1) / kShares;
+  const int64_t share = ((int64_t)mine * a.n_kv + a.shares - 1) / a.shares;
   return share > a.least_steps ? (int)share : a.least_steps;
 }
-
-// A tile of up to kWholeSteps steps stays whole: its pieces' way through memory and the second launch take
-// longer than the steps they save (1 x 509 tokens of 32 heads, nine steps: 25 us whole, 36 in
-// two).  Longer ones are cut down to kLeastSteps (1 x 5 over 8192: 24.2 us with six, 21.7 with four,
-// 21.0 with three, of which more join).
-constexpr int kWholeSteps = 12, kLeastSteps = 4;
 
 // The tile's keys [lo, hi), the steps of one piece of them, and how many pieces there are.
 struct Piece {
   int lo, hi, first, count, pieces;
 };
-__device__ inline Piece piece_of(const ChunkArgs& a, const Tile& t, int piece, int per, int keys) {
+__device__ inline Piece piece_of(const ChunkArgs& a, const Tile& t, int piece, int per) {
   Piece p;
   p.hi = hi_of(t.position((t.to - 1) / a.group));
   p.lo = lo_of(a, t.position(t.from / a.group));
-  const int all = steps_in(p.lo, p.hi, keys);
-  if (all <= kWholeSteps) per = kWholeSteps;
-  p.pieces = (all + per - 1) / per;
+  const int all = steps_in(a, p.lo, p.hi);
+  const int n = all <= a.whole_steps ? 1 : (all + per / 2) / per;
+  per = n > 1 ? (all + n - 1) / n : all;
+  p.pieces = n > 1 ? (all + per - 1) / per : 1;
   const int from = piece * per < all ? piece * per : all;
-  p.first = p.lo / keys + from;
+  p.first = (p.lo >> a.key_shift) + from;
   p.count = from + per < all ? per : all - from;
   return p;
 }
@@ -158,9 +159,9 @@ __device__ inline Piece piece_of(const ChunkArgs& a, const Tile& t, int piece, i
 // How a step's keys and values lie in LDS: rows of D 16-bit values, in 16-byte pieces whose places
 // within a row are turned by the row, so that the 16 rows of a pass over K (one piece each) lie on
 // different banks, and the four rows of a transposing read of V (four pieces each) do.
-template <class T, bool NARROW, int D>
+template <class T, bool NARROW, int D, int KEYS>
 struct Shape {
-  static constexpr int kKeys = D >= 192 ? 32 : 64;     // per step
+  static constexpr int kKeys = KEYS;                   // per step
   static constexpr int EB = NARROW ? 1 : 2;
   static constexpr int kPieces = D / 8;                // of a row in LDS
   static constexpr int kRow = 2 * D;
@@ -203,9 +204,9 @@ __device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "m
 
 // Brings a step's keys and values into LDS.  16-bit rows go there straight from memory, 8-bit ones
 // through registers, where they are widened once for all four waves.
-template <class T, bool NARROW, int D, int W>
+template <class T, bool NARROW, int D, int KEYS, int W>
 struct Loader {
-  using S = Shape<T, NARROW, D>;
+  using S = Shape<T, NARROW, D, KEYS>;
   static constexpr int kThreads = 64 * W;
   const int32_t* table;  // of the sequence
   int page_shift, n_pages, lo, hi;  // the tile's keys
@@ -237,7 +238,12 @@ struct Loader {
     u32x4 x[NARROW ? kLoads : 1];
   };
   Side k, v;
-  __device__ inline void start(int lane) {
+  __device__ inline void open(const ChunkArgs& a, const Tile& t, const Piece& p, int kvh, int lane) {
+    table = a.table + t.seq * a.table_stride;
+    page_shift = a.page_shift; n_pages = a.n_pages; lo = p.lo; hi = p.hi;
+    k.base = (const uint8_t*)a.k + (int64_t)S::EB * kvh * a.k_head;
+    v.base = (const uint8_t*)a.v + (int64_t)S::EB * kvh * a.v_head;
+    k.page = a.k_page; k.row = a.k_row; v.page = a.v_page; v.row = a.v_row;
     const int at = kWhole ? lane / kCached % 4 : 0;
     k.lane = S::EB * at * k.row;
     v.lane = S::EB * at * v.row;
@@ -316,6 +322,21 @@ __device__ inline uint32_t odd_ones(uint32_t w) {
   return ((w & 0x7fff7fffu) + Mma<T>::kExpStep) & 0x80008000u;
 }
 
+// Takes them out of `pieces` of 16 bytes.
+template <class T>
+__device__ inline void clear_odd(uint8_t* v, int pieces, int thread, int threads) {
+  for (int e = thread; e < pieces; e += threads) {
+    u32x4* at = reinterpret_cast<u32x4*>(v + 16 * e);
+    u32x4 x = *at;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const uint32_t bad = odd_ones<T>(x[y]);
+      x[y] &= ~(bad | (bad - (bad >> 15)));
+    }
+    *at = x;
+  }
+}
+
 // The exponentials are taken of s - m + kLift (base 2), and the running maximum m is raised only once a
 // score is kSlack above it, so the largest is 2^(kLift + kSlack): all that fp16 holds.  In fp16 the lift
 // keeps a long tail under one large key; both cancel in o / l.
@@ -336,9 +357,9 @@ __device__ inline float log_sum(float m, float l) {
 }
 
 // A wave's 32 query rows; a lane has row lane % 32.
-template <class T, bool NARROW, int D>
+template <class T, bool NARROW, int D, int KEYS>
 struct Rows {
-  using S = Shape<T, NARROW, D>;
+  using S = Shape<T, NARROW, D, KEYS>;
   static constexpr int KC = D / 16, OB = D / 32;
   using Scores = f32x16[S::kBlocks];
   using Keys = u32x4[KC][S::kBlocks];
@@ -351,6 +372,23 @@ struct Rows {
   uint64_t up[(OB + 3) / 4], down[(OB + 3) / 4];
   int lo, hi;  // the keys that the row sees
 
+  // The row of this token and head, but for o: cleared here, it would be kept in memory longer (234 to 256
+  // registers and spills in chunk_kernel).  The scale is kept above zero, as the largest score is found before it is
+  // applied: a sign goes to the queries, and a scale of zero makes them zeros.
+  __device__ inline void begin(const ChunkArgs& a, const Tile& t, int token, int head, float to_log2,
+                               int lane) {
+    const uint32_t flip = to_log2 < 0.0f ? 0x80008000u : 0u, keep = to_log2 == 0.0f ? 0u : ~0u;
+    const uint8_t* from = (const uint8_t*)a.q + 2 * ((t.first + token) * a.qt + head * a.qh);
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+      q[c] = (*reinterpret_cast<const u32x4*>(from + 32 * c + 16 * (lane >> 5)) ^ flip) & keep;
+#pragma unroll
+    for (int b = 0; b < (OB + 3) / 4; ++b) up[b] = down[b] = 0u;
+    m = -INFINITY;
+    l = 0.0f;
+    lo = lo_of(a, t.position(token));
+    hi = hi_of(t.position(token));
+  }
   static __device__ inline u32x4 read_keys(const uint8_t* keys, int block, int c, int lane) {
     const int row = 32 * block + (lane & 31);
     return *reinterpret_cast<const u32x4*>(keys + row * S::kRow +
@@ -483,43 +521,59 @@ struct Rows {
   }
 };
 
+template <bool NARROW>
+__device__ inline float to_log2_of(const ChunkArgs& a, int kvh) {
+  const float f = a.scale * kLog2e;
+  return NARROW && a.k_scale ? f * a.k_scale[kvh] : f;
+}
+template <bool NARROW>
+__device__ inline float v_mul_of(const ChunkArgs& a, int kvh) {
+  return NARROW && a.v_scale ? a.v_scale[kvh] : 1.0f;
+}
+
+// A piece of 32 rows of a tile leaves its sums as a wave holds them, dims 8 g + 4 h .. of row r in lane
+// 32 h + r of group g, so that they go to memory and come back 1024 bytes at once (by rows, 8 x 128
+// over 1000 took 88 us), and its maxima and weights.
+__device__ inline int64_t part_of(const ChunkArgs& a, int piece, int rows32, int kvh) {
+  return ((int64_t)piece * a.tiles * (a.rows / 32) + rows32) * a.n_kv + kvh;
+}
+template <int D>
+__device__ inline f32x4* part_sums(const ChunkArgs& a, int64_t part, int group, int lane) {
+  return reinterpret_cast<f32x4*>(a.part_o) + (part * (D / 8) + group) * 64 + lane;
+}
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ inline f32x2* part_weight(const ChunkArgs& a, int64_t part, int r) {
+  return reinterpret_cast<f32x2*>(a.part_ml) + part * 32 + r;
+}
+
+// Keys of a step that a workgroup's waves share.
+constexpr int shared_keys(int dim) { return dim >= 192 ? 32 : 64; }
+
 template <class T, bool NARROW, int D, int W>
 __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkArgs a) {
-  using S = Shape<T, NARROW, D>;
-  using R = Rows<T, NARROW, D>;
+  constexpr int kKeys = shared_keys(D);
+  using S = Shape<T, NARROW, D, kKeys>;
+  using R = Rows<T, NARROW, D, kKeys>;
   constexpr int kThreads = 64 * W;
   extern __shared__ __attribute__((aligned(256))) uint8_t lds[];  // two steps' keys and values
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, r = lane & 31;
   // Workgroups go to the 8 XCDs in turn: the tiles of a key head, which read the same rows, meet on
-  // few of them.  Later tiles of a sequence see more keys and are begun first.
+  // few of them.  Later tiles of a sequence see more keys and are begun first, and the pieces that
+  // most tiles do not need come last (with a tile's pieces side by side 8 x 128 over 1000 took 72
+  // us for 50).
   const int kvh = blockIdx.x % (unsigned)a.n_kv, rest = blockIdx.x / (unsigned)a.n_kv;
-  const int piece = rest % a.pieces;
-  const Tile tile = find_tile(a, a.tiles - 1 - rest / a.pieces, lane);
+  const int piece = rest / a.tiles;
+  const Seq seqs = seq_at(a, lane);
+  const int index = a.tiles - 1 - rest % a.tiles;
+  const Tile tile = find_tile(a, seqs, index, lane);
   if (tile.from == tile.to) return;
-
-  Loader<T, NARROW, D, W> in;
-  const Piece steps = piece_of(a, tile, piece, piece_steps(a, S::kKeys, lane), S::kKeys);
+  const Piece steps = piece_of(a, tile, piece, piece_steps(a, seqs, lane));
   if (piece > 0 && piece >= steps.pieces) return;
-  in.lo = steps.lo;
-  in.hi = steps.hi;
-  float to_log2 = a.scale * kLog2e, v_mul = 1.0f;
-  if constexpr (NARROW) {
-    if (a.k_scale) to_log2 *= a.k_scale[kvh];
-    if (a.v_scale) v_mul = a.v_scale[kvh];
-  }
-  in.k.base = (const uint8_t*)a.k + (int64_t)S::EB * kvh * a.k_head;
-  in.v.base = (const uint8_t*)a.v + (int64_t)S::EB * kvh * a.v_head;
-  in.table = a.table + tile.seq * a.table_stride;
-  in.k.page = a.k_page; in.k.row = a.k_row; in.v.page = a.v_page; in.v.row = a.v_row;
-  in.page_shift = a.page_shift; in.n_pages = a.n_pages;
-  in.start(lane);
-
-  // The scale is kept above zero, as the largest score is found before it is applied: a sign goes to
-  // the queries, and a scale of zero makes them zeros.
-  const uint32_t flip = to_log2 < 0.0f ? 0x80008000u : 0u, keep = to_log2 == 0.0f ? 0u : ~0u;
-  to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
+  Loader<T, NARROW, D, kKeys, W> in;
+  in.open(a, tile, steps, kvh, lane);
+  float to_log2 = to_log2_of<NARROW>(a, kvh);
   const int first = tile.from + 32 * wave;  // the wave's rows; past the last row, that one again
   const bool works = first < tile.to;
   const int last = first + 32 < tile.to ? first + 31 : tile.to - 1;
@@ -528,18 +582,10 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
   const int row = first + r < tile.to ? first + r : tile.to - 1;
   const int token = row / a.group, head = kvh * a.group + row % a.group;
   R w;
-  const uint8_t* q = (const uint8_t*)a.q + 2 * ((tile.first + token) * a.qt + head * a.qh);
-#pragma unroll
-  for (int c = 0; c < R::KC; ++c)
-    w.q[c] = (*reinterpret_cast<const u32x4*>(q + 32 * c + 16 * h) ^ flip) & keep;
+  w.begin(a, tile, token, head, to_log2, lane);
 #pragma unroll
   for (int b = 0; b < R::OB; ++b) w.o[b] = f32x16{};
-#pragma unroll
-  for (int b = 0; b < (R::OB + 3) / 4; ++b) w.up[b] = w.down[b] = 0u;
-  w.m = -INFINITY;
-  w.l = 0.0f;
-  w.lo = lo_of(a, tile.position(token));
-  w.hi = hi_of(tile.position(token));
+  to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
   // 0 * inf is NaN, so where some row does not see some key, values that are not finite are taken out
   // of the step and noted for the rows that do see them.
   __shared__ int odd_step[2];
@@ -588,16 +634,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
         if (__builtin_amdgcn_readfirstlane(odd_step[i & 1])) {
           if (works) w.note_odd(v, key0, page, lane);
           mask::lds_barrier();
-          for (int e = threadIdx.x; e < kMine; e += kThreads) {
-            u32x4* at = reinterpret_cast<u32x4*>(v + 16 * e);
-            u32x4 x = *at;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t bad = odd_ones<T>(x[y]);
-              x[y] &= ~(bad | (bad - (bad >> 15)));
-            }
-            *at = x;
-          }
+          clear_odd<T>(v, kMine, threadIdx.x, kThreads);
           mask::lds_barrier();
           if (threadIdx.x == 0) odd_step[i & 1] = 0;
         }
@@ -640,7 +677,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
   const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
   if (steps.pieces <= 1) {
     const bool none = w.l == 0.0f;  // no key, or all scores -inf: zeros
-    const float f = v_mul / w.l;
+    const float f = v_mul_of<NARROW>(a, kvh) / w.l;
     T* out = (T*)a.out + (tile.first + token) * a.ot + head * a.oh;
 #pragma unroll
     for (int b = 0; b < R::OB; ++b)
@@ -654,7 +691,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
     if (a.lse && h == 0) a.lse[at] = log_sum<T>(w.m, w.l);
     return;
   }
-  const int64_t part = (int64_t)piece * a.n_tokens * a.n_heads + at;
+  const int64_t part = part_of(a, piece, index * W + wave, kvh);
 #pragma unroll
   for (int b = 0; b < R::OB; ++b)
 #pragma unroll
@@ -662,118 +699,326 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
       f32x4 x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * y + i);
-      *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * b + 8 * y + 4 * h) = x;
+      *part_sums<D>(a, part, 4 * b + y, lane) = x;
+    }
+  if (h == 0) *part_weight(a, part, r) = f32x2{w.m, w.l};
+}
+
+// All loads but the last `N` are there.
+template <int N>
+__device__ inline void wait_loads_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// The wave's accesses to LDS are done.
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+
+// A tile of 32 rows: its four waves take 32 keys of each step of 128, bring them in by themselves, without
+// a barrier, and join at the end.
+constexpr int kFewRows = 32, kFewShift = 7;
+template <class T, bool NARROW, int D>
+__global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
+  constexpr int kKeys = 32, kWaves = 4, kStep = 1 << kFewShift;
+  using S = Shape<T, NARROW, D, kKeys>;
+  using R = Rows<T, NARROW, D, kKeys>;
+  using In = Loader<T, NARROW, D, kKeys, 1>;
+  extern __shared__ __attribute__((aligned(256))) uint8_t lds[];
+  __shared__ float ml[kWaves][32][2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, r = lane & 31;
+  const int kvh = blockIdx.x % (unsigned)a.n_kv, rest = blockIdx.x / (unsigned)a.n_kv;
+  const int piece = rest / a.tiles;
+  const Seq seqs = seq_at(a, lane);
+  const int index = a.tiles - 1 - rest % a.tiles;
+  const Tile tile = find_tile(a, seqs, index, lane);
+  if (tile.from == tile.to) return;
+  const Piece steps = piece_of(a, tile, piece, piece_steps(a, seqs, lane));
+  if (piece > 0 && piece >= steps.pieces) return;
+  In in;
+  in.open(a, tile, steps, kvh, lane);
+  float to_log2 = to_log2_of<NARROW>(a, kvh);
+  const int row = tile.from + r < tile.to ? tile.from + r : tile.to - 1;
+  const int token = row / a.group, head = kvh * a.group + row % a.group;
+  R w;
+  w.begin(a, tile, token, head, to_log2, lane);
+#pragma unroll
+  for (int b = 0; b < R::OB; ++b) w.o[b] = f32x16{};
+  to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
+  const int all_lo = lo_of(a, tile.position((tile.to - 1) / a.group));
+  const int all_hi = hi_of(tile.position(tile.from / a.group));
+
+  uint8_t* const keys = lds + wave * 2 * S::kBuffer;
+  uint8_t* const values = keys + S::kBuffer;
+  int key0 = steps.first * kStep + kKeys * wave;
+  const int end = (steps.first + steps.count) * kStep;
+  const int stop = steps.hi < end ? steps.hi : end;
+  if (key0 + kKeys <= steps.lo) key0 += kStep;
+  if (key0 < stop) {
+    int page = in.page_of(in.look_up(key0, lane), key0, lane);
+    in.template load<false>(keys, page, key0, 0, lane);
+    in.template load<true>(values, page, key0, 0, lane);
+    int entry = in.look_up(key0 + kStep, lane);
+    for (; key0 < stop;) {
+      const int next = key0 + kStep;
+      const bool more = next < stop;
+      if constexpr (NARROW) {
+        in.template lay_out<false>(keys, 0, lane);
+        in.template lay_out<true>(values, 0, lane);
+        wait_lds();
+      } else {
+        wait_loads_but<In::kLoads>();
+      }
+      typename R::Scores s;
+      {
+        typename R::Keys k;
+#pragma unroll
+        for (int c = 0; c < R::KC; ++c)
+#pragma unroll
+          for (int b = 0; b < S::kBlocks; ++b) k[c][b] = R::read_keys(keys, b, c, lane);
+        wait_lds();  // the next keys may take their place
+        w.score(k, s);
+      }
+      int next_page = -1;
+      if (more) {
+        next_page = in.page_of(entry, next, lane);
+        in.template load<false>(keys, next_page, next, 0, lane);
+        if constexpr (NARROW) in.template load<true>(values, next_page, next, 0, lane);
+        entry = in.look_up(next + kStep, lane);
+      }
+      const bool edge = !__all(page >= 0) || key0 < all_lo || key0 + kKeys > all_hi;
+      if (edge) w.mask_out(s, key0, page, lane);
+      w.raise(s, to_log2);
+      u32x4 p[S::kSteps];
+      w.soften(s, to_log2, p);
+      if constexpr (!NARROW) {
+        if (more)
+          wait_loads_but<In::kLoads>();
+        else
+          wait_loads();
+      }
+      if (edge) {
+        uint32_t odd = 0u;
+#pragma unroll 1
+        for (int e = lane; e < S::kBuffer / 16; e += 64) {
+          u32x4* at = reinterpret_cast<u32x4*>(values + 16 * e);
+          const u32x4 x = *at;
+          const int row = e / S::kPieces, key = key0 + row;
+          const bool paged = __shfl(page, row) >= 0;
+          const bool seen = paged && key >= in.lo && key < in.hi;
+          const uint32_t bad =
+              odd_ones<T>(x.x) | odd_ones<T>(x.y) | odd_ones<T>(x.z) | odd_ones<T>(x.w);
+          if (!seen && bad) *at = u32x4{0u, 0u, 0u, 0u};  // whatever was left in unused rows
+          odd |= seen ? bad : 0u;
+        }
+        wait_lds();
+        if (__any(odd)) {
+          w.note_odd(values, key0, page, lane);
+          wait_lds();
+          clear_odd<T>(values, S::kBuffer / 16, lane, 64);
+          wait_lds();
+        }
+      }
+      typename R::Values v;
+#pragma unroll
+      for (int t = 0; t < S::kSteps; ++t)
+#pragma unroll
+        for (int b = 0; b < R::OB; ++b) v[t][b] = R::read_values(values, b, t, lane);
+      wait_lds();
+      if constexpr (!NARROW) {
+        if (more) in.template load<true>(values, next_page, next, 0, lane);
+      }
+      w.take_values(v, p);
+      key0 = next;
+      page = next_page;
+    }
+  }
+
+  // Join the waves: dims c .. c + 3 of all rows side by side.
+  w.l += __shfl_xor(w.l, 32);
+  float* mine = reinterpret_cast<float*>(keys);
+#pragma unroll
+  for (int b = 0; b < R::OB; ++b)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      f32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = w.value(b, 4 * y + i);
+      *reinterpret_cast<f32x4*>(mine + 4 * (32 * (8 * b + 2 * y + h) + r)) = x;
     }
   if (h == 0) {
-    a.part_ml[2 * part] = w.m;
-    a.part_ml[2 * part + 1] = w.l;
+    ml[wave][r][0] = w.m;
+    ml[wave][r][1] = w.l;
+  }
+  mask::lds_barrier();
+  if (tile.from + r >= tile.to) return;
+  float m = -INFINITY, l = 0.0f, f[kWaves];
+#pragma unroll
+  for (int y = 0; y < kWaves; ++y) m = fmaxf(m, ml[y][r][0]);
+#pragma unroll
+  for (int y = 0; y < kWaves; ++y) {
+    f[y] = __builtin_amdgcn_exp2f(ml[y][r][0] - (m == -INFINITY ? 0.0f : m));
+    l += f[y] * ml[y][r][1];
+  }
+  const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
+  const int64_t part = part_of(a, piece, index, kvh);
+  const bool whole = steps.pieces <= 1, none = l == 0.0f;
+  const float inv = v_mul_of<NARROW>(a, kvh) / l;
+  constexpr int kShare = D / 4 / kWaves;  // of the dims, four at a time
+  static_assert(kShare % 2 == 0, "two halves of a wave");
+#pragma unroll
+  for (int y = 0; y < kShare / 2; ++y) {
+    const int c = wave * kShare + 2 * y + h;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int z = 0; z < kWaves; ++z)
+      sum += f[z] * *reinterpret_cast<const f32x4*>(
+                        reinterpret_cast<const float*>(lds + z * 2 * S::kBuffer) + 4 * (32 * c + r));
+    if (whole) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : sum[i] * inv;
+      store_n<4>((T*)a.out + (tile.first + token) * a.ot + head * a.oh + 4 * c, x);
+    } else {
+      *part_sums<D>(a, part, c / 2, lane) = sum;
+    }
+  }
+  if (wave == 0 && h == 0) {
+    if (!whole)
+      *part_weight(a, part, r) = f32x2{m, l};
+    else if (a.lse)
+      a.lse[at] = log_sum<T>(m, l);
   }
 }
 
-// Joins the pieces of a row, a wave each: lane c has the maximum and the sum of piece c (at most 64),
-// four dims a lane, D / 4 lanes a piece.  Rows whose tile is one piece have their result already.
+// Joins the pieces of 32 rows of a tile: a wave takes join_groups groups of 8 dims, and where there are
+// many pieces join_waves waves take every join_waves-th.  Tiles of one piece have their result already.
 constexpr int kJoinWaves = 4;
 template <class T, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a) {
-  constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kLoads = 8;
-  constexpr int kKeys = D >= 192 ? 32 : 64;
+  constexpr int kLoads = 8;  // pieces in flight
+  __shared__ float others[kJoinWaves][6][64];
   const int lane = threadIdx.x & 63;
-  const int64_t at =
-      (int64_t)blockIdx.x * kJoinWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int token = (int)(at / a.n_heads), head = (int)(at % a.n_heads);
-  if (token >= a.n_tokens) return;
-  Tile tile{0, 0, 0, 0, 0, 0};
-  for (int base = 0; base < a.n_seqs; base += 64) {
-    const Seq q = seq_at(a, base + lane);
-    const uint64_t has = __ballot(token >= q.first && token - q.first < q.n_new);
-    if (!has) continue;
-    const int who = __builtin_ctzll(has);
-    tile.seq = base + who;
-    tile.first = __builtin_amdgcn_readlane(q.first, who);
-    tile.n_new = __builtin_amdgcn_readlane(q.n_new, who);
-    tile.len = __builtin_amdgcn_readfirstlane(clamp_to(a.lens[tile.seq], a.max_len));
-    const int row = (token - tile.first) * a.group + head % a.group, rows = tile.n_new * a.group;
-    tile.from = row / a.rows * a.rows;
-    tile.to = tile.from + a.rows < rows ? tile.from + a.rows : rows;
-    break;
-  }
-  if (tile.from == tile.to) return;
-  const int pieces = piece_of(a, tile, 0, piece_steps(a, kKeys, lane), kKeys).pieces;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, r = lane & 31;
+  const int split = a.join_waves;
+  const int item = split == 1 ? blockIdx.x * kJoinWaves + wave : blockIdx.x;
+  const int shares = D / 8 / a.join_groups, per = a.rows / 32;
+  const int share = item % shares, kvh = item / shares % a.n_kv, rows32 = item / shares / a.n_kv;
+  if (rows32 >= a.tiles * per) return;
+  const Seq seqs = seq_at(a, lane);
+  const Tile tile = find_tile(a, seqs, rows32 / per, lane);
+  const int first = tile.from + rows32 % per * 32;
+  if (first >= tile.to) return;
+  const int pieces = piece_of(a, tile, 0, piece_steps(a, seqs, lane)).pieces;
   if (pieces <= 1) return;
-  const int64_t step = (int64_t)a.n_tokens * a.n_heads;
-  const int slot = lane / kLanes, d = 4 * (lane % kLanes);
-  const float* from = a.part_o + at * D + d;
+  float pm[kLoads], pl[kLoads];
   f32x4 x[kLoads];
-#pragma unroll
-  for (int y = 0; y < kLoads; ++y) {
-    const int c = y * kAtOnce + slot;
-    x[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (slot < kAtOnce && c < pieces) x[y] = *reinterpret_cast<const f32x4*>(from + c * step * D);
-  }
-  const bool has = lane < pieces;
-  const float pm = has ? a.part_ml[2 * (at + lane * step)] : -INFINITY;
-  const float pl = has ? a.part_ml[2 * (at + lane * step) + 1] : 0.0f;
-  float m = pm;
-#pragma unroll
-  for (int z = 32; z > 0; z >>= 1) m = fmaxf(m, __shfl_xor(m, z));
-  const float f = has ? __builtin_amdgcn_exp2f(pm - (m == -INFINITY ? 0.0f : m)) : 0.0f;
-  float l = f * pl;
-#pragma unroll
-  for (int z = 32; z > 0; z >>= 1) l += __shfl_xor(l, z);
-  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c0 = 0;;) {
+  const auto load_weights = [&](int c0) {
 #pragma unroll
     for (int y = 0; y < kLoads; ++y) {
-      const int c = c0 + y * kAtOnce + slot;
-      sum += __shfl(f, c & 63) * x[y];
+      const int c = c0 + y * split;
+      pm[y] = -INFINITY;
+      pl[y] = 0.0f;
+      if (c < pieces) {
+        const f32x2 w = *part_weight(a, part_of(a, c, rows32, kvh), r);
+        pm[y] = w.x;
+        pl[y] = w.y;
+      }
     }
-    c0 += kLoads * kAtOnce;
-    if (c0 >= pieces) break;
+  };
+  const auto load_sums = [&](int c0, int group) {
 #pragma unroll
     for (int y = 0; y < kLoads; ++y) {
-      const int c = c0 + y * kAtOnce + slot;
+      const int c = c0 + y * split;
       x[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (slot < kAtOnce && c < pieces) x[y] = *reinterpret_cast<const f32x4*>(from + c * step * D);
+      if (c < pieces) x[y] = *part_sums<D>(a, part_of(a, c, rows32, kvh), group, lane);
     }
-  }
-  if constexpr (kAtOnce > 1) {
+  };
+  const int from = split == 1 ? 0 : wave, more = kLoads * split;
+  const int row = first + r < tile.to ? first + r : tile.to - 1;
+  const int token = tile.first + row / a.group, head = kvh * a.group + row % a.group;
+  const float v_mul = a.v_scale ? a.v_scale[kvh] : 1.0f;
+  load_weights(from);
+  load_sums(from, share * a.join_groups);
+  for (int group = share * a.join_groups, last = group + a.join_groups - 1;;) {
+    float m = -INFINITY, l = 0.0f;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    const auto add = [&](float m1, float l1, f32x4 x1, float base) {
+      const float f = __builtin_amdgcn_exp2f(m1 - base);
+      l += f * l1;
+      sum += f * x1;
+    };
+    const auto raise = [&](float higher) {
+      const float base = higher == -INFINITY ? 0.0f : higher, f = __builtin_amdgcn_exp2f(m - base);
+      l *= f;
+      sum *= f;
+      m = higher;
+      return base;
+    };
+    for (int c0 = from;;) {
+      float top = m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x = sum[i];
+      for (int y = 0; y < kLoads; ++y) top = fmaxf(top, pm[y]);
+      const float base = raise(top);
 #pragma unroll
-      for (int y = 1; y < kAtOnce; ++y) x += __shfl(sum[i], (lane + y * kLanes) & 63);
-      sum[i] = x;
+      for (int y = 0; y < kLoads; ++y) add(pm[y], pl[y], x[y], base);
+      c0 += more;
+      if (c0 >= pieces) break;
+      load_weights(c0);
+      load_sums(c0, group);
     }
-  }
-  if (slot > 0) return;
-  const float inv = (a.v_scale ? a.v_scale[head / a.group] : 1.0f) / l;
-  float out[4];
+    if (split > 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
-  store_n<4>((T*)a.out + token * a.ot + head * a.oh + d, out);
-  if (a.lse && d == 0) a.lse[at] = log_sum<T>(m, l);
+      for (int i = 0; i < 4; ++i) others[wave][i][lane] = sum[i];
+      others[wave][4][lane] = m;
+      others[wave][5][lane] = l;
+      mask::lds_barrier();
+      if (wave > 0) return;
+#pragma unroll
+      for (int y = 1; y < kJoinWaves; ++y) {
+        const float m1 = others[y][4][lane];
+        const f32x4 x1 = {others[y][0][lane], others[y][1][lane], others[y][2][lane],
+                          others[y][3][lane]};
+        add(m1, others[y][5][lane], x1, raise(fmaxf(m, m1)));
+      }
+    }
+    const float inv = v_mul / l;
+    float out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
+    if (first + r < tile.to) {
+      store_n<4>((T*)a.out + token * a.ot + head * a.oh + 8 * group + 4 * h, out);
+      if (a.lse && group == 0 && h == 0) a.lse[(int64_t)token * a.n_heads + head] = log_sum<T>(m, l);
+    }
+    if (group == last) break;
+    ++group;
+    if (pieces > more) load_weights(0);
+    load_sums(0, group);
+  }
 }
 
 template <class T, bool NARROW, int D, int W>
 void start(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
-  constexpr int kLds = 4 * Shape<T, NARROW, D>::kBuffer;
+  constexpr int kLds = 4 * Shape<T, NARROW, D, shared_keys(D)>::kBuffer;
   hipLaunchKernelGGL((chunk_kernel<T, NARROW, D, W>), dim3(blocks), dim3(64 * W), kLds, s, a);
 }
 
 template <class T, bool NARROW, int D>
 int launch(const ChunkArgs& a, unsigned blocks, hipStream_t s) {
-  if constexpr (!NARROW && D < 192) {
-    if (a.rows == rows_of(8))
-      start<T, NARROW, D, 8>(a, blocks, s);
-    else
-      start<T, NARROW, D, 4>(a, blocks, s);
-  } else {
+  if (a.rows == rows_of(4)) {
     start<T, NARROW, D, 4>(a, blocks, s);
+  } else if constexpr (D < 192) {
+    if (a.rows == kFewRows) {
+      constexpr int kLds = 8 * Shape<T, NARROW, D, 32>::kBuffer;
+      hipLaunchKernelGGL((chunk_few_kernel<T, NARROW, D>), dim3(blocks), dim3(256), kLds, s, a);
+    } else if constexpr (!NARROW) {
+      start<T, NARROW, D, 8>(a, blocks, s);
+    }
   }
   SPAX_HIP_CHECK(hipGetLastError());
   if (a.pieces > 1) {
-    const int64_t rows = (int64_t)a.n_tokens * a.n_heads;
-    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
+    const int64_t items = (int64_t)a.tiles * (a.rows / 32) * a.n_kv * (D / 8 / a.join_groups);
+    hipLaunchKernelGGL((chunk_join_kernel<T, D>), dim3((unsigned)(a.join_waves > 1 ? items : (items + kJoinWaves - 1) / kJoinWaves)),
                        dim3(64 * kJoinWaves), 0, s, a);
     SPAX_HIP_CHECK(hipGetLastError());
   }
@@ -793,6 +1038,16 @@ int launch_dim(const ChunkArgs& a, int dim, unsigned blocks, hipStream_t s) {
 
 }  // namespace
 
+// A tile of up to kWholeSteps steps stays whole: its pieces' way through memory and the second launch take
+// longer than the steps they save (1 x 509 tokens of 32 heads, nine steps: 25 us whole, 36 in
+// two).  Longer ones are cut down to kLeastSteps (1 x 5 over 8192: 24.2 us with six, 21.7 with four,
+// 21.0 with three, of which more join).  The same for tiles of few rows, whose steps are twice as long:
+// 1 x 509 17.1 us whole, 28.4 in two; 1 x 5 20.4 us down to two steps, 21.5 to four.
+constexpr int kWholeSteps = 12, kLeastSteps = 4, kFewWhole = 6, kFewLeast = 2;
+// Pieces of all tiles, those that a tile does not need included: their workgroups end at once, but 4096
+// took 61 us for 8 x 128 over 1000 where 2048 took 53.
+constexpr int64_t kMostPieces = 2048;
+
 ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   const spax_kv_cache& c = *a->cache;
   ChunkPlan p{};
@@ -802,30 +1057,43 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
     // every sequence with tokens has at most one tile that is not full
     return a->n_tokens * group / rows + (c.n_seqs < a->n_tokens ? c.n_seqs : a->n_tokens);
   };
-  // Eight waves that share a step's keys bring half as many in for a row as two workgroups of four, and
-  // have a unit to themselves (1 x 8192 of 16 bits: 657 us, 691 with four; 24 mixed 88 and 106), but
-  // widen 8-bit keys all at the same time (8 x 512 over 15872: 1755 and 1350), and want one
-  // workgroup for each unit (1 x 509 of 32 heads: 31 and 25).
-  const bool wide = c.type != SPAX_E4M3 && c.head_dim < 192 &&
-                    tiles(rows_of(8)) * c.n_kv_heads >= 256;
-  p.rows = rows_of(wide ? 8 : 4);
-  p.tiles = tiles(p.rows);
   int64_t keys = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->n_tokens < keys)
     keys = (int64_t)a->window + a->n_tokens;
-  const int64_t width = c.head_dim >= 192 ? 32 : 64;
+  // Tiles of 32 rows, whose four waves take a step's keys in turn, where larger ones would stay empty (64
+  // users' next token over 8192: 442 us, 567 in tiles of 128; 64 mixed of up to 256 tokens over
+  // 2048, 93 rows a sequence: 63 and 90; 24 mixed, 158 rows: 74 and 72; 8 x 32 over 4096, 128 rows:
+  // 59 and 49) or would not fill the units for long (1 x 509 of 32 heads: 17 and 25; 1 x 300 over 600:
+  // 30 and 42; 1 x 1024: 37 and 43; 4 x 512 over 1024: 107 and 75; 1 x 512 over 16000: 399 and 210).
+  const int64_t rows = a->n_tokens * group;
+  const bool few = c.head_dim < 192 && (rows <= (int64_t)96 * c.n_seqs ||
+                                        (keys <= 2048 && rows / rows_of(4) * c.n_kv_heads <= 256));
+  // Eight waves that share a step's keys bring half as many in for a row as two workgroups of four, and
+  // have a unit to themselves (1 x 8192 of 16 bits: 657 us, 691 with four; 24 mixed 88 and 106), but
+  // widen 8-bit keys all at the same time (8 x 512 over 15872: 1755 and 1350), and want one
+  // workgroup for each unit (1 x 512, without tiles of 32: 31 and 25).
+  const bool wide = !few && c.type != SPAX_E4M3 && c.head_dim < 192 &&
+                    tiles(rows_of(8)) * c.n_kv_heads >= 256;
+  p.rows = few ? kFewRows : rows_of(wide ? 8 : 4);
+  // as many as run at once (eight waves, with 512 for 256: 4 x 512 over 1024 97 for 75 us; four waves,
+  // with 256 for 512: 8 x 32 over 4096 58 for 49)
+  p.shares = wide ? 256 : 512;
+  p.tiles = tiles(p.rows);
+  p.key_shift = few ? kFewShift : c.head_dim >= 192 ? 5 : 6;
+  p.whole_steps = few ? kFewWhole : kWholeSteps;
+  const int64_t least = few ? kFewLeast : kLeastSteps;
+  const int64_t width = (int64_t)1 << p.key_shift;
   const int64_t steps = (keys + width - 1) / width + 1;  // a window starts anywhere
   const int64_t items = p.tiles * c.n_kv_heads;
-  int64_t pieces = 2048 / items;
-  if (pieces > steps / kLeastSteps) pieces = steps / kLeastSteps;
-  if (steps <= kWholeSteps) pieces = 1;
+  int64_t pieces = kMostPieces / items;
+  if (pieces > steps / least) pieces = steps / least;
+  if (steps <= p.whole_steps) pieces = 1;
   pieces = pieces < 1 ? 1 : pieces > 64 ? 64 : pieces;
   p.least_steps = (int32_t)((steps + pieces - 1) / pieces);
   p.pieces = (int32_t)((steps + p.least_steps - 1) / p.least_steps);
   p.blocks = items * p.pieces;
   if (p.pieces > 1)
-    p.ws_bytes = aligned_size((size_t)p.pieces * a->n_tokens * a->n_heads *
-                              ((size_t)c.head_dim + 2) * sizeof(float));
+    p.ws_bytes = aligned_size((size_t)(items * p.pieces) * p.rows * (c.head_dim + 2) * sizeof(float));
   return p;
 }
 
@@ -847,9 +1115,14 @@ int launch_chunk_attention(const spax_chunk_attention_args* p, void* ws, hipStre
   a.page_shift = __builtin_ctz((unsigned)c.page_size);
   a.max_len = p->max_len; a.window = p->window; a.scale = p->scale;
   a.rows = plan.rows; a.tiles = (int32_t)plan.tiles; a.pieces = plan.pieces;
-  a.least_steps = plan.least_steps;
+  a.least_steps = plan.least_steps; a.whole_steps = plan.whole_steps; a.key_shift = plan.key_shift; a.shares = plan.shares;
   a.part_o = (float*)ws;
-  a.part_ml = (float*)ws + (size_t)plan.pieces * p->n_tokens * p->n_heads * c.head_dim;
+  a.part_ml = (float*)ws + (size_t)plan.blocks * plan.rows * c.head_dim;
+  // (32 pieces of 1 x 5 over 8192: 5.9 us by four waves, 10.8 by one)
+  a.join_waves = plan.pieces > 16 ? kJoinWaves : 1;
+  a.join_groups = a.join_waves == 1 && plan.tiles * (plan.rows / 32) * c.n_kv_heads * (c.head_dim / 8) > 8192
+                      ? 4
+                      : 1;
   const unsigned blocks = (unsigned)plan.blocks;
   if (c.type == SPAX_E4M3)
     return p->type == SPAX_F16 ? launch_dim<f16, true>(a, c.head_dim, blocks, s)

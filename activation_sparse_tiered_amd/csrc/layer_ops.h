@@ -51,7 +51,8 @@ AttentionPlan attention_plan(const spax_attention_args* a);
 struct ChunkPlan {
   int32_t rows;  // of a tile
   int64_t tiles;
-  int32_t pieces, least_steps;
+  int32_t key_shift;  // a step is 2^key_shift keys
+  int32_t pieces, least_steps, whole_steps, shares;
   int64_t blocks;
   size_t ws_bytes;
 };

@@ -256,6 +256,27 @@ def test_chunk_attention(env, case, far):  # noqa: F811
     _chunk_check(q, kc, vc, table, starts, ln, scales, out, lse, dim, qt, window, max_len)
 
 
+# more rows for each sequence than small tiles are for, and tables with room for more keys: tiles of 128
+# rows, and with 32 key heads of 256
+BIG = [
+    ([(100, 0), (130, 1500), (101, 37)], 2, 1, 128, 16, "fp16", "fp16", 0, "heads", None),
+    ([(100, 0), (130, 1500), (101, 37)], 6, 2, 96, 16, "bf16", "e4m3", 0, "tokens", None),
+    ([(140, 900), (300, 0)], 4, 2, 128, 32, "fp16", "e4m3", 0, "heads", None),
+    ([(140, 900), (300, 0), (0, 70)], 4, 2, 64, 4, "bf16", "bf16", 700, "heads", None),
+    ([(130, 1100), (200, -40)], 2, 2, 192, 16, "fp16", "fp16", 0, "heads", None),
+    ([(130, 1100), (200, -40)], 2, 2, 256, 16, "bf16", "e4m3", 0, "heads", None),
+    ([(100, 30)] * 6 + [(130, 0), (97, 3000)], 32, 32, 64, 16, "bf16", "bf16", 0, "heads", None),
+    ([(100, 100)] * 4 + [(257, 0), (120, 2500)], 32, 32, 128, 16, "fp16", "fp16", 0, "tokens", None),
+    ([(100, 100)] * 4 + [(257, 0), (120, 2500)], 32, 32, 96, 64, "fp16", "fp16", 300, "heads", None),
+]
+
+
+@pytest.mark.parametrize("case", BIG, ids=[f"{i}-{c[1]}-{c[2]}-{c[3]}-{c[5]}-{c[6]}"
+                                           for i, c in enumerate(BIG)])
+def test_chunk_attention_in_large_tiles(env, case):  # noqa: F811
+    test_chunk_attention(env, case, True)
+
+
 def test_chunk_many_sequences(env):  # noqa: F811
     """More sequences than a wave has lanes, most of one token, some of none."""
     torch, spax, dev = env
@@ -367,12 +388,13 @@ def _chunk_call(env, q, cache, starts, ln, **kw):
 
 @pytest.mark.parametrize("far", [False, True], ids=["whole", "pieces"])
 @pytest.mark.parametrize("page", [4, 16, 64])
-def test_chunk_pages_that_are_not_there(env, page, far):  # noqa: F811
+@pytest.mark.parametrize("rows,dim", [(70, 64), (170, 64), (70, 96), (170, 96)])
+def test_chunk_pages_that_are_not_there(env, page, far, rows, dim):  # noqa: F811
     """Entries that name no page, in the middle, at the beginning and for all of a token's keys: those
     keys are left out, and a token without any gives zeros and -inf."""
     torch, spax, dev = env
-    sizes = [(70, 300), (5, 0), (3, 200)]
-    q, kc, vc, table, starts, ln, scales = _chunk_inputs(env, sizes, 4, 2, 64, page, "fp16", "fp16",
+    sizes = [(rows, 300), (5, 0), (3, 200)]
+    q, kc, vc, table, starts, ln, scales = _chunk_inputs(env, sizes, 4, 2, dim, page, "fp16", "fp16",
                                                          "heads", 13)
     kc.masked_fill_(torch.isnan(kc), 7.0)
     for s, at in ((0, 100), (0, 260), (0, 345), (2, 0)):
@@ -383,7 +405,7 @@ def test_chunk_pages_that_are_not_there(env, page, far):  # noqa: F811
         wide[:, :table.shape[1]] = table
         table = wide
     out, lse = _chunk_call(env, q, spax.make_kv_cache(kc, vc, table), starts, ln)
-    _chunk_check(q, kc, vc, table, starts, ln, scales, out, lse, 64, "fp16", 0, None)
+    _chunk_check(q, kc, vc, table, starts, ln, scales, out, lse, dim, "fp16", 0, None)
     first = int(starts[1])
     assert not bool(out[first:first + 5].any()) and bool((lse[first:first + 5] == -float("inf")).all())
 
