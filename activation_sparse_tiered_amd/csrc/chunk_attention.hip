@@ -1083,7 +1083,7 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   p.whole_steps = few ? kFewWhole : kWholeSteps;
   const int64_t least = few ? kFewLeast : kLeastSteps;
   const int64_t width = (int64_t)1 << p.key_shift;
-  const int64_t steps = (keys + width - 1) / width + 1;  // a window starts anywhere
+  const int64_t steps = (keys + width - 1) / width + (a->window > 0);  // a window starts anywhere
   const int64_t items = p.tiles * c.n_kv_heads;
   int64_t pieces = kMostPieces / items;
   if (pieces > steps / least) pieces = steps / least;

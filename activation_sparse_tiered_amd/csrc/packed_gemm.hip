@@ -95,20 +95,32 @@ __device__ inline void finish(const GemmArgs& a, int m, int col, f32x4 t0, f32x4
 }
 
 // Two int4 values of one column (k and k + 1) as fp16, from words whose low and high halves hold them
-// at bit 4 i: 0x6400 | q is 1024 + q, and the multiply-add rounds s q + z once.  The constants are
-// hidden in registers, where an and and an or become one instruction.
+// at bit 4 i: 0x6400 | q is 1024 + q, with q one place higher 1024 + 16 q, and the multiply-add rounds
+// s q + z once.  The constants are hidden in registers, where an and and an or become one
+// instruction.
 struct Widen {
-  uint32_t mask, magic;
-  __device__ inline Widen() : mask(0x000f000fu), magic(0x64006400u) {
-    asm("" : "+v"(mask));
+  uint32_t low, high, magic;
+  __device__ inline Widen() : low(0x000f000fu), high(0x00f000f0u), magic(0x64006400u) {
+    asm("" : "+v"(low));
+    asm("" : "+v"(high));
     asm("" : "+s"(magic));
   }
   __device__ inline uint32_t two(uint32_t u, int i, f16x2 s, f16x2 z) const {
-    const uint32_t q = ((u >> (4 * i)) & mask) | magic;
-    const f16x2 v = __builtin_bit_cast(f16x2, q) - f16x2{(f16)1024.0f, (f16)1024.0f};
+    const uint32_t w = i < 2 ? u : u >> 8;
+    f16x2 v = __builtin_bit_cast(f16x2, (w & (i % 2 ? high : low)) | magic);
+    if (i % 2)
+      v = __builtin_elementwise_fma(v, f16x2{(f16)0.0625f, (f16)0.0625f}, f16x2{(f16)-64.0f, (f16)-64.0f});
+    else
+      v -= f16x2{(f16)1024.0f, (f16)1024.0f};
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, s, z));
   }
 };
+
+// Lane L's value, of each 16 lanes.
+template <int L>
+__device__ inline f16x2 from_lane(uint32_t v) {
+  return __builtin_bit_cast(f16x2, __builtin_amdgcn_update_dpp(0u, v, 0x150 + L, 0xf, 0xf, true));
+}
 
 // 32 rows, 256 columns; the workgroup's waves take every kWaves-th step of its k.
 template <bool INT4>
@@ -122,7 +134,7 @@ struct Few {
   struct Step {
     u32x4 x;
     u32x4 w[INT4 ? 1 : 8];
-    uint32_t q[INT4 ? 8 : 1], sz[INT4 ? 8 : 1];
+    uint32_t q[INT4 ? 8 : 1], sz;  // sz: of record lane % 8 of the lane's eight
   };
 };
 
@@ -144,7 +156,8 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
   const int col = has_col(a, c_tile, half, at) ? first_col(a, c_tile, half) + at : 0;
   // Addresses are a uniform part and 32 bits of the lane's own (8 records are below 2^28 bytes).
   const uint32_t w_at = 8u * h * (uint32_t)a.w_stride + (INT4 ? (uint32_t)col / 2 : 2u * col);
-  const uint32_t sz_at = 8u * h * (uint32_t)a.w_stride + (uint32_t)a.n / 2 + (uint32_t)col / 128 * 4;
+  const uint32_t sz_at = (8u * h + (lane & 7)) * (uint32_t)a.w_stride + (uint32_t)a.n / 2 +
+                         (uint32_t)col / 128 * 4;
   const int m0 = 32 * m_tile;
   const int64_t x_at = (int64_t)(m0 + r < a.rows ? m0 + r : a.rows - 1) * a.xs + 8 * h;
   const auto load = [&](typename F::Step& z, int step) {
@@ -153,11 +166,11 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
       const f16* x = a.x + k0;
       const uint8_t* rec = a.w + (int64_t)k0 * a.w_stride;
       z.x = *reinterpret_cast<const u32x4*>(x + x_at);
+      if constexpr (INT4) z.sz = *reinterpret_cast<const uint32_t*>(rec + sz_at);
 #pragma unroll
       for (int e = 0; e < 8; ++e, rec += a.w_stride) {
         if constexpr (INT4) {
           z.q[e] = *reinterpret_cast<const uint32_t*>(rec + w_at);
-          z.sz[e] = *reinterpret_cast<const uint32_t*>(rec + sz_at);
         } else {
           z.w[e] = *reinterpret_cast<const u32x4*>(rec + w_at);
         }
@@ -170,12 +183,16 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
       for (int i = 0; i < 4; ++i)
         v[i] &= 2 * i + 1 < valid ? ~0u : 2 * i < valid ? 0xffffu : 0u;
       z.x = v;
+      const auto record = [&](int e) {
+        return a.w + (int64_t)(e < valid ? k0 + 8 * h + e : a.k - 1) * a.w_stride;
+      };
+      if constexpr (INT4)
+        z.sz = *reinterpret_cast<const uint32_t*>(record(lane & 7) + a.n / 2 + col / 128 * 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint8_t* rec = a.w + (int64_t)(e < valid ? k0 + 8 * h + e : a.k - 1) * a.w_stride;
+        const uint8_t* rec = record(e);
         if constexpr (INT4) {
           z.q[e] = *reinterpret_cast<const uint32_t*>(rec + col / 2);
-          z.sz[e] = *reinterpret_cast<const uint32_t*>(rec + a.n / 2 + col / 128 * 4);
         } else {
           z.w[e] = *reinterpret_cast<const u32x4*>(rec + 2 * (int64_t)col);
         }
@@ -194,11 +211,14 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
       for (int p = 0; p < 4; ++p) {
         lo[p] = __builtin_amdgcn_perm(z.q[2 * p + 1], z.q[2 * p], 0x05040100u);
         hi[p] = __builtin_amdgcn_perm(z.q[2 * p + 1], z.q[2 * p], 0x07060302u);
-        s[p] = __builtin_bit_cast(
-            f16x2, __builtin_amdgcn_perm(z.sz[2 * p + 1], z.sz[2 * p], 0x05040100u));
-        zero[p] = __builtin_bit_cast(
-            f16x2, __builtin_amdgcn_perm(z.sz[2 * p + 1], z.sz[2 * p], 0x07060302u));
       }
+      // scales and zeros of two records, from their lanes
+      const uint32_t up = __builtin_amdgcn_update_dpp(0u, z.sz, 0x101, 0xf, 0xf, true);  // lane + 1's
+      const uint32_t ss = __builtin_amdgcn_perm(up, z.sz, 0x05040100u);
+      const uint32_t zz = __builtin_amdgcn_perm(up, z.sz, 0x07060302u);
+      s[0] = from_lane<0>(ss); s[1] = from_lane<2>(ss); s[2] = from_lane<4>(ss); s[3] = from_lane<6>(ss);
+      zero[0] = from_lane<0>(zz); zero[1] = from_lane<2>(zz);
+      zero[2] = from_lane<4>(zz); zero[3] = from_lane<6>(zz);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -222,13 +242,12 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
 #pragma unroll
   for (int y = 0; y < F::kAhead; ++y)
     if (s + y * F::kWaves < stop) load(z[y], s + y * F::kWaves);
-  for (; s < stop; s += F::kWaves) {
-    typename F::Step next = z[F::kAhead - 1];
-    if (s + F::kAhead * F::kWaves < stop) load(next, s + F::kAhead * F::kWaves);
-    use(z[0]);
+  for (; s < stop; s += F::kAhead * F::kWaves) {
 #pragma unroll
-    for (int y = 0; y + 1 < F::kAhead; ++y) z[y] = z[y + 1];
-    z[F::kAhead - 1] = next;
+    for (int y = 0; y < F::kAhead; ++y) {
+      if (s + y * F::kWaves < stop) use(z[y]);
+      if (s + (y + F::kAhead) * F::kWaves < stop) load(z[y], s + (y + F::kAhead) * F::kWaves);
+    }
   }
 
   // Join the waves, half of the rows at a time.  A lane has row r, and of register i of every operand
