@@ -649,6 +649,11 @@ LARGE = [
     (1000, 4100, [4032], "fp16", "act", "gelu", True, "bf16", "bf16", 1.0),
     (3001, 190, [4352], "int4", "plain", "silu", True, None, "fp16", 1.0),
     (1000, 3000, [2048, 2048], "int4", "gated", "silu", False, None, "fp16", 1.0),
+    # k in pieces between tiles of 64 and of 128 rows
+    (64, 2000, [2176, 2176], "fp16", "gated", "silu", True, "bf16", "fp16", 1.0),
+    (40, 8001, [12032], "int4", "plain", "silu", True, None, "fp16", 1.0),
+    (120, 4100, [10240, 10240], "fp16", "gated", "gelu", False, None, "bf16", 1.0),
+    (120, 4100, [20480], "int4", "plain", "silu", False, "fp32", "fp32", 1.0),
 ]
 
 
