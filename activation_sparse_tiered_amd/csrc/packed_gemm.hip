@@ -432,51 +432,77 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
   for (int f = 0; f < 2; ++f)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[f][t] = f32x16{};
-  const auto multiply = [&](int step) {
+  // The operands of 16 k, and the products with them.
+  u32x4 x[2][TT], w[2][2];
+  const auto read = [&](int step, int c) {
     const uint8_t* xs = stages + (step & 1) * M::kStage;
     const uint8_t* ws = xs + M::kX;
-    u32x4 x[2][TT], w[2][2];
-    const auto read = [&](int c) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int i = lane & 15, g = lane >> 4;
-        const int row = 16 * c + 8 * (g >> 1) + (i >> 2);
-        const int piece = 16 * f + 4 * wn + 2 * (g & 1) + ((i & 3) >> 1);
-        const uint8_t* p = ws + row * (2 * kCols) + 16 * M::w_place(row, piece) + 8 * (i & 1);
-        const u32x2 lo = read_turned(p), hi = read_turned(p + 4 * 2 * kCols);
-        w[c & 1][f] = u32x4{lo.x, lo.y, hi.x, hi.y};
-      }
+    for (int f = 0; f < 2; ++f) {
+      const int i = lane & 15, g = lane >> 4;
+      const int row = 16 * c + 8 * (g >> 1) + (i >> 2);
+      const int piece = 16 * f + 4 * wn + 2 * (g & 1) + ((i & 3) >> 1);
+      const uint8_t* p = ws + row * (2 * kCols) + 16 * M::w_place(row, piece) + 8 * (i & 1);
+      const u32x2 lo = read_turned(p), hi = read_turned(p + 4 * 2 * kCols);
+      w[c & 1][f] = u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int row = 32 * (wm * TT + t) + r;
-        x[c & 1][t] = *reinterpret_cast<const u32x4*>(xs + row * (2 * M::kDepth) +
-                                                      16 * M::x_place(row, 2 * c + h));
-      }
-    };
-    read(0);
-#pragma unroll
-    for (int c = 0; c < M::kDepth / 16; ++c) {
-      if (c + 1 < M::kDepth / 16) read(c + 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              __builtin_bit_cast(f16x8, w[c & 1][f]), __builtin_bit_cast(f16x8, x[c & 1][t]),
-              acc[f][t], 0, 0, 0);
+    for (int t = 0; t < TT; ++t) {
+      const int row = 32 * (wm * TT + t) + r;
+      x[c & 1][t] = *reinterpret_cast<const u32x4*>(xs + row * (2 * M::kDepth) +
+                                                    16 * M::x_place(row, 2 * c + h));
     }
   };
-  if (first < stop) {
-    load(first);
-    lay_out(first);
-  }
-  for (int step = first; step < stop; ++step) {
+  const auto multiply = [&](int c) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+        acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            __builtin_bit_cast(f16x8, w[c & 1][f]), __builtin_bit_cast(f16x8, x[c & 1][t]),
+            acc[f][t], 0, 0, 0);
+  };
+  constexpr int kChunks = M::kDepth / 16;
+  load(first);
+  lay_out(first);
+  if constexpr (INT4) {
+    // The waves meet before the last products of a step, when it has been read and the next one is laid
+    // out, so that these run while the next step's first operands come (4096 x 22016 842 us, 894
+    // when they meet between steps; fp16, which lays nothing out, 787 and 784).  After the last step
+    // they lay out and read once more what nothing uses.
     wait_loads();
-    mask::lds_barrier();  // this stage is laid out, the other one has been read
-    if (step + 1 < stop) load(step + 1);
-    multiply(step);
-    if (step + 1 < stop) lay_out(step + 1);
+    mask::lds_barrier();
+    read(first, 0);
+    if (first + 1 < stop) load(first + 1);
+    for (int step = first; step < stop; ++step) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c + 1 < kChunks) {
+          read(step, c + 1);
+        } else {
+          lay_out(step + 1);
+          wait_loads();
+          mask::lds_barrier();
+          read(step + 1, 0);
+          if (step + 2 < stop) load(step + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(c);
+      }
+    }
+  } else {
+    for (int step = first; step < stop; ++step) {
+      wait_loads();
+      mask::lds_barrier();  // this stage is laid out, the other one has been read
+      if (step + 1 < stop) load(step + 1);
+      read(step, 0);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c + 1 < kChunks) read(step, c + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(c);
+      }
+    }
   }
 
   // The sums go to their rows through LDS, half of the rows at a time.
