@@ -1,23 +1,34 @@
 // spax_chunk_attention: a chunk of new query tokens per sequence over a paged cache, causal.
 //
 // A sequence's query rows for one key head, tokens times the group's heads, are laid end to end and
-// cut into tiles of 128, so any group fills them.  Per row with keys k_j, values v_j, in one pass:
+// cut into tiles, so any group fills them.  Per row with keys k_j, values v_j, in one pass:
 //   s_j = scale q.k_j,  m = running max of s,  p = exp(s - m),
 //   l <- l exp(m_old - m) + sum p,   o <- o exp(m_old - m) + sum p v,   out = o / l.
 // Pieces of a tile's keys (m, l, o) join by the same rule.
 //
-// A workgroup of four waves takes a tile, 32 rows a wave, and walks over its keys, kKeys at a time,
-// which pass through LDS once for all four:
+// A wave has 32 rows.  Four or eight of them take a tile of 128 or 256 rows and walk over its keys a step
+// at a time, which pass through LDS once for all (chunk_kernel); or four share the 32 rows of a small
+// tile, each with its own keys (chunk_few_kernel); chunk_plan says when.
 //   * S^T = K Q^T by 32x32x16 matrix instructions, keys as rows, query rows as columns.
 //   * S^T's layout (lane: one row, keys 8 b + 4 h + i) is that of the second product's P operand if
 //     that product counts keys in the order {4 h + i, 8 + 4 h + i} of every 16, so probabilities
 //     never cross lanes and a row's maximum and sum are in two lanes.
 //   * O^T = V^T P^T: eight keys of one dim come from LDS by transposing reads of four rows.
-//   * p enters the product as one 16-bit value, in fp16 lifted by 2^15 (Mma::kLift): splitting it
-//     in two, as the attention of single tokens does, would add half of the matrix work again where
-//     that is the bound, for an error that is about that of rounding the result.
-//   * Masked keys get p = 0, but 0 * inf is NaN: in tiles that some row does not see whole, values
-//     that are not finite are taken out of the product and counted apart (see take_values).
+//   * p enters the product as one 16-bit value, in fp16 lifted by 2^14 (Soft): splitting it in two, as
+//     the attention of single tokens does, would add half of the matrix work again where that is the
+//     bound, for an error that is about that of rounding the result.
+//   * The maximum is raised only where a score is kSlack above it: most steps leave o as it is.
+//   * Masked keys get p = 0, but 0 * inf is NaN: in steps that some row does not see whole, values
+//     that are not finite are zeroed in LDS and noted for the rows that see them (note_odd).
+//
+// What bounds it.  Many rows and keys: matrix instructions are under way for 0.43 of the SIMDs'
+// cycles (counters; 0.38 from e4m3), vector instructions, the exponentials above all, for 0.48, and
+// the two overlap in part only, with two waves on a SIMD: 1 x 8192 of 32 heads on 8, fp16, 597 us,
+// 922 TFLOP/s; 8 x 512 over 15872 from e4m3 1226 us, 883 TFLOP/s; a large library product reaches
+// 1400.  Two tiles of rows per wave, which would share its reads of keys and values, spilled (908 us
+// for 620 then); scores of the next step between the products of this one 722 us.  Few rows: the
+// chain starts, table, keys, two products, join, second launch, 20.5 us for 1 x 5 over 8192, of
+// which the keys' 33.6 MB need 4.7.
 #include "attn_core.h"
 #include "layer_ops.h"
 #include "mask_core.h"
@@ -203,7 +214,7 @@ __device__ inline void load_lds(const void* from, const void* to) {
 __device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 
 // Brings a step's keys and values into LDS.  16-bit rows go there straight from memory, 8-bit ones
-// through registers, where they are widened once for all four waves.
+// through registers, where they are widened once for all of its waves.
 template <class T, bool NARROW, int D, int KEYS, int W>
 struct Loader {
   using S = Shape<T, NARROW, D, KEYS>;
@@ -713,7 +724,9 @@ __device__ inline void wait_loads_but() {
 __device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
 // A tile of 32 rows: its four waves take 32 keys of each step of 128, bring them in by themselves, without
-// a barrier, and join at the end.
+// a barrier, and join at the end.  The next keys are asked for as soon as this step's have been read,
+// and so are values, so one buffer of each does and two workgroups fit a unit (1 x 509 of 32 heads,
+// fp16: 17.3 us, 25.4 in tiles of 128 rows).
 constexpr int kFewRows = 32, kFewShift = 7;
 template <class T, bool NARROW, int D>
 __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {

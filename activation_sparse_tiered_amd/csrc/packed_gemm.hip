@@ -3,9 +3,23 @@
 //   t[m][n] = sum_k x[m][k] W[k][n] + bias[n];  u = t, act(t) or act(t_0) t_1;  y = r + scale u.
 //
 // The blob holds W by input channel: record k has all n side by side, while a matrix instruction
-// wants eight k of one n in a lane.  So a lane reads eight n of each of its eight k and turns the
-// block within its registers: operand j of the eight is value j of every k, and row i of
-// operand j stands for column 8 i + j.
+// wants eight k of one n in a lane.  Tiles of 32 rows (gemm_few_kernel) turn them in registers: a lane
+// reads eight n of each of its eight k, operand j of the eight is value j of every k, and row i of
+// operand j stands for column 8 i + j.  Larger ones (gemm_many_kernel) stage x and W in LDS for eight
+// waves and read W by transposing reads.  A workgroup has 256 columns, with GATED 128 of each matrix, so
+// the gate is applied where the sums are.  Where tiles are few, k is cut into pieces whose sums
+// (fp32) a second launch adds in order: results depend on the sizes alone.
+//
+// int4 weights become w_hat rounded to fp16 (one multiply-add of 16 bits per pair): half of a step of
+// 2^-11 of each weight, which is what an fp16 base loses when it is packed; sums are in fp32.
+//
+// What bounds it (us of calls back to back, the weights in memory).  Many rows: 4096 x 4096 x 22016
+// fp16 752, 982 TFLOP/s (a large library product reaches 1400), int4 803, 920: matrix
+// instructions are under way in 0.52 of the SIMDs' cycles, the rest are LDS reads (6 KB for every eight
+// of them) and the step's barrier; a wave with 128 x 128 sums would read a third less and needs all
+// of its SIMD's registers.  Few rows: 5 x 4096 x 12288 fp16 23.9, of which the first launch takes 19
+// (100 MB at 5.3 TB/s) and the join 4; 61 x 11008 x 4096 int4 21.0, of which 17 and 4: vector
+// instructions, most of them to widen the codes once for every 32 rows, fill half of the cycles.
 #include "act.h"
 #include "layer_ops.h"
 #include "mask_core.h"
@@ -593,15 +607,16 @@ int launch_many(const GemmArgs& a, unsigned blocks, hipStream_t s) {
 
 // The tile and the splits of k by what they are expected to take, in us, with one workgroup on each of 256
 // compute units: rounds of workgroups, their steps, and where k is split the sums' way through
-// memory and a second launch.  The times of a step are fitted to 66 products of each base, with the
-// weights in memory and not in a cache: what they choose took 0.5% (fp16) and 0.2% (int4) longer
-// than the best tile of all four, at most 8%.  Best of each, us, tiles of 32, 64, 128 and 256 rows:
-//   4096 x 22016 fp16, 5 rows     73.9   75.4   76.9      -
-//   4096 x 22016 fp16, 64 rows    88.5   78.4   79.6      -
-//   4096 x 22016 fp16, 128 rows  126.3  107.7   84.1      -
-//   4096 x 22016 fp16, 512 rows      -  193.7  198.1  134.6
-//   4096 x 22016 int4, 5 rows     38.6   56.5   61.4      -
-//   4096 x 22016 int4, 128 rows   89.4   88.4   72.2      -
+// memory and a second launch.  The times of a step are fitted to 70 products of each base, each with
+// as many blobs in turn as keep the weights out of the caches: what they choose took 0.8% (fp16) and
+// 0.3% (int4) longer on average than the best tile of all four.  Some of them, us, tiles of 32, 64, 128 and
+// 256 rows:
+//   4096 x 22016 fp16, 5 rows     39.1   49.4   51.3      -
+//   4096 x 22016 fp16, 64 rows    60.7   54.1   55.4      -
+//   4096 x 22016 fp16, 128 rows   96.2   81.9   61.2      -
+//   4096 x 22016 fp16, 512 rows      -  163.9  162.9  123.0
+//   4096 x 22016 int4, 5 rows     24.3   44.1   48.1      -
+//   4096 x 22016 int4, 128 rows   79.9   80.6   61.3      -
 GemmPlan gemm_plan(const spax_packed_gemm_args* a) {
   const spax_layout& L = *a->layout;
   // a tile's rows, k of a step of the workgroup, its time, fewest steps of a split
@@ -611,8 +626,8 @@ GemmPlan gemm_plan(const spax_packed_gemm_args* a) {
     int32_t least;
   };
   static const Kind kinds[2][4] = {
-      {{32, 128, 1.65f, 2}, {64, 64, 0.87f, 4}, {128, 64, 1.10f, 4}, {256, 64, 1.25f, 4}},
-      {{32, 128, 1.00f, 2}, {64, 64, 1.05f, 4}, {128, 64, 1.40f, 4}, {256, 64, 1.55f, 4}}};
+      {{32, 128, 2.20f, 2}, {64, 64, 1.21f, 4}, {128, 64, 1.50f, 4}, {256, 64, 2.03f, 4}},
+      {{32, 128, 1.15f, 2}, {64, 64, 1.13f, 4}, {128, 64, 1.25f, 4}, {256, 64, 1.45f, 4}}};
   const bool gated = a->form == SPAX_GEMM_GATED;
   GemmPlan best{};
   if (a->n_rows < 1) return best;
