@@ -209,7 +209,7 @@ __device__ inline void load_lds(const void* from, const void* to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(at), "v"(from)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 

@@ -17,8 +17,8 @@
 // fp16 752, 982 TFLOP/s (a large library product reaches 1400), int4 803, 920: matrix
 // instructions are under way in 0.52 of the SIMDs' cycles, the rest are LDS reads (6 KB for every eight
 // of them) and the step's barrier; a wave with 128 x 128 sums would read a third less and needs all
-// of its SIMD's registers.  Few rows: 5 x 4096 x 12288 fp16 23.9, of which the first launch takes 19
-// (100 MB at 5.3 TB/s) and the join 4; 61 x 11008 x 4096 int4 21.0, of which 17 and 4: vector
+// of its SIMD's registers.  Few rows: 5 x 4096 x 12288 fp16 23.9, of which the first launch takes 20
+// (100 MB at 5 TB/s) and the join 4; 61 x 11008 x 4096 int4 21.0, of which 17 and 4: vector
 // instructions, most of them to widen the codes once for every 32 rows, fill half of the cycles.
 #include "act.h"
 #include "layer_ops.h"
@@ -314,7 +314,7 @@ __device__ inline void load_lds(const void* from, const void* to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(at), "v"(from)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 

@@ -622,7 +622,7 @@ int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes
  *             with strides a multiple of 8 elements.
  *   lse    : n_tokens * n_heads, may be NULL.
  * Probabilities enter the product with v as one `type` value (spax_paged_attention's as two): within
- * 2^-9 of themselves in BF16, and in F16 within 2^-12 of themselves or 2^-39 of the row's largest.
+ * 2^-8 of themselves in BF16, and in F16 within 2^-11 of themselves or 2^-39 of the row's largest.
  *   max_len : host bound on lens; with n_tokens it sets how the keys are shared out.
  *   ws      : spax_chunk_attention_workspace_bytes(a) bytes (0: none needed), 256-byte aligned,
  *             any contents; calls that may run at the same time need a workspace each.
