@@ -268,6 +268,9 @@ BIG = [
     ([(100, 30)] * 6 + [(130, 0), (97, 3000)], 32, 32, 64, 16, "bf16", "bf16", 0, "heads", None),
     ([(100, 100)] * 4 + [(257, 0), (120, 2500)], 32, 32, 128, 16, "fp16", "fp16", 0, "tokens", None),
     ([(100, 100)] * 4 + [(257, 0), (120, 2500)], 32, 32, 96, 64, "fp16", "fp16", 300, "heads", None),
+    # more pieces than are joined at once, of small tiles and of large ones
+    ([(3, 12000)], 1, 1, 64, 16, "fp16", "fp16", 0, "heads", None),
+    ([(130, 12000)], 1, 1, 128, 16, "bf16", "bf16", 0, "heads", None),
 ]
 
 
@@ -295,16 +298,17 @@ def test_chunk_many_sequences(env):  # noqa: F811
 
 @pytest.mark.parametrize("kind", ["fp16", "bf16", "e4m3"])
 @pytest.mark.parametrize("far", [False, True], ids=["whole", "pieces"])
-def test_chunk_later_tokens_hold_anything(env, kind, far):  # noqa: F811
+@pytest.mark.parametrize("others", [0, 3])
+def test_chunk_later_tokens_hold_anything(env, kind, far, others):  # noqa: F811
     """NaN and infinities in keys and values of tokens that a row does not see change nothing for it;
     rows that see them get what the formula gives."""
     torch, spax, dev = env
     ct = kind
     qt = "bf16" if kind == "bf16" else "fp16"
-    sizes = [(100, 30)]
+    sizes = [(100, 30)] + [(0, 1)] * others      # fewer rows for each sequence: small tiles
     q, kc, vc, table, starts, ln, scales = _chunk_inputs(env, sizes, 2, 1, 64, 16, qt, ct, "heads", 3)
     if far:
-        wide = torch.full((1, 1000), -1, dtype=torch.int32, device=dev)
+        wide = torch.full((1 + others, 1000), -1, dtype=torch.int32, device=dev)
         wide[:, :table.shape[1]] = table
         table = wide
     cache = spax.make_kv_cache(kc, vc, table, *scales)
