@@ -274,7 +274,8 @@ int spax_tiered_gemv(const spax_layout* L, const void* packed, const uint16_t* x
   GemvPlan plan;
   int st = check_gemv_args(L, packed, x, full_idx, approx_idx, counts, y, ws, ws_bytes, &plan);
   if (st) return st;
-  return launch_tiered_gemv(L, plan, packed, x, full_idx, approx_idx, counts, y, false, stream);
+  return launch_tiered_gemv(L, plan, packed, x, full_idx, approx_idx, counts, y, false, stream,
+                            Lists::kCaller);
 }
 
 int spax_column_ranges(const int32_t* idx, int32_t n, int32_t gap, int32_t* first,

@@ -105,6 +105,7 @@ template <int FMT, class Blob>
 __global__ __launch_bounds__(kGemvThreads) void batched_gemv_kernel(const GemvDesc* __restrict__ gd,
                                                                     int n_phases, int n_items) {
   __shared__ float red[gemv::kWaves * gemv::ItemRows<FMT>::tile];
+  // (a phase's lists hold d_in entries, as the mask kernel wrote them)
   // Item i runs on XCD i % 8 (the grid is a multiple of 8 or holds one item per
   // workgroup), so the XCD-aware order applies to the item index.  Only the speed depends on
   // this: the order is a bijection whatever the grid.
@@ -115,7 +116,8 @@ __global__ __launch_bounds__(kGemvThreads) void batched_gemv_kernel(const GemvDe
     const int local = item - g.item0;
     const int tile = (int)((uint32_t)local % (uint32_t)g.sh.n_tiles);
     const int chunk = (int)((uint32_t)local / (uint32_t)g.sh.n_tiles);
-    gemv::gemv_item<FMT, Blob, false, gemv::ItemRows<FMT>::rpl, gemv::ItemRows<FMT>::unroll>(
+    gemv::gemv_item<FMT, Blob, false, true, gemv::ItemRows<FMT>::rpl,
+                    gemv::ItemRows<FMT>::unroll>(
         g.sh, g.packed, g.x32, g.full_idx, g.approx_idx, g.counts, g.y, tile, chunk, red);
     __syncthreads();  // red is reused by the next item
   }

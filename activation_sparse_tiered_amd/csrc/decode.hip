@@ -541,7 +541,7 @@ int launch_decode_step(const spax_step* st, hipStream_t s, bool noalloc, StepHoo
       if (rc) return rc;
       if (st->events) SPAX_HIP_CHECK(hipEventRecord(st->events[2 * i], s));
       rc = launch_tiered_gemv(L, plan, ph.packed, ph.x, ph.full_idx, ph.approx_idx, ph.counts,
-                              ph.y, cleared || clear_in_mask, s, false, partials);
+                              ph.y, cleared || clear_in_mask, s, Lists::kWhole, partials);
       if (rc) return rc;
       if (st->events) SPAX_HIP_CHECK(hipEventRecord(st->events[2 * i + 1], s));
       if (hooks && (rc = hooks->after(i, s))) return rc;

@@ -20,7 +20,7 @@ namespace {
 
 using gemv::kWaves;
 
-template <int FMT, bool kCompact, class Blob>
+template <int FMT, bool kCompact, bool kWhole, class Blob>
 __global__ __launch_bounds__(kGemvThreads) void tiered_gemv_kernel(
     gemv::Shape sh, const uint8_t* __restrict__ packed, const uint32_t* __restrict__ x32,
     const int32_t* __restrict__ full_idx, const int32_t* __restrict__ approx_idx,
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kGemvThreads) void tiered_gemv_kernel(
   const int item = gemv::xcd_order((int)blockIdx.x, (int)gridDim.x);
   const int tile = (int)((uint32_t)item % (uint32_t)sh.n_tiles);
   const int chunk = (int)((uint32_t)item / (uint32_t)sh.n_tiles);
-  gemv::gemv_item<FMT, Blob, kCompact>(sh, packed, x32, full_idx, approx_idx, counts, y, tile,
+  gemv::gemv_item<FMT, Blob, kCompact, kWhole>(sh, packed, x32, full_idx, approx_idx, counts, y, tile,
                                        chunk, red, partials);
 }
 
@@ -227,7 +227,7 @@ int launch_reduce_chunks(const float* partials, int32_t n_chunks, int64_t T, flo
 int launch_tiered_gemv(const spax_layout* L, const GemvPlan& plan, const void* packed,
                        const uint16_t* x, const int32_t* full_idx, const int32_t* approx_idx,
                        const int32_t* counts, float* y, bool y_zeroed, hipStream_t s,
-                       bool compact, float* partials) {
+                       Lists lists, float* partials) {
   if (plan.n_chunks == 1) partials = nullptr;  // one chunk: plain stores, already deterministic
   if (plan.n_chunks > 1 && !y_zeroed && !partials) {
     int st = launch_zero_f32(y, L->d_out_total, s);
@@ -239,20 +239,23 @@ int launch_tiered_gemv(const spax_layout* L, const GemvPlan& plan, const void* p
   const auto* x32 = reinterpret_cast<const uint32_t*>(x);
   // The compacted staging copy has the blob's layout (record slots in place of channels).
   const bool narrow = narrow_regions(L);
-#define SPAX_GEMV_LAUNCH(F, C, B)                                                             \
-  hipLaunchKernelGGL((tiered_gemv_kernel<F, C, gemv::B>), grid, dim3(kGemvThreads), 0, s, sh, \
+#define SPAX_GEMV_LAUNCH(F, C, W, B)                                                             \
+  hipLaunchKernelGGL((tiered_gemv_kernel<F, C, W, gemv::B>), grid, dim3(kGemvThreads), 0, s, sh, \
                      pk, x32, full_idx, approx_idx, counts, y, partials)
-#define SPAX_GEMV_LAUNCH_FMT(F)                                    \
-  if (compact && narrow) SPAX_GEMV_LAUNCH(F, true, RegionBlob);    \
-  else if (compact) SPAX_GEMV_LAUNCH(F, true, RecordBlob);         \
-  else if (narrow) SPAX_GEMV_LAUNCH(F, false, RegionBlob);         \
-  else SPAX_GEMV_LAUNCH(F, false, RecordBlob)
+#define SPAX_GEMV_LAUNCH_BLOB(F, B)                                           \
+  if (lists == Lists::kStaged) SPAX_GEMV_LAUNCH(F, true, true, B);            \
+  else if (lists == Lists::kWhole) SPAX_GEMV_LAUNCH(F, false, true, B);       \
+  else SPAX_GEMV_LAUNCH(F, false, false, B)
+#define SPAX_GEMV_LAUNCH_FMT(F)                          \
+  if (narrow) { SPAX_GEMV_LAUNCH_BLOB(F, RegionBlob); }  \
+  else { SPAX_GEMV_LAUNCH_BLOB(F, RecordBlob); }
   if (L->base_fmt == SPAX_FMT_FP16) {
     SPAX_GEMV_LAUNCH_FMT(SPAX_FMT_FP16);
   } else {
     SPAX_GEMV_LAUNCH_FMT(SPAX_FMT_INT4);
   }
 #undef SPAX_GEMV_LAUNCH_FMT
+#undef SPAX_GEMV_LAUNCH_BLOB
 #undef SPAX_GEMV_LAUNCH
   SPAX_HIP_CHECK(hipGetLastError());
   if (partials) return launch_reduce_chunks(partials, plan.n_chunks, L->d_out_total, y, s);

@@ -20,6 +20,7 @@
 #pragma once
 
 #include "common.h"
+#include "list_share.h"
 
 namespace spax {
 namespace gemv {
@@ -237,15 +238,22 @@ struct RegBlock {
   }
 };
 
-// Strided list blocks (stand-alone and batched GEMV): a wave's list entries are
-// first + stride * p for p = 0, 1, ...; lane l of block p0 holds p = p0 + l.  The entry
-// indices are fixed before the counts are known, so a block's index loads can be issued
-// before (or with) the counts load; an entry index is clamped into the list's capacity
-// (d_in entries), so a lane past the wave's count reads a stale but in-bounds entry, which
-// finish_blocks drops.
-__device__ __forceinline__ uint32_t load_index(const void* __restrict__ idx, int first,
-                                               int stride, int p, uint32_t jmax) {
-  const int entry = min(first + stride * p, (int)jmax);  // < 2^31: stride * p <= 2^29
+// Strided list blocks (stand-alone and batched GEMV): lane l of block p0 holds the wave's entry
+// p = p0 + l.  Lanes past the wave's `mine` entries read nothing, since a caller's list may end with
+// its last entry.
+__device__ __forceinline__ uint32_t load_index(const void* __restrict__ idx, ListShare share, int p,
+                                               int mine) {
+  const int entry = share.entry(p, mine);
+  return entry < 0 ? 0u : load_global<uint32_t>(reinterpret_cast<const uint32_t*>(idx) + entry);
+}
+
+// Lists that hold d_in entries whatever their counts (a step's and the pinned path's own): the first
+// block's index loads go out with the counts', and a lane past the wave's entries reads a stale one,
+// which finish_blocks drops.  Counts first cost up to 0.5 us a call (4096 x 4096 fp16 7.9 to 8.2
+// us, 4096 x 22016 int4 12.7 to 13.2, fp16 14.6 to 14.4).
+__device__ __forceinline__ uint32_t load_index_early(const void* __restrict__ idx, ListShare share,
+                                                     int p, uint32_t jmax) {
+  const int entry = min(share.first + share.stride * p, (int)jmax);  // < 2^31: stride * p <= 2^29
   return load_global<uint32_t>(reinterpret_cast<const uint32_t*>(idx) + entry);
 }
 
@@ -495,10 +503,10 @@ struct ItemRows {
 // of the lists in global memory -- the entries chunk, chunk + n_chunks, ... -- (counts
 // clamped to [0, d_in] and channels to [0, d_in), so malformed lists cannot address outside
 // the blob).  kCompact: the lists hold slot | channel << 16 entries into a compacted
-// staging copy of the records (`packed` is then the staging buffer).  A workgroup
-// of kWaves waves; RPL rows per lane (a 64 RPL-row tile), U columns per round; ends after the
+// staging copy of the records (`packed` is then the staging buffer).  kWhole: both lists hold d_in
+// entries, whatever their counts.  A workgroup of kWaves waves; RPL rows per lane (a 64 RPL-row tile), U columns per round; ends after the
 // tile's atomics.  red: kWaves x 64 RPL floats.  Blob: RegionBlob or RecordBlob.
-template <int FMT, class Blob, bool kCompact = false, int RPL = 8, int U = kUnroll>
+template <int FMT, class Blob, bool kCompact, bool kWhole, int RPL = 8, int U = kUnroll>
 __device__ __forceinline__ void gemv_item(const Shape& sh, const uint8_t* __restrict__ packed,
                                           const uint32_t* __restrict__ x32,
                                           const int32_t* __restrict__ full_idx,
@@ -515,18 +523,15 @@ __device__ __forceinline__ void gemv_item(const Shape& sh, const uint8_t* __rest
   // height is a multiple of 64, so a lane's rows are all inside or all past T.
   const int row = row0 + lane * RPL < T ? row0 + lane * RPL : 0;
   const uint32_t jmax = (uint32_t)sh.d_in - 1u;
-  // Chunk c takes the list entries c, c + n_chunks, c + 2 n_chunks, ... and wave w of the
-  // workgroup every kWaves-th of those, so this wave's entries are first + stride * p.  The
-  // first block's index loads go out with the counts load; the counts only fix how many of
-  // the entries are valid.  Every chunk and every wave gets the same count within one.
-  const int stride = sh.n_chunks * kWaves;
-  const int first = chunk + sh.n_chunks * wave;
-  uint32_t rF = load_index(full_idx, first, stride, lane, jmax);
-  uint32_t rA = load_index(approx_idx, first, stride, lane, jmax);
+  const ListShare share(chunk, sh.n_chunks, wave, kWaves);
+  uint32_t rF = 0u, rA = 0u;
+  if constexpr (kWhole) {
+    rF = load_index_early(full_idx, share, lane, jmax);
+    rA = load_index_early(approx_idx, share, lane, jmax);
+  }
   const int nF = uniform(min(max(load_global<int32_t>(counts), 0), sh.d_in));
   const int nA = uniform(min(max(load_global<int32_t>(counts + 1), 0), sh.d_in));
-  const int cF = nF > first ? (nF - first + stride - 1) / stride : 0;  // this wave's entries
-  const int cA = nA > first ? (nA - first + stride - 1) / stride : 0;
+  const int cF = share.count(nF), cA = share.count(nA);  // this wave's entries
   float acc[RPL];
 #pragma unroll
   for (int h = 0; h < RPL; ++h) acc[h] = 0.0f;
@@ -535,9 +540,9 @@ __device__ __forceinline__ void gemv_item(const Shape& sh, const uint8_t* __rest
   const Blob b(sh, packed);
   // 64 list entries per tier and block; the channels fit the 16-bit entry field (d_in <= 32768)
   for (int p0 = 0; p0 < cF || p0 < cA; p0 += 64) {
-    if (p0 > 0) {
-      rF = load_index(full_idx, first, stride, p0 + lane, jmax);
-      rA = load_index(approx_idx, first, stride, p0 + lane, jmax);
+    if (!kWhole || p0 > 0) {
+      rF = load_index(full_idx, share, p0 + lane, cF);
+      rA = load_index(approx_idx, share, p0 + lane, cA);
     }
     const int nf = min(cF - p0, 64), na = min(cA - p0, 64);  // may be <= 0
     RegBlock bf, ba;

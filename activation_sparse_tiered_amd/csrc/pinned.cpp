@@ -210,7 +210,8 @@ int tiered_gemv_pinned_device_merge(const spax_layout* L, const void* host_dev,
                                    t.listA, t.colF, t.colA, t.totals, s);
   if (rc) return rc;
   rc = launch_tiered_gemv(L, gemv_plan(L), ws, x, reinterpret_cast<const int32_t*>(t.listF),
-                          reinterpret_cast<const int32_t*>(t.listA), counts, y, false, s, true);
+                          reinterpret_cast<const int32_t*>(t.listA), counts, y, false, s,
+                          Lists::kStaged);
   if (rc) return rc;
   if (stats) {
     int32_t h[kTotals];
@@ -338,7 +339,8 @@ int tiered_gemv_pinned(const spax_layout* L, const void* packed_host, const void
   // ---- the GEMV over the staged records (counts are still the device's)
   rc = launch_tiered_gemv(&staged, gemv_plan(L), staging, x,
                           reinterpret_cast<const int32_t*>(t.listF),
-                          reinterpret_cast<const int32_t*>(t.listA), counts, y, false, s, true);
+                          reinterpret_cast<const int32_t*>(t.listA), counts, y, false, s,
+                          Lists::kStaged);
   if (rc) return rc;
   if (stats) {
     stats->selected_bytes = (int64_t)nF * L->stride_F + (int64_t)nA * L->stride_A;

@@ -219,7 +219,8 @@ size_t spax_gemv_workspace_bytes(const spax_layout* L);
  *   full_idx, approx_idx, counts : device, as written by spax_build_tiers (or any
  *                 caller lists of distinct channels with counts[0], counts[1]).  Counts are
  *                 clamped to [0, d_in] and indices to [0, d_in) on the device, so malformed
- *                 lists give an unspecified y but never an out-of-bounds access.
+ *                 lists give an unspecified y but never an out-of-bounds access.  Entries past
+ *                 a list's count are not read: it need not be longer (one entry at least).
  *   y           : device, d_out_total fp32, 16-byte aligned; fully overwritten (all zeros
  *                 if both lists are empty).  Rows follow the fused order of *L.
  *   ws, ws_bytes: device workspace of at least spax_gemv_workspace_bytes(L) bytes,
