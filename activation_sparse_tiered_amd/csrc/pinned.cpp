@@ -270,13 +270,15 @@ int tiered_gemv_pinned(const spax_layout* L, const void* packed_host, const void
   uint32_t* h_outF = reinterpret_cast<uint32_t*>(h_apx + d);
   uint32_t* h_outA = h_outF + d;
 
-  // ---- the mask, back on the host
-  SPAX_HIP_CHECK(hipMemcpyAsync(h_counts, counts, 12, hipMemcpyDeviceToHost, s));
-  SPAX_HIP_CHECK(hipMemcpyAsync(h_full, full_idx, 4 * (size_t)d, hipMemcpyDeviceToHost, s));
-  SPAX_HIP_CHECK(hipMemcpyAsync(h_apx, approx_idx, 4 * (size_t)d, hipMemcpyDeviceToHost, s));
+  // ---- the mask, back on the host: the counts first, as a caller's lists may end with their last
+  // entries
+  SPAX_HIP_CHECK(hipMemcpyAsync(h_counts, counts, 8, hipMemcpyDeviceToHost, s));
   SPAX_HIP_CHECK(hipStreamSynchronize(s));
   const int nF = h_counts[0] < 0 ? 0 : (h_counts[0] > d ? d : h_counts[0]);
   const int nA = h_counts[1] < 0 ? 0 : (h_counts[1] > d ? d : h_counts[1]);
+  if (nF) SPAX_HIP_CHECK(hipMemcpyAsync(h_full, full_idx, 4 * (size_t)nF, hipMemcpyDeviceToHost, s));
+  if (nA) SPAX_HIP_CHECK(hipMemcpyAsync(h_apx, approx_idx, 4 * (size_t)nA, hipMemcpyDeviceToHost, s));
+  SPAX_HIP_CHECK(hipStreamSynchronize(s));
 
   // ---- ranges -> record copies into the compacted staging area; compacted lists
   uint8_t* staging = static_cast<uint8_t*>(ws);
