@@ -349,8 +349,8 @@ __device__ inline void clear_odd(uint8_t* v, int pieces, int thread, int threads
 }
 
 // The exponentials are taken of s - m + kLift (base 2), and the running maximum m is raised only once a
-// score is kSlack above it, so the largest is 2^(kLift + kSlack): all that fp16 holds.  In fp16 the lift
-// keeps a long tail under one large key; both cancel in o / l.
+// score is kSlack above it, so the largest is 2^(kLift + kSlack), with 2^-13 of rounding (soften):
+// all that fp16 holds.  In fp16 the lift keeps a long tail under one large key; both cancel in o / l.
 template <class T>
 struct Soft;
 template <>
@@ -377,7 +377,7 @@ struct Rows {
   using Values = u32x4[S::kSteps][OB];
   u32x4 q[KC];
   f32x16 o[OB];
-  float m, l;
+  float m, l;  // the running maximum of the raw scores, and the lane's part of the sum
   // of values that are not finite: whether dim 32 b + i (in o's order, bit 16 b + i) met one that is
   // not -inf, and one that is not inf
   uint64_t up[(OB + 3) / 4], down[(OB + 3) / 4];
@@ -436,7 +436,7 @@ struct Rows {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = (bits >> (16 * b + i)) & 1u ? s[b][i] : -INFINITY;
   }
-  // The running maximum; to_log2 > 0.
+  // The running maximum, raised where it pays; to_log2 > 0.
   __device__ inline void raise(const Scores& s, float to_log2) {
     float top = s[0][0];
 #pragma unroll
@@ -446,18 +446,27 @@ struct Rows {
     // the row's other lane
     const auto both =
         __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * to_log2;
-    if (!__any(top > m + Soft<T>::kSlack)) return;
+    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
+    if (!__any((top - m) * to_log2 > Soft<T>::kSlack)) return;
     const float higher = fmaxf(m, top);
-    const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
+    const float f = higher == m ? 1.0f : __builtin_amdgcn_exp2f((m - higher) * to_log2);
     m = higher;
     l *= f;
 #pragma unroll
     for (int b = 0; b < OB; ++b) o[b] *= f;
   }
-  // Scores to p, in the second product's operand order, and their sums.
-  __device__ inline void soften(const Scores& s, float to_log2, u32x4 (&p)[S::kSteps]) {
-    const float base = (m == -INFINITY ? 0.0f : m) - Soft<T>::kLift;
+  // Scores to p, in the second product's operand order, and their sums.  The exponent is one
+  // multiply-add from a base that is rounded once, to 2^-13 below kPlain; past it, where that
+  // rounding would lift p by more than kLift + kSlack, the maximum is taken off first.
+  static constexpr float kPlain = 4096.0f;
+  __device__ inline void soften(Scores& s, float to_log2, u32x4 (&p)[S::kSteps]) {
+    const float top = m == -INFINITY ? 0.0f : m;
+    float base = fmaf(top, to_log2, -Soft<T>::kLift);
+    if (!__all(fabsf(base) < kPlain)) {
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b) s[b] -= top;
+      base = -Soft<T>::kLift;
+    }
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < S::kSteps; ++t)
@@ -537,6 +546,8 @@ __device__ inline float to_log2_of(const ChunkArgs& a, int kvh) {
   const float f = a.scale * kLog2e;
   return NARROW && a.k_scale ? f * a.k_scale[kvh] : f;
 }
+// The queries have its sign, and are zeros where it is zero (Rows::begin).
+__device__ inline float positive(float to_log2) { return to_log2 == 0.0f ? 1.0f : fabsf(to_log2); }
 template <bool NARROW>
 __device__ inline float v_mul_of(const ChunkArgs& a, int kvh) {
   return NARROW && a.v_scale ? a.v_scale[kvh] : 1.0f;
@@ -544,7 +555,7 @@ __device__ inline float v_mul_of(const ChunkArgs& a, int kvh) {
 
 // A piece of 32 rows of a tile leaves its sums as a wave holds them, dims 8 g + 4 h .. of row r in lane
 // 32 h + r of group g, so that they go to memory and come back 1024 bytes at once (by rows, 8 x 128
-// over 1000 took 88 us), and its maxima and weights.
+// over 1000 took 88 us), and its maxima (of raw scores) and weights.
 __device__ inline int64_t part_of(const ChunkArgs& a, int piece, int rows32, int kvh) {
   return ((int64_t)piece * a.tiles * (a.rows / 32) + rows32) * a.n_kv + kvh;
 }
@@ -596,7 +607,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
   w.begin(a, tile, token, head, to_log2, lane);
 #pragma unroll
   for (int b = 0; b < R::OB; ++b) w.o[b] = f32x16{};
-  to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
+  to_log2 = positive(to_log2);
   // 0 * inf is NaN, so where some row does not see some key, values that are not finite are taken out
   // of the step and noted for the rows that do see them.
   __shared__ int odd_step[2];
@@ -699,7 +710,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
         for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : w.value(b, 4 * y + i) * f;
         store_n<4>(out + 32 * b + 8 * y + 4 * h, x);
       }
-    if (a.lse && h == 0) a.lse[at] = log_sum<T>(w.m, w.l);
+    if (a.lse && h == 0) a.lse[at] = log_sum<T>(w.m * to_log2, w.l);
     return;
   }
   const int64_t part = part_of(a, piece, index * W + wave, kvh);
@@ -756,7 +767,7 @@ __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
   w.begin(a, tile, token, head, to_log2, lane);
 #pragma unroll
   for (int b = 0; b < R::OB; ++b) w.o[b] = f32x16{};
-  to_log2 = to_log2 == 0.0f ? 1.0f : fabsf(to_log2);
+  to_log2 = positive(to_log2);
   const int all_lo = lo_of(a, tile.position((tile.to - 1) / a.group));
   const int all_hi = hi_of(tile.position(tile.from / a.group));
 
@@ -869,7 +880,7 @@ __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
   for (int y = 0; y < kWaves; ++y) m = fmaxf(m, ml[y][r][0]);
 #pragma unroll
   for (int y = 0; y < kWaves; ++y) {
-    f[y] = __builtin_amdgcn_exp2f(ml[y][r][0] - (m == -INFINITY ? 0.0f : m));
+    f[y] = __builtin_amdgcn_exp2f((ml[y][r][0] - (m == -INFINITY ? 0.0f : m)) * to_log2);
     l += f[y] * ml[y][r][1];
   }
   const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
@@ -899,7 +910,7 @@ __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
     if (!whole)
       *part_weight(a, part, r) = f32x2{m, l};
     else if (a.lse)
-      a.lse[at] = log_sum<T>(m, l);
+      a.lse[at] = log_sum<T>(m * to_log2, l);
   }
 }
 
@@ -918,6 +929,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a
   const int shares = D / 8 / a.join_groups, per = a.rows / 32;
   const int share = item % shares, kvh = item / shares % a.n_kv, rows32 = item / shares / a.n_kv;
   if (rows32 >= a.tiles * per) return;
+  // (scales come with 8-bit caches alone)
+  const float v_mul = a.v_scale ? a.v_scale[kvh] : 1.0f;
+  const float to_log2 = positive(a.scale * kLog2e * (a.k_scale ? a.k_scale[kvh] : 1.0f));
   const Seq seqs = seq_at(a, lane);
   const Tile tile = find_tile(a, seqs, rows32 / per, lane);
   const int first = tile.from + rows32 % per * 32;
@@ -950,19 +964,19 @@ __global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a
   const int from = split == 1 ? 0 : wave, more = kLoads * split;
   const int row = first + r < tile.to ? first + r : tile.to - 1;
   const int token = tile.first + row / a.group, head = kvh * a.group + row % a.group;
-  const float v_mul = a.v_scale ? a.v_scale[kvh] : 1.0f;
   load_weights(from);
   load_sums(from, share * a.join_groups);
   for (int group = share * a.join_groups, last = group + a.join_groups - 1;;) {
     float m = -INFINITY, l = 0.0f;
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     const auto add = [&](float m1, float l1, f32x4 x1, float base) {
-      const float f = __builtin_amdgcn_exp2f(m1 - base);
+      const float f = __builtin_amdgcn_exp2f((m1 - base) * to_log2);
       l += f * l1;
       sum += f * x1;
     };
     const auto raise = [&](float higher) {
-      const float base = higher == -INFINITY ? 0.0f : higher, f = __builtin_amdgcn_exp2f(m - base);
+      const float base = higher == -INFINITY ? 0.0f : higher;
+      const float f = __builtin_amdgcn_exp2f((m - base) * to_log2);
       l *= f;
       sum *= f;
       m = higher;
@@ -1001,7 +1015,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a
     for (int i = 0; i < 4; ++i) out[i] = l == 0.0f ? 0.0f : sum[i] * inv;
     if (first + r < tile.to) {
       store_n<4>((T*)a.out + token * a.ot + head * a.oh + 8 * group + 4 * h, out);
-      if (a.lse && group == 0 && h == 0) a.lse[(int64_t)token * a.n_heads + head] = log_sum<T>(m, l);
+      if (a.lse && group == 0 && h == 0) a.lse[(int64_t)token * a.n_heads + head] = log_sum<T>(m * to_log2, l);
     }
     if (group == last) break;
     ++group;
