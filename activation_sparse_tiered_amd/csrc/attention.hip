@@ -314,7 +314,15 @@ struct Wave {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][i] *= f;
     }
-    const float base = (m == -INFINITY ? 0.0f : m) - Mma<T>::kLift;
+    // Rounded once, to 2^-13 below 4096; past it, where that rounding would lift p past what fp16
+    // holds, the maximum is taken off first.
+    const float most = m == -INFINITY ? 0.0f : m;
+    float base = most - Mma<T>::kLift;
+    if (!__all(fabsf(base) < 4096.0f)) {
+#pragma unroll
+      for (int i = 0; i < 4 * KH; ++i) p[i] -= most;
+      base = -Mma<T>::kLift;
+    }
     u32x4 hi2, lo2;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {

@@ -14,7 +14,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // kLift: the exponentials are taken of s - m + kLift (base 2), so the largest is 2^kLift, the most
-// that fp16 holds with room for its rounding.  It cancels in o / l, and lse takes it off again.
+// that fp16 holds with room for its rounding and 2^-13 of the base's.  It cancels in o / l, and lse takes it off again.
 template <class T>
 struct Mma;
 template <>
