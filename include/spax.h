@@ -613,10 +613,10 @@ int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes
  * h / (n_heads / n_kv_heads):
  *   score_j = scale * k_scale * q . k_j,   out = v_scale * sum_j softmax(score)_j v_j,
  *   lse = ln sum_j exp(score_j).
- * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)], starts to
- * [0, n_tokens]; a sequence whose starts do not ascend has no tokens, and rows claimed by two
- * sequences hold unspecified values.  Keys on entries that name no page are left out; bytes of rows
- * that a token does not see never reach its result, whatever they hold.  A token with no keys (or at a
+ * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)], starts[s] to
+ * [0, n_tokens] and as no smaller than any start before it: a sequence whose starts do not ascend
+ * has no tokens, and no row belongs to two.  Keys on entries that name no page are left out; bytes
+ * of rows that a token does not see never reach its result, whatever they hold.  A token with no keys (or at a
  * negative position), or whose scores are all -inf, gives zeros and lse -inf.  Rows of no
  * sequence (before starts[0], behind starts[n_seqs]) are left as they were.
  *   q, out : `type` (SPAX_F16 or SPAX_BF16), the cache's type or the cache E4M3; 16-byte aligned
