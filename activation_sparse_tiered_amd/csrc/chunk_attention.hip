@@ -521,7 +521,28 @@ struct Rows {
       for (int b = 0; b < OB; ++b) o[b] = Mma<T>::mul32(v[t][b], p[t], o[b]);
   }
   // Notes which dims of the row meet a value that is not finite, which decides them whatever else
-  // they meet.
+  // they meet and however small its weight: in dims 8 g + 4 h .. of one key,
+  __device__ inline void note(u32x2 w, int g) {
+    uint64_t u = 0, d = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t word = w[i / 2];  // (a cast of the element itself takes the first)
+      const typename Mma<T>::v2 x = __builtin_bit_cast(typename Mma<T>::v2, word);
+      const float f = (float)(i % 2 ? x.y : x.x);
+      if (!(fabsf(f) < INFINITY)) {
+        u |= f < 0.0f ? 0u : 1u << i;
+        d |= f > 0.0f ? 0u : 1u << i;
+      }
+    }
+    const int to = 4 * (g & 15);
+    up[0] |= g < 16 ? u << to : 0;
+    down[0] |= g < 16 ? d << to : 0;
+    if constexpr (OB > 4) {
+      up[1] |= g < 16 ? 0 : u << to;
+      down[1] |= g < 16 ? 0 : d << to;
+    }
+  }
+  // in a step's values in LDS,
   __device__ inline void note_odd(const uint8_t* values, int key0, int page, int lane) {
     const int h = lane >> 5;
     const uint32_t bits = seen(key0, page, lane), others = __shfl_xor(bits, 32);
@@ -535,30 +556,40 @@ struct Rows {
       for (int g = 0; g < 4 * OB; ++g) {  // dims 8 g + 4 h ..
         const u32x2 w = *reinterpret_cast<const u32x2*>(values + key * S::kRow +
                                                         16 * S::v_place(key, g) + 8 * h);
-        uint64_t u = 0, d = 0;
+        note(w & keep, g);
+      }
+    }
+  }
+  // and in memory, in every step-th kKeys keys from key0 up to stop: steps that all rows see whole
+  // leave such a value in the product, where a weight that rounds to 0 makes it NaN.  Only where a
+  // sum came out not finite though the weights are, so most tiles never get here.  (8-bit values
+  // are finite or NaN, which the product keeps.)
+  template <class In>
+  __device__ inline void look_again(const In& in, int key0, int step, int stop, int lane) {
+    float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const typename Mma<T>::v2 x = __builtin_bit_cast(typename Mma<T>::v2, w[i / 2] & keep);
-          const float f = (float)(i % 2 ? x.y : x.x);
-          if (!(fabsf(f) < INFINITY)) {
-            u |= f < 0.0f ? 0u : 1u << i;
-            d |= f > 0.0f ? 0u : 1u << i;
-          }
-        }
-        const int to = 4 * (g & 15);
-        up[0] |= g < 16 ? u << to : 0;
-        down[0] |= g < 16 ? d << to : 0;
-        if constexpr (OB > 4) {
-          up[1] |= g < 16 ? 0 : u << to;
-          down[1] |= g < 16 ? 0 : d << to;
-        }
+    for (int b = 0; b < OB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z = fmaf(o[b][i], 0.0f, z);
+    if (!__any(z != 0.0f && fabsf(l) < INFINITY)) return;
+#pragma unroll 1
+    for (; key0 < stop; key0 += step) {
+      const int page = in.page_of(in.look_up(key0, lane), key0, lane);
+#pragma unroll 1
+      for (int i = 0; i < S::kKeys; ++i) {
+        const int pg = __shfl(page, i), key = key0 + i;
+        const uint32_t keep = pg >= 0 && key >= lo && key < hi ? ~0u : 0u;
+        const uint8_t* row = in.row_at(in.v, pg, key) + 8 * (lane >> 5);
+#pragma unroll 1
+        for (int g = 0; g < 4 * OB; ++g)
+          note(*reinterpret_cast<const u32x2*>(row + 16 * g) & keep, g);
       }
     }
   }
   __device__ inline float value(int b, int i) const {
     const uint64_t bit = (uint64_t)1 << (16 * (b % 4) + i);
     const bool u = up[b / 4] & bit, d = down[b / 4] & bit;
-    return u || d ? o[b][i] + (u ? d ? NAN : INFINITY : -INFINITY) : o[b][i];
+    return u || d ? u ? d ? NAN : INFINITY : -INFINITY : o[b][i];
   }
 };
 
@@ -583,6 +614,21 @@ __device__ inline int64_t part_of(const ChunkArgs& a, int piece, int rows32, int
 template <int D>
 __device__ inline f32x4* part_sums(const ChunkArgs& a, int64_t part, int group, int lane) {
   return reinterpret_cast<f32x4*>(a.part_o) + (part * (D / 8) + group) * 64 + lane;
+}
+// Sums that are not finite decide a joined one, whatever their weights (0 * inf is NaN).
+__device__ inline bool is_finite(f32x4 x) {
+  return fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) < INFINITY &&
+         x.x == x.x && x.y == x.y && x.z == x.z && x.w == x.w;
+}
+__device__ inline f32x4 odd_ones(f32x4 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = fabsf(x[i]) < INFINITY ? 0.0f : x[i];
+  return x;
+}
+__device__ inline f32x4 decided(f32x4 sum, f32x4 odd) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i] = odd[i] == 0.0f ? sum[i] : odd[i];
+  return sum;
 }
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 __device__ inline f32x2* part_weight(const ChunkArgs& a, int64_t part, int r) {
@@ -716,6 +762,8 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
 
   if (!works) return;
   w.l += __shfl_xor(w.l, 32);
+  if constexpr (!NARROW)
+    w.look_again(in, steps.first * S::kKeys, S::kKeys, (steps.first + steps.count) * S::kKeys, lane);
   if (first + r >= tile.to) return;
   const int64_t at = (int64_t)(tile.first + token) * a.n_heads + head;
   if (steps.pieces <= 1) {
@@ -798,6 +846,7 @@ __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
   const int end = (steps.first + steps.count) * kStep;
   const int stop = steps.hi < end ? steps.hi : end;
   if (key0 + kKeys <= steps.lo) key0 += kStep;
+  const int begin = key0;
   if (key0 < stop) {
     int page = in.page_of(in.look_up(key0, lane), key0, lane);
     in.template load<false>(keys, page, key0, 0, lane);
@@ -880,6 +929,7 @@ __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
 
   // Join the waves: dims c .. c + 3 of all rows side by side.
   w.l += __shfl_xor(w.l, 32);
+  if constexpr (!NARROW) w.look_again(in, begin, kStep, stop, lane);
   float* mine = reinterpret_cast<float*>(keys);
 #pragma unroll
   for (int b = 0; b < R::OB; ++b)
@@ -910,14 +960,23 @@ __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
   const float inv = v_mul_of<NARROW>(a, kvh) / l;
   constexpr int kShare = D / 4 / kWaves;  // of the dims, four at a time
   static_assert(kShare % 2 == 0, "two halves of a wave");
+  const auto x_of = [&](int z, int c) {  // wave z's sums
+    return *reinterpret_cast<const f32x4*>(
+        reinterpret_cast<const float*>(lds + z * 2 * S::kBuffer) + 4 * (32 * c + r));
+  };
 #pragma unroll
   for (int y = 0; y < kShare / 2; ++y) {
     const int c = wave * kShare + 2 * y + h;
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int z = 0; z < kWaves; ++z)
-      sum += f[z] * *reinterpret_cast<const f32x4*>(
-                        reinterpret_cast<const float*>(lds + z * 2 * S::kBuffer) + 4 * (32 * c + r));
+      sum += f[z] * x_of(z, c);
+    if (!NARROW && __any(!is_finite(sum))) {
+      f32x4 odd = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int z = 0; z < kWaves; ++z) odd += odd_ones(x_of(z, c));
+      sum = decided(sum, odd);
+    }
     if (whole) {
       float x[4];
 #pragma unroll
@@ -1015,6 +1074,14 @@ __global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a
       load_weights(c0);
       load_sums(c0, group);
     }
+    // A sum that is not finite decides, whatever its weight: looked for again, where there is one.
+    if (__any(first + r < tile.to && !is_finite(sum))) {
+      f32x4 odd = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int c = from; c < pieces; c += split)
+        odd += odd_ones(*part_sums<D>(a, part_of(a, c, rows32, kvh), group, lane));
+      sum = decided(sum, odd);
+    }
     if (split > 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) others[wave][i][lane] = sum[i];
@@ -1022,13 +1089,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void chunk_join_kernel(ChunkArgs a
       others[wave][5][lane] = l;
       mask::lds_barrier();
       if (wave > 0) return;
+      f32x4 odd = odd_ones(sum);
 #pragma unroll
       for (int y = 1; y < kJoinWaves; ++y) {
         const float m1 = others[y][4][lane];
         const f32x4 x1 = {others[y][0][lane], others[y][1][lane], others[y][2][lane],
                           others[y][3][lane]};
         add(m1, others[y][5][lane], x1, raise(fmaxf(m, m1)));
+        odd += odd_ones(x1);
       }
+      sum = decided(sum, odd);
     }
     const float inv = v_mul / l;
     float out[4];

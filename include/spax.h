@@ -616,8 +616,10 @@ int spax_paged_attention(const spax_attention_args* a, void* ws, size_t ws_bytes
  * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)], starts[s] to
  * [0, n_tokens] and as no smaller than any start before it: a sequence whose starts do not ascend
  * has no tokens, and no row belongs to two.  Keys on entries that name no page are left out; bytes
- * of rows that a token does not see never reach its result, whatever they hold.  A token with no keys (or at a
- * negative position), or whose scores are all -inf, gives zeros and lse -inf.  Rows of no
+ * of rows that a token does not see never reach its result, whatever they hold.  A value that it
+ * sees and that is not finite decides its dim, however small its weight: infinite, or NaN if it is
+ * NaN or meets an infinity of the other sign.  A token with no keys (or at a negative position),
+ * or whose scores are all -inf, gives zeros and lse -inf.  Rows of no
  * sequence (before starts[0], behind starts[n_seqs]) are left as they were.
  *   q, out : `type` (SPAX_F16 or SPAX_BF16), the cache's type or the cache E4M3; 16-byte aligned
  *             with strides a multiple of 8 elements.
