@@ -189,7 +189,7 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
           z.w[e] = *reinterpret_cast<const u32x4*>(rec + w_at);
         }
       }
-    } else {  // the last k: past them x counts as zeros, and the last record stands in
+    } else {  // the last k: past them x and the weights count as zeros (0 * inf is NaN)
       const int valid = a.k - k0 - 8 * h;  // of the lane's eight
       u32x4 v = {0u, 0u, 0u, 0u};
       if (valid > 0) v = *reinterpret_cast<const u32x4*>(a.x + k0 + x_at);
@@ -201,7 +201,9 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
         return a.w + (int64_t)(e < valid ? k0 + 8 * h + e : a.k - 1) * a.w_stride;
       };
       if constexpr (INT4)
-        z.sz = *reinterpret_cast<const uint32_t*>(record(lane & 7) + a.n / 2 + col / 128 * 4);
+        z.sz = (lane & 7) < valid
+                   ? *reinterpret_cast<const uint32_t*>(record(lane & 7) + a.n / 2 + col / 128 * 4)
+                   : 0u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint8_t* rec = record(e);
@@ -209,6 +211,7 @@ __global__ __launch_bounds__(Few<INT4>::kThreads) void gemm_few_kernel(GemmArgs 
           z.q[e] = *reinterpret_cast<const uint32_t*>(rec + col / 2);
         } else {
           z.w[e] = *reinterpret_cast<const u32x4*>(rec + 2 * (int64_t)col);
+          if (e >= valid) z.w[e] = u32x4{0u, 0u, 0u, 0u};
         }
       }
     }
@@ -416,16 +419,27 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
     }
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i) {
-      // past the last record: that one again, times zero
+      // past the last record: that one again, until clear_tail, and of int4 scale and zero 0
       const int k = k0 + w_row[i] < a.k ? k0 + w_row[i] : a.k - 1;
       const int64_t at = (int64_t)k * a.w_stride;
       if constexpr (INT4) {
         codes = *reinterpret_cast<const u32x4*>(w_from[i] + at);
         sz = *reinterpret_cast<const uint32_t*>(sz_from + at);
+        sz = k0 + w_row[i] < a.k ? sz : 0u;
       } else {
         load_lds(w_from[i] + at, stage + M::kX + (wave * kWLoads + i) * 1024);
       }
     }
+  };
+  // The last step's weights past the last record are zeros (0 * inf is NaN): each thread clears what it
+  // had loaded there, once that has come.
+  const auto clear_tail = [&](int step) {
+    if (INT4 || (step + 1) * M::kDepth <= a.k) return;
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i)
+      if (step * M::kDepth + w_row[i] >= a.k)
+        *reinterpret_cast<u32x4*>(stages + (step & 1) * M::kStage + M::kX +
+                                  16 * ((wave * kWLoads + i) * 64 + lane)) = u32x4{0u, 0u, 0u, 0u};
   };
   const auto lay_out = [&](int step) {
     if constexpr (INT4) {
@@ -507,6 +521,7 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
   } else {
     for (int step = first; step < stop; ++step) {
       wait_loads();
+      clear_tail(step);
       mask::lds_barrier();  // this stage is laid out, the other one has been read
       if (step + 1 < stop) load(step + 1);
       read(step, 0);

@@ -725,7 +725,8 @@ enum { SPAX_GEMM_PLAIN = 0, SPAX_GEMM_ACT = 1, SPAX_GEMM_GATED = 2 };
  *   residual : residual_type, y : y_type (SPAX_F32, SPAX_F16, SPAX_BF16); residual may be y itself
  *              (type and stride alike).
  * Sums are in 32 bits, in an order that depends on the sizes alone; the weights of an INT4 base
- * enter the product as w_hat rounded to fp16 (the tiered GEMV keeps them in 32 bits).
+ * enter the product as w_hat rounded to fp16 (the tiered GEMV keeps them in 32 bits), so one of
+ * 65520 and more is infinite.
  *   ws       : spax_packed_gemm_workspace_bytes(a) bytes (0: none needed), 256-byte aligned, any
  *              contents; calls that may run at the same time need a workspace each.
  * n_rows 0 does nothing.
