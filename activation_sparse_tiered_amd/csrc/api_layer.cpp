@@ -507,9 +507,9 @@ int check_packed_gemm(const spax_packed_gemm_args* a, Spans* spans) {
       !aligned(a->residual, a->residual ? (size_t)elem::bytes_of(a->residual_type) : 1))
     return fail(SPAX_ERR_ALIGN, "a pointer is not aligned to its element");
   const int64_t n = a->n_rows, d = gated ? L.d_out[0] : L.d_out_total;
-  if (n > 1 && (a->x_stride < L.d_in || a->y_stride < d || (a->residual && a->residual_stride < d) ||
-                !stride_range(n, a->x_stride) || !stride_range(n, a->y_stride) ||
-                !stride_range(n, a->residual_stride)))
+  if (n > 1 && (a->x_stride < L.d_in || a->y_stride < d || !stride_range(n, a->x_stride) ||
+                !stride_range(n, a->y_stride) ||
+                (a->residual && (a->residual_stride < d || !stride_range(n, a->residual_stride)))))
     return fail(SPAX_ERR_PARAM, "a stride is below its row or out of range");
   if (gemm_plan(a).blocks >= 1 << 22)  // a grid holds 2^32 threads
     return fail(SPAX_ERR_SHAPE, "%d rows of %lld columns are too many", a->n_rows,
