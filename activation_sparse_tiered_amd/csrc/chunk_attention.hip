@@ -32,11 +32,13 @@
 #include "attn_core.h"
 #include "layer_ops.h"
 #include "mask_core.h"
+#include "staging.h"
 
 namespace spax {
 namespace {
 
 using namespace elem;
+using namespace staging;
 using namespace attn;
 
 // Query rows of a tile of so many waves.
@@ -222,18 +224,6 @@ struct Shape {
   static __device__ inline int turned(int c) { return c >= kPieces ? c - kPieces : c; }
 };
 
-// 16 bytes a lane from memory to LDS, lane after lane from `to` (uniform) on.  By hand, since the
-// compiler lets every later LDS access wait for such a load; wait_loads() does before a barrier.
-__device__ inline void load_lds(const void* from, const void* to) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(
-      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(at), "v"(from)
-               : "memory", "m0");
-}
-__device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
-
 // Brings a step's keys and values into LDS.  16-bit rows go there straight from memory, 8-bit ones
 // through registers, where they are widened once for all of its waves.
 template <class T, bool NARROW, int D, int KEYS, int W>
@@ -340,13 +330,6 @@ struct Loader {
                  Mma<T>::template widen<false>(y), Mma<T>::template widen<true>(y)};
   }
 };
-
-// Four keys of one dim per lane: rows `row`.. of 16 dims for every 16 lanes.
-__device__ inline u32x2 read_turned(const uint8_t* p) {
-  typedef short v4 __attribute__((ext_vector_type(4)));
-  typedef __attribute__((address_space(3))) v4 lds_v4;
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)p));
-}
 
 // The sign bits of those of two values that are not finite.
 template <class T>
