@@ -402,13 +402,12 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
     }
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i) {
-      // past the last record: that one again, until clear_tail, and of int4 scale and zero 0
+      // past the last record: that one again, until clear_tail or lay_out
       const int k = k0 + w_row[i] < a.k ? k0 + w_row[i] : a.k - 1;
       const int64_t at = (int64_t)k * a.w_stride;
       if constexpr (INT4) {
         codes = *reinterpret_cast<const u32x4*>(w_from[i] + at);
         sz = *reinterpret_cast<const uint32_t*>(sz_from + at);
-        sz = k0 + w_row[i] < a.k ? sz : 0u;
       } else {
         load_lds(w_from[i] + at, stage + M::kX + (wave * kWLoads + i) * 1024);
       }
@@ -428,8 +427,11 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
     if constexpr (INT4) {
       const int e = wave * 64 + lane, row = e / 8;
       uint8_t* to = stages + (step & 1) * M::kStage + M::kX + row * (2 * kCols);
-      const uint32_t s = __builtin_amdgcn_perm(sz, sz, 0x05040504u);
-      const uint32_t z = __builtin_amdgcn_perm(sz, sz, 0x07060706u);
+      // past the last record, scale and zero 0 (here and not in load, which would wait for them:
+      // 4096 x 4096 x 22016 818 us, 896 there)
+      const uint32_t words = step * M::kDepth + w_row[0] < a.k ? sz : 0u;
+      const uint32_t s = __builtin_amdgcn_perm(words, words, 0x05040504u);
+      const uint32_t z = __builtin_amdgcn_perm(words, words, 0x07060706u);
 #pragma unroll
       for (int y = 0; y < 4; ++y)
         *reinterpret_cast<u32x4*>(to + 16 * M::w_place(row, 4 * (e % 8) + y)) =
