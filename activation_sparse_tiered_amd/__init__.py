@@ -555,8 +555,9 @@ def make_chunk_attention(cache: KvCache, q, starts, lens, out, max_len: int | No
     """q and out [n_tokens, n_heads, head_dim], the new tokens of all sequences one after another;
     starts int32 [n_seqs + 1] (where each sequence's begin, and where the last one's end), lens
     int32 [n_seqs] (keys of each sequence, its new tokens' own among them), lse fp32
-    [n_tokens, n_heads] or None.  max_len: bound on lens (default: what the page table holds);
-    scale: default 1 / sqrt(head_dim)."""
+    [n_tokens, n_heads] or None.  max_len: bound on lens (default: what the page table holds; a
+    close one saves time and workspace, which are planned for it); scale: default
+    1 / sqrt(head_dim)."""
     _rows(q, "q", 3)
     _rows(out, "out", 3)
     _same_shape(q, "q", (q.shape[0], q.shape[1], cache.head_dim))

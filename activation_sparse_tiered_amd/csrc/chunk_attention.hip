@@ -22,12 +22,12 @@
 //     that are not finite are zeroed in LDS and noted for the rows that see them (note_odd).
 //
 // What bounds it.  Many rows and keys: matrix instructions are under way for 0.43 of the SIMDs'
-// cycles (counters; 0.38 from e4m3), vector instructions, the exponentials above all, for 0.48, and
-// the two overlap in part only, with two waves on a SIMD: 1 x 8192 of 32 heads on 8, fp16, 597 us,
-// 922 TFLOP/s; 8 x 512 over 15872 from e4m3 1226 us, 883 TFLOP/s; a large library product reaches
+// cycles (counters; 0.37 from e4m3), vector instructions, the exponentials above all, for 0.47, and
+// the two overlap in part only, with two waves on a SIMD: 1 x 8192 of 32 heads on 8, fp16, 600 us,
+// 917 TFLOP/s; 8 x 512 over 15872 from e4m3 1236 us, 875 TFLOP/s; a large library product reaches
 // 1400.  Two tiles of rows per wave, which would share its reads of keys and values, spilled (908 us
-// for 620 then); scores of the next step between the products of this one 722 us.  Few rows: the
-// chain starts, table, keys, two products, join, second launch, 20.5 us for 1 x 5 over 8192, of
+// for 620 then); scores of the next step between the products of this one 722 us for 620.  Few rows:
+// the chain starts, table, keys, two products, join, second launch, 18.4 us for 1 x 5 over 8192, of
 // which the keys' 33.6 MB need 4.7.
 #include "attn_core.h"
 #include "layer_ops.h"
@@ -590,7 +590,7 @@ __device__ inline float v_mul_of(const ChunkArgs& a, int kvh) {
 
 // A piece of 32 rows of a tile leaves its sums as a wave holds them, dims 8 g + 4 h .. of row r in lane
 // 32 h + r of group g, so that they go to memory and come back 1024 bytes at once (by rows, 8 x 128
-// over 1000 took 88 us), and its maxima (of raw scores) and weights.
+// over 1000 took 88 us for 73 then), and its maxima (of raw scores) and weights.
 __device__ inline int64_t part_of(const ChunkArgs& a, int piece, int rows32, int kvh) {
   return ((int64_t)piece * a.tiles * (a.rows / 32) + rows32) * a.n_kv + kvh;
 }
@@ -634,7 +634,7 @@ __global__ __launch_bounds__(64 * W, D >= 192 ? 1 : 2) void chunk_kernel(ChunkAr
   // Workgroups go to the 8 XCDs in turn: the tiles of a key head, which read the same rows, meet on
   // few of them.  Later tiles of a sequence see more keys and are begun first, and the pieces that
   // most tiles do not need come last (with a tile's pieces side by side 8 x 128 over 1000 took 72
-  // us for 50).
+  // us for 50 then).
   const int kvh = blockIdx.x % (unsigned)a.n_kv, rest = blockIdx.x / (unsigned)a.n_kv;
   const int piece = rest / a.tiles;
   const Seq seqs = seqs_at(a, 0, 0, lane);
@@ -789,7 +789,7 @@ __device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "m
 // A tile of 32 rows: its four waves take 32 keys of each step of 128, bring them in by themselves, without
 // a barrier, and join at the end.  The next keys are asked for as soon as this step's have been read,
 // and so are values, so one buffer of each does and two workgroups fit a unit (1 x 509 of 32 heads,
-// fp16: 17.3 us, 25.4 in tiles of 128 rows).
+// fp16: 15.9 us, 23.7 in tiles of 128 rows).
 constexpr int kFewRows = 32, kFewShift = 7;
 template <class T, bool NARROW, int D>
 __global__ __launch_bounds__(256, 2) void chunk_few_kernel(ChunkArgs a) {
@@ -1140,13 +1140,14 @@ int launch_dim(const ChunkArgs& a, int dim, unsigned blocks, hipStream_t s) {
 }  // namespace
 
 // A tile of up to kWholeSteps steps stays whole: its pieces' way through memory and the second launch take
-// longer than the steps they save (1 x 509 tokens of 32 heads, nine steps: 25 us whole, 36 in
-// two).  Longer ones are cut down to kLeastSteps (1 x 5 over 8192: 24.2 us with six, 21.7 with four,
-// 21.0 with three, of which more join).  The same for tiles of few rows, whose steps are twice as long:
-// 1 x 509 17.1 us whole, 28.4 in two; 1 x 5 20.4 us down to two steps, 21.5 to four.
+// longer than the steps they save (1 x 509 tokens of 32 heads in tiles of 128 rows, eight steps: 23.5
+// us whole, 30.8 in two).  Longer ones are cut down to kLeastSteps (1 x 5 over 8192 in such tiles: 23.9
+// us with six, 20.2 with four, 21.2 with three).  The same for tiles of few rows, whose steps are
+// twice as long: 1 x 509 15.5 us whole, 23.8 in two; 1 x 5 over 8192 18.7 us down to two steps, 22.6
+// to four, 20.0 to one.
 constexpr int kWholeSteps = 12, kLeastSteps = 4, kFewWhole = 6, kFewLeast = 2;
 // Pieces of all tiles, those that a tile does not need included: their workgroups end at once, but 4096
-// took 61 us for 8 x 128 over 1000 where 2048 took 53.
+// took 60 us for 8 x 128 over 1000 where 2048 took 53.
 constexpr int64_t kMostPieces = 2048;
 
 ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
@@ -1162,22 +1163,22 @@ ChunkPlan chunk_plan(const spax_chunk_attention_args* a) {
   if (a->window > 0 && (int64_t)a->window + a->n_tokens < keys)
     keys = (int64_t)a->window + a->n_tokens;
   // Tiles of 32 rows, whose four waves take a step's keys in turn, where larger ones would stay empty (64
-  // users' next token over 8192: 442 us, 567 in tiles of 128; 64 mixed of up to 256 tokens over
-  // 2048, 93 rows a sequence: 63 and 90; 24 mixed, 158 rows: 74 and 72; 8 x 32 over 4096, 128 rows:
-  // 59 and 49) or would not fill the units for long (1 x 509 of 32 heads: 17 and 25; 1 x 300 over 600:
-  // 30 and 42; 1 x 1024: 37 and 43; 4 x 512 over 1024: 107 and 75; 1 x 512 over 16000: 399 and 210).
+  // users' next token over 8192: 368 us, 406 in tiles of 128; 64 mixed of up to 256 tokens over
+  // 2048, 93 rows a sequence: 63 and 89; 24 mixed, 158 rows: 73 and 70; 8 x 32 over 4096, 128 rows:
+  // 61 and 53) or would not fill the units for long (1 x 509 of 32 heads: 16 and 24; 1 x 300 over 600:
+  // 29 and 41; 1 x 1024: 37 and 42; 4 x 512 over 1024: 109 and 77; 1 x 512 over 16000: 260 and 180).
   const int64_t rows = a->n_tokens * group;
   const bool few = c.head_dim < 192 && (rows <= (int64_t)96 * c.n_seqs ||
                                         (keys <= 2048 && rows / rows_of(4) * c.n_kv_heads <= 256));
   // Eight waves that share a step's keys bring half as many in for a row as two workgroups of four, and
-  // have a unit to themselves (1 x 8192 of 16 bits: 657 us, 691 with four; 24 mixed 88 and 106), but
-  // widen 8-bit keys all at the same time (8 x 512 over 15872: 1755 and 1350), and want one
-  // workgroup for each unit (1 x 512, without tiles of 32: 31 and 25).
+  // have a unit to themselves (1 x 8192 of 16 bits: 630 us, 660 with four; 24 mixed 71 and 65), but
+  // widen 8-bit keys all at the same time (8 x 512 over 15872: 1755 and 1350 then), and want one
+  // workgroup for each unit (1 x 512 of 32 key heads, without tiles of 32: 30 and 24).
   const bool wide = !few && c.type != SPAX_E4M3 && c.head_dim < 192 &&
                     tiles(rows_of(8)) * c.n_kv_heads >= 256;
   p.rows = few ? kFewRows : rows_of(wide ? 8 : 4);
-  // as many as run at once (eight waves, with 512 for 256: 4 x 512 over 1024 97 for 75 us; four waves,
-  // with 256 for 512: 8 x 32 over 4096 58 for 49)
+  // as many as run at once (eight waves, with 512 for 256: 4 x 512 over 1024 101 for 79 us; four waves,
+  // with 256 for 512: 8 x 32 over 4096 60 for 57)
   p.shares = wide ? 256 : 512;
   p.tiles = tiles(p.rows);
   p.key_shift = few ? kFewShift : c.head_dim >= 192 ? 5 : 6;
@@ -1219,7 +1220,7 @@ int launch_chunk_attention(const spax_chunk_attention_args* p, void* ws, hipStre
   a.least_steps = plan.least_steps; a.whole_steps = plan.whole_steps; a.key_shift = plan.key_shift; a.shares = plan.shares;
   a.part_o = (float*)ws;
   a.part_ml = (float*)ws + (size_t)plan.blocks * plan.rows * c.head_dim;
-  // (32 pieces of 1 x 5 over 8192: 5.9 us by four waves, 10.8 by one)
+  // (32 pieces of 1 x 5 over 8192: 18.6 us by four waves, 20.5 by one)
   a.join_waves = plan.pieces > 16 ? kJoinWaves : 1;
   a.join_groups = a.join_waves == 1 && plan.tiles * (plan.rows / 32) * c.n_kv_heads * (c.head_dim / 8) > 8192
                       ? 4

@@ -16,8 +16,8 @@
 // before the stores can go.
 //
 // A normed head (x w / sqrt(mean x^2 + eps), or of x less its mean) is summed over its threads by moves
-// between registers, in 32 bits, before it turns: the same bytes, 24.0 us for the same prompts,
-// 3.8 TB/s; what it adds is the chain from a head's values through their sum to its stores.
+// between registers, in 32 bits, before it turns: the same bytes, 25.1 us for the same prompts,
+// 3.7 TB/s; what it adds is the chain from a head's values through their sum to its stores.
 #include "layer_ops.h"
 #include "mask_core.h"
 
@@ -385,7 +385,7 @@ int launch_kv_append(const spax_kv_append_args* p, const spax_head_norm* n, hipS
   // 16 bytes of a 16-bit head at a time where the rotated part divides into such pieces (the
   // prompts of 4099 tokens: 20.0 us with pieces of eight pairs, 20.6 of four, where 40 values are
   // rotated, and 59 of one, where 20 are).  Normed, pieces of four: their weights take half the registers
-  // (24.0 us, 26.1 of eight).
+  // (24.0 us, 26.1 of eight, then).
   const int pairs = !n && p->rot_dim % 16 == 0 ? 8 : p->rot_dim % 8 == 0 ? 4 : 1;
   const int items = pairs > 1 ? a.dim / (2 * pairs) : p->rot_dim / 2 + a.dim - p->rot_dim;
   int lanes = items;

@@ -14,10 +14,10 @@
 // 2^-11 of each weight, which is what an fp16 base loses when it is packed; sums are in fp32.
 //
 // What bounds it (us of calls back to back, the weights in memory).  Many rows: 4096 x 4096 x 22016
-// fp16 752, 982 TFLOP/s (a large library product reaches 1400), int4 803, 920: matrix
+// fp16 766, 964 TFLOP/s (a large library product reaches 1400), int4 809, 913: matrix
 // instructions are under way in 0.52 of the SIMDs' cycles, the rest are LDS reads (6 KB for every eight
 // of them) and the step's barrier; a wave with 128 x 128 sums would read a third less and needs all
-// of its SIMD's registers.  Few rows: 5 x 4096 x 12288 fp16 23.9, of which the first launch takes 20
+// of its SIMD's registers.  Few rows: 5 x 4096 x 12288 fp16 23.7, of which the first launch takes 20
 // (100 MB at 5 TB/s) and the join 4; 61 x 11008 x 4096 int4 21.0, of which 17 and 4: vector
 // instructions, most of them to widen the codes once for every 32 rows, fill half of the cycles.
 #include "act.h"
@@ -428,7 +428,7 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
       const int e = wave * 64 + lane, row = e / 8;
       uint8_t* to = stages + (step & 1) * M::kStage + M::kX + row * (2 * kCols);
       // past the last record, scale and zero 0 (here and not in load, which would wait for them:
-      // 4096 x 4096 x 22016 818 us, 896 there)
+      // 4096 x 4096 x 22016 809 us, 896 there)
       const uint32_t words = step * M::kDepth + w_row[0] < a.k ? sz : 0u;
       const uint32_t s = __builtin_amdgcn_perm(words, words, 0x05040504u);
       const uint32_t z = __builtin_amdgcn_perm(words, words, 0x07060706u);
@@ -481,7 +481,7 @@ __global__ __launch_bounds__((Many<INT4, TT>::kThreads), 2) void gemm_many_kerne
   if constexpr (INT4) {
     // The waves meet before the last products of a step, when it has been read and the next one is laid
     // out, so that these run while the next step's first operands come (4096 x 22016 842 us, 894
-    // when they meet between steps; fp16, which lays nothing out, 787 and 784).  After the last step
+    // when they meet between steps, then; fp16, which lays nothing out, 787 and 784).  After the last step
     // they lay out and read once more what nothing uses.
     wait_loads();
     mask::lds_barrier();
@@ -611,12 +611,12 @@ int launch_many(const GemmArgs& a, unsigned blocks, hipStream_t s) {
 // as many blobs in turn as keep the weights out of the caches: what they choose took 0.8% (fp16) and
 // 0.3% (int4) longer on average than the best tile of all four.  Some of them, us, tiles of 32, 64, 128 and
 // 256 rows:
-//   4096 x 22016 fp16, 5 rows     39.1   49.4   51.3      -
-//   4096 x 22016 fp16, 64 rows    60.7   54.1   55.4      -
-//   4096 x 22016 fp16, 128 rows   96.2   81.9   61.2      -
-//   4096 x 22016 fp16, 512 rows      -  163.9  162.9  123.0
-//   4096 x 22016 int4, 5 rows     24.3   44.1   48.1      -
-//   4096 x 22016 int4, 128 rows   79.9   80.6   61.3      -
+//   4096 x 22016 fp16, 5 rows     39.2   49.8   51.8   61.0
+//   4096 x 22016 fp16, 64 rows    61.1   54.1   56.1   63.8
+//   4096 x 22016 fp16, 128 rows   97.2   82.5   60.5   68.8
+//   4096 x 22016 fp16, 512 rows  241.7  167.4  171.1  127.1
+//   4096 x 22016 int4, 5 rows     29.4   47.1   49.5   62.6
+//   4096 x 22016 int4, 128 rows   80.2   82.2   61.8   70.7
 GemmPlan gemm_plan(const spax_packed_gemm_args* a) {
   const spax_layout& L = *a->layout;
   // a tile's rows, k of a step of the workgroup, its time, fewest steps of a split
