@@ -572,7 +572,8 @@ int spax_kv_append_normed(const spax_kv_append_args* a, const spax_head_norm* no
  *   lse = ln sum_j exp(score_j).
  * lens[s] is taken as clamped to [0, min(max_len, max_pages * page_size)].  Keys on entries
  * that name no page are left out; bytes of rows outside the range never reach the result,
- * whatever they hold.  A sequence with no keys, or whose scores are all -inf, gives zeros and
+ * whatever they hold; a value in the range that is not finite leaves its dim of the result not
+ * finite (NaN, as a rule).  A sequence with no keys, or whose scores are all -inf, gives zeros and
  * lse -inf.  q, out : `type` (SPAX_F16 or SPAX_BF16), the cache's type or the cache E4M3; 16-byte
  * aligned with strides a multiple of 8 elements.  Probabilities enter the product with v as the
  * sum of two `type` values: within 2^-17 of themselves in BF16, and in F16 within 2^-22 of
